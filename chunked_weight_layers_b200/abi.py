@@ -30,6 +30,18 @@ TTT_RULE_MLP_GD = 3
 TTT_F32 = 0
 TTT_BF16 = 1
 
+TTT_NORM_NONE = 0
+TTT_NORM_RMS = 1
+TTT_NORM_L2 = 2
+TTT_ROPE_HALF = 0
+TTT_ROPE_INTERLEAVED = 1
+TTT_ROPE_SCALE_NONE = 0
+TTT_ROPE_SCALE_LINEAR = 1
+TTT_ROPE_SCALE_NTK = 2
+TTT_ROPE_SCALE_YARN = 3
+TTT_ACT_SILU = 0
+TTT_ACT_GELU = 1
+
 TTT_OPT_LINEAR_CHUNK = 1
 TTT_OPT_WAIT_LIMIT_NS = 2
 TTT_OPT_INJECT_STALL = 3
@@ -64,7 +76,52 @@ class ttt_config(ctypes.Structure):
     ]
 
 
+class ttt_strides(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("head", ctypes.c_int64), ("token", ctypes.c_int64)]
+
+
+class ttt_qk_desc(ctypes.Structure):
+    _fields_ = [
+        ("io_dtype", ctypes.c_int32),
+        ("batch", ctypes.c_int32),
+        ("q_heads", ctypes.c_int32),
+        ("k_heads", ctypes.c_int32),
+        ("width", ctypes.c_int32),
+        ("rot", ctypes.c_int32),
+        ("norm", ctypes.c_int32),
+        ("layout", ctypes.c_int32),
+        ("eps", ctypes.c_float),
+        ("magnitude", ctypes.c_float),
+        ("tokens", ctypes.c_int64),
+        ("position0", ctypes.c_int64),
+        ("positions_stride", ctypes.c_int64),
+        ("q", ttt_strides),
+        ("k", ttt_strides),
+        ("q_out", ttt_strides),
+        ("k_out", ttt_strides),
+        ("q_grad", ttt_strides),
+        ("k_grad", ttt_strides),
+    ]
+
+
+class ttt_gated_scan_desc(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int32),
+        ("heads", ctypes.c_int32),
+        ("tokens", ctypes.c_int64),
+        ("scale", ctypes.c_float),
+        ("q", ttt_strides),
+        ("k", ttt_strides),
+        ("v", ttt_strides),
+        ("o", ttt_strides),
+        ("g", ttt_strides),
+    ]
+
+
 _vp = ctypes.c_void_p
+_sz = ctypes.c_size_t
+_i32 = ctypes.c_int32
+_i64 = ctypes.c_int64
 _st = ctypes.c_int
 _SIGNATURES = {
     "ttt_abi_version": (ctypes.c_int32, []),
@@ -90,6 +147,19 @@ _SIGNATURES = {
     "ttt_last_error_string": (ctypes.c_char_p, []),
     "ttt_target_values_noalloc": (_st, [_vp, _vp, _vp, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32,
                                         ctypes.c_int32, ctypes.c_int32, _vp, _vp, _vp]),
+    "ttt_qk_norm_rope": (_st, [_vp] * 10),
+    "ttt_qk_norm_rope_workspace": (_sz, [_vp]),
+    "ttt_qk_norm_rope_backward": (_st, [_vp] * 14 + [_sz, _vp]),
+    "ttt_rope_frequencies": (_st, [_i32, ctypes.c_double, _i32, ctypes.c_double, ctypes.c_double, ctypes.c_double,
+                                   ctypes.c_double, _vp, _vp]),
+    "ttt_gated_scan": (_st, [_vp] * 9 + [_sz, _vp]),
+    "ttt_gated_scan_workspace": (_sz, [_vp]),
+    "ttt_gated_scan_backward": (_st, [_vp] * 14 + [_sz, _vp]),
+    "ttt_gated_scan_backward_workspace": (_sz, [_vp]),
+    "ttt_gated_scan_step": (_st, [_vp] * 8),
+    "ttt_gated_ffn": (_st, [_vp, _vp, _vp, _i64, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp]),
+    "ttt_gated_ffn_backward": (_st, [_vp] * 6 + [_i64, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _sz, _vp, _vp]),
+    "ttt_gated_ffn_backward_workspace": (_sz, [_i64, _i32, _i32]),
 }
 
 _lib = None

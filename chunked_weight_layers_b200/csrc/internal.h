@@ -231,6 +231,31 @@ ttt_status gate_route(ttt_state* st, const float* loss, int64_t T, cudaStream_t 
 // Nearest rank ceil(gate_pct·64) of the gate's percentile (1-based).
 int gate_rank(const ttt_config& c);
 
+// ---- operators around the scans (stateless; arguments checked by their C entry points) --------
+
+ttt_status qk_norm_rope(const ttt_qk_desc* d, const void* q, const void* k, const float* qw, const float* kw,
+                        const int64_t* positions, const double* freqs, void* qo, void* ko, int num_sms, cudaStream_t s);
+ttt_status qk_norm_rope_backward(const ttt_qk_desc* d, const void* dqo, const void* dko, const void* q, const void* k,
+                                 const float* qw, const float* kw, const int64_t* positions, const double* freqs, void* dq,
+                                 void* dk, float* dqw, float* dkw, void* ws, int num_sms, cudaStream_t s);
+size_t qk_norm_rope_workspace(const ttt_qk_desc* d, int num_sms);
+
+ttt_status gated_scan(const ttt_gated_scan_desc* d, const void* q, const void* k, const void* v, const float* g,
+                      const float* S0, void* o, float* S_end, void* ws, int num_sms, cudaStream_t s);
+ttt_status gated_scan_backward(const ttt_gated_scan_desc* d, const void* dout, const void* q, const void* k,
+                               const void* v, const float* g, const float* S0, const float* dS_end, void* dq, void* dk,
+                               void* dv, float* dg, float* dS0, void* ws, int num_sms, cudaStream_t s);
+ttt_status gated_scan_step(const ttt_gated_scan_desc* d, const void* q, const void* k, const void* v, const float* g,
+                           float* state, void* o, cudaStream_t s);
+size_t gated_scan_workspace(const ttt_gated_scan_desc* d, bool backward, int num_sms);
+
+ttt_status gated_ffn(const void* X, const void* Wg, const void* Wu, int64_t T, int d, int f, int act, void* Z, void* G, void* U,
+                     int32_t* status, int num_sms, cudaStream_t s);
+ttt_status gated_ffn_backward(const void* dZ, const void* X, const void* Wg, const void* Wu, const void* G, const void* U,
+                              int64_t T, int d, int f, int act, void* dX, void* dWg, void* dWu, void* ws, int32_t* status,
+                              int num_sms, cudaStream_t s);
+size_t gated_ffn_backward_workspace(int64_t T, int d, int f, int num_sms);
+
 // Small utility kernels.
 ttt_status f32_to_bf16(const float* src, __nv_bfloat16* dst, size_t n, cudaStream_t s,
                        ttt_state* st);

@@ -67,6 +67,7 @@
 #ifndef TTT_H_
 #define TTT_H_
 
+#include <stddef.h>
 #include <stdint.h>
 
 #ifdef __cplusplus
@@ -411,6 +412,164 @@ int64_t ttt_state_launch_count(const ttt_state* st);
 
 /* Synchronise the device and free everything the state owns. NULL is a no-op. */
 ttt_status ttt_state_destroy(ttt_state* st);
+
+/* ---- operators around the scans -------------------------------------------------------------
+ *
+ * The calls below keep no state: everything they read and write is an argument. They follow the
+ * conventions above (device pointers of the current device, 16-byte aligned, work enqueued on
+ * `stream`, no synchronisation, errors by status) and differ in two points.
+ *  - Tensors with a ttt_strides may lie in any order: element (b, h, t, i) of a [batch, heads,
+ *    tokens, width] tensor is at b·batch + h·head + t·token + i (strides in elements, the last
+ *    dimension dense). Strides are non-negative and, times the element size, multiples of 16
+ *    bytes (those of the gates: any); an input's may be 0 (one row for all), an output's rows
+ *    may not overlap (INVALID_ARG).
+ *  - A call that needs scratch memory takes `workspace` (device, 256-byte aligned) of at least
+ *    the bytes that its *_workspace function returns for the same arguments on the same device
+ *    (0: may be NULL). Two calls whose GPU work may overlap need two workspaces. Its contents do
+ *    not matter before a call and mean nothing after it.
+ * They allocate nothing, so they can be captured into a CUDA graph from the first call on. Unless
+ * a declaration says otherwise, outputs may not overlap inputs or one another. Every row of a call
+ * is read: padding must hold finite numbers, since 0 · NaN is NaN. */
+
+typedef struct {
+  int64_t batch, head, token; /* elements between neighbours in that dimension */
+} ttt_strides;
+
+typedef enum { TTT_NORM_NONE = 0, TTT_NORM_RMS = 1, TTT_NORM_L2 = 2 } ttt_norm;
+typedef enum {
+  TTT_ROPE_HALF = 0,        /* pairs (i, i + rot/2) */
+  TTT_ROPE_INTERLEAVED = 1  /* pairs (2i, 2i + 1) */
+} ttt_rope_layout;
+
+/* Queries and keys of one ttt_qk_norm_rope call. */
+typedef struct {
+  int32_t io_dtype;          /* ttt_dtype of queries, keys and outputs: BF16 or F32 */
+  int32_t batch;
+  int32_t q_heads, k_heads;  /* one of them may be 0: only the other tensor is taken */
+  int32_t width;             /* head width: a multiple of 8, at most 256 */
+  int32_t rot;               /* the first rot values are rotated: a multiple of 16 from 0 to width */
+  int32_t norm;              /* ttt_norm */
+  int32_t layout;            /* ttt_rope_layout */
+  float eps;                 /* under the square root of the norm; >= 0 */
+  float magnitude;           /* factor on every cosine and sine (1; see ttt_rope_frequencies) */
+  int64_t tokens;
+  int64_t position0;         /* without positions: token t of every sequence is at position0 + t */
+  int64_t positions_stride;  /* positions of sequence b start at b·positions_stride (0: shared) */
+  ttt_strides q, k;          /* the inputs */
+  ttt_strides q_out, k_out;  /* the outputs; backward: the gradients of the outputs */
+  ttt_strides q_grad, k_grad; /* backward only: the gradients of the inputs */
+} ttt_qk_desc;
+
+/* Norm of each query and key head and rotary position, in one pass over the data. A row x of
+ * `width` values becomes n = x / sqrt(mean(x²) + eps) (RMS) or x / sqrt(Σx² + eps) (L2) or x
+ * (NONE), times the gain w (RMS; NULL: 1); its first `rot` values are then rotated pair by pair:
+ * (a, b) → magnitude·(a·cos θ − b·sin θ, b·cos θ + a·sin θ), θ = position·freqs[i] for pair i. The
+ * arithmetic is fp32 (the angle is reduced in 64 bits), rounded once at the end.
+ *   q, k            device, io_dtype, [batch, q_heads or k_heads, tokens, width].
+ *   q_weight, k_weight  device fp32 [width], or NULL; NORM_RMS only.
+ *   positions       device int64, or NULL (position0 + t). Any value is allowed, also negative.
+ *   freqs           device, double [rot/2], radians per position (NULL iff rot is 0).
+ *   q_out, k_out    device; may be q and k themselves with the same strides (in place).
+ * q and q_out are NULL iff q_heads is 0; likewise k. batch·tokens = 0 is a no-op. Makes the
+ * queries and keys that the TTT-Linear family and ttt_gated_scan take, straight from a
+ * projection's output. Errors: INVALID_ARG, UNSUPPORTED (dtype, width, rot), CUDA. */
+ttt_status ttt_qk_norm_rope(const ttt_qk_desc* desc, const void* q, const void* k, const float* q_weight,
+                            const float* k_weight, const int64_t* positions, const double* freqs, void* q_out,
+                            void* k_out, ttt_stream stream);
+
+/* Gradients of ttt_qk_norm_rope. dq_out and dk_out (strides q_out, k_out) are the gradients of its
+ * outputs, q, k, the weights, positions and freqs its inputs (q and k may be NULL with NORM_NONE,
+ * which does not need them). Writes dq, dk (strides q_grad, k_grad) and, where not NULL, dq_weight
+ * and dk_weight (fp32 [width], the sums over all rows; NORM_RMS with that weight only; the
+ * same bits every time). With batch·tokens = 0 the weights' gradients are set to 0. */
+ttt_status ttt_qk_norm_rope_backward(const ttt_qk_desc* desc, const void* dq_out, const void* dk_out, const void* q,
+                                     const void* k, const float* q_weight, const float* k_weight,
+                                     const int64_t* positions, const double* freqs, void* dq, void* dk,
+                                     float* dq_weight, float* dk_weight, void* workspace, size_t workspace_bytes,
+                                     ttt_stream stream);
+size_t ttt_qk_norm_rope_workspace(const ttt_qk_desc* desc);
+
+typedef enum {
+  TTT_ROPE_SCALE_NONE = 0,
+  TTT_ROPE_SCALE_LINEAR = 1, /* every frequency divided by factor (positions interpolated) */
+  TTT_ROPE_SCALE_NTK = 2,    /* base times factor^(rot/(rot − 2)): low frequencies stretched most */
+  TTT_ROPE_SCALE_YARN = 3    /* frequencies that turn more than beta_fast times within `trained`
+                                positions kept, those that turn less than beta_slow times divided by
+                                factor, a linear ramp between; magnitude 0.1·ln(factor) + 1 */
+} ttt_rope_scaling;
+
+/* Frequencies base^(−2i/rot) of the rot/2 rotated pairs, scaled for contexts `factor` times the
+ * `trained` length, into freqs (HOST, double [rot/2]) and, where not NULL, *magnitude. Host
+ * arithmetic in 64 bits; touches no device. `trained`, beta_fast and beta_slow are read by YARN
+ * alone. Errors: INVALID_ARG (rot not a positive even number, base <= 1, factor < 1, NTK with
+ * rot 2, YARN with trained <= 0 or not beta_fast > beta_slow > 0, NULL freqs). */
+ttt_status ttt_rope_frequencies(int32_t rot, double base, int32_t scaling, double factor, double trained,
+                                double beta_fast, double beta_slow, double* freqs, float* magnitude);
+
+/* One gated scan: [batch, heads, tokens, 64] bf16 rows and [batch, heads, tokens] fp32 gates. */
+typedef struct {
+  int32_t batch, heads;
+  int64_t tokens;
+  float scale;               /* factor on the outputs, e.g. 1/√64 */
+  ttt_strides q, k, v;
+  ttt_strides o;             /* the outputs; backward: their gradients */
+  ttt_strides g;             /* gates: strides need no alignment */
+} ttt_gated_scan_desc;
+
+/* The fast weight with a forget gate: per (sequence, head), S_t = e^{g_t}·S_{t−1} + k_tᵀ·v_t and
+ * o_t = scale·q_t·S_t, from S0 (device fp32 [batch, heads, 64, 64], or NULL: zero). It is the
+ * In-Place rule's Hebbian update on a 64 x 64 per-head state, with a gate per token and a step per
+ * token. Gates are natural logarithms, usually <= 0; −inf (as any gate below −104, whose factor is 0 in
+ * fp32) forgets everything before its token: documents laid end to end start with such a gate.
+ * Writes o (device bf16) and, where not NULL, S_end (device fp32 like S0: the state after the last
+ * token; may be S0 itself). tokens = 0 writes S_end = S0 (or 0) and nothing else. States and sums
+ * are fp32; one factor of each product is rounded to bf16, but those that make S_end keep 16 bits
+ * or more. Errors: INVALID_ARG, UNSUPPORTED (batch·heads above 2^24), CUDA. */
+ttt_status ttt_gated_scan(const ttt_gated_scan_desc* desc, const void* q, const void* k, const void* v,
+                          const float* g, const float* S0, void* o, float* S_end, void* workspace,
+                          size_t workspace_bytes, ttt_stream stream);
+size_t ttt_gated_scan_workspace(const ttt_gated_scan_desc* desc);
+
+/* Gradients of ttt_gated_scan. d_o (strides o) is the gradient of its outputs, dS_end (device fp32
+ * [batch, heads, 64, 64], or NULL: zero) that of S_end. Writes dq, dk, dv (device, dense bf16
+ * [batch, heads, tokens, 64]), dg (device, dense fp32 [batch, heads, tokens]; 0 where the gate's
+ * factor is 0 in fp32) and, where not NULL, dS0 (fp32 like S0; may be dS_end itself). The gradients of an input with a
+ * stride of 0 are those of its separate rows: the caller adds them up. The states before every
+ * chunk of 64 tokens are made again, in the workspace (256 bytes per token, sequence and head). */
+ttt_status ttt_gated_scan_backward(const ttt_gated_scan_desc* desc, const void* d_o, const void* q, const void* k,
+                                   const void* v, const float* g, const float* S0, const float* dS_end, void* dq,
+                                   void* dk, void* dv, float* dg, float* dS0, void* workspace,
+                                   size_t workspace_bytes, ttt_stream stream);
+size_t ttt_gated_scan_backward_workspace(const ttt_gated_scan_desc* desc);
+
+/* One token of every sequence and head: S ← e^g·S + kᵀ·v in place (device fp32 [batch, heads, 64,
+ * 64]) and o = scale·q·S, all in fp32. desc as above with tokens = 1 (token strides are not read). */
+ttt_status ttt_gated_scan_step(const ttt_gated_scan_desc* desc, const void* q, const void* k, const void* v,
+                               const float* g, float* S, void* o, ttt_stream stream);
+
+typedef enum { TTT_ACT_SILU = 0, TTT_ACT_GELU = 1 } ttt_activation; /* x·σ(x); x·Φ(x) */
+
+/* Gated feed-forward block: Z = act(G) ⊙ U with G = X·Wgᵀ and U = X·Wuᵀ, in one kernel. Z is what
+ * the In-Place scan takes as its keys (the input of the block's Wdown).
+ *   X   device bf16 [T, d];  Wg, Wu  device bf16 [f, d];  Z  device bf16 [T, f].
+ *   G, U  device bf16 [T, f], or both NULL: the pre-activations, kept for the backward pass (Z is
+ *       made from them before they are rounded).
+ *   status  device int32 or NULL, as for ttt_target_values_noalloc: set to 0, then to
+ *       TTT_ERR_TIMEOUT if a bounded device-side wait ran out (the outputs are then incomplete).
+ * d and f are multiples of 8 up to 2^20, T from 0 (a no-op) to 2^24. Errors: INVALID_ARG,
+ * UNSUPPORTED (d, f, T), CUDA. */
+ttt_status ttt_gated_ffn(const void* X, const void* Wg, const void* Wu, int64_t T, int32_t d, int32_t f, int32_t act,
+                         void* Z, void* G, void* U, int32_t* status, ttt_stream stream);
+
+/* Gradients of ttt_gated_ffn from dZ and the kept G and U: with dG = dZ ⊙ U ⊙ act'(G) and dU = dZ ⊙
+ * act(G), each rounded to bf16 once, writes dX = dG·Wg + dU·Wu (bf16 [T, d], or NULL: not wanted),
+ * dWg = dGᵀ·X and dWu = dUᵀ·X (bf16 [f, d], or both NULL). With T = 0 the weights' gradients are set
+ * to 0. */
+ttt_status ttt_gated_ffn_backward(const void* dZ, const void* X, const void* Wg, const void* Wu, const void* G,
+                                  const void* U, int64_t T, int32_t d, int32_t f, int32_t act, void* dX, void* dWg,
+                                  void* dWu, void* workspace, size_t workspace_bytes, int32_t* status,
+                                  ttt_stream stream);
+size_t ttt_gated_ffn_backward_workspace(int64_t T, int32_t d, int32_t f);
 
 /* Message of the last error returned on the calling thread ("" if none). */
 const char* ttt_last_error_string(void);
