@@ -47,36 +47,106 @@ struct QkArgs {
   float* partial;  // backward: [CTAs][2][width]
 };
 
-template <class T>
-__device__ __forceinline__ void load8(const T* p, float (&v)[8]);
-template <>
-__device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* p, float (&v)[8]) {
-  const uint4 x = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]));
-    v[2 * i] = f.x;
-    v[2 * i + 1] = f.y;
-  }
+// Two fp32 values in one 64-bit register: sm_100a multiplies and adds them in one instruction,
+// each rounded as alone. The kernels were bound by instruction issue (185 a row and warp with
+// scalar arithmetic, 34 us where the bytes need 16), so all of a row's arithmetic is in pairs.
+struct F2 {
+  unsigned long long v;
+};
+__device__ __forceinline__ F2 f2(float x, float y) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(x), "f"(y));
+  return r;
 }
-template <>
-__device__ __forceinline__ void load8<float>(const float* p, float (&v)[8]) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+__device__ __forceinline__ float2 split(F2 a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+  return r;
+}
+__device__ __forceinline__ F2 mul(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
 }
 
+// Eight values of a row as they lie in memory, and as four pairs. partner(): the eight values that
+// are rotated with this lane's: the other lane's, or the same with each pair swapped.
 template <class T>
-__device__ __forceinline__ void store8(T* p, const float (&v)[8]);
+struct Raw;
 template <>
-__device__ __forceinline__ void store8<__nv_bfloat16>(__nv_bfloat16* p, const float (&v)[8]) {
-  *reinterpret_cast<uint4*>(p) =
-      make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
-}
+struct Raw<__nv_bfloat16> {
+  uint32_t w[4];
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    const uint4 a = *reinterpret_cast<const uint4*>(p);
+    w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
+  }
+  __device__ __forceinline__ void zero() { w[0] = w[1] = w[2] = w[3] = 0; }
+  __device__ __forceinline__ void get(F2 (&v)[4]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = f2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+  }
+  template <bool HALF>
+  __device__ __forceinline__ void partner(F2 (&v)[4], bool in, int lane) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t x = HALF ? __shfl_sync(0xffffffffu, w[i], lane) : w[i];
+      x = in ? x : 0u;  // the coefficient there is 0, and 0 times an infinity is NaN
+      const float lo = __uint_as_float(x << 16), hi = __uint_as_float(x & 0xffff0000u);
+      v[i] = HALF ? f2(lo, hi) : f2(hi, lo);
+    }
+  }
+  __device__ __forceinline__ static void store(__nv_bfloat16* p, const F2 (&v)[4]) {
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = split(v[i]);
+      o[i] = pack_bf16(f.x, f.y);
+    }
+    *reinterpret_cast<uint4*>(p) = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+};
 template <>
-__device__ __forceinline__ void store8<float>(float* p, const float (&v)[8]) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+struct Raw<float> {
+  float w[8];
+  __device__ __forceinline__ void load(const float* p) {
+    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+    w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = 0.f;
+  }
+  __device__ __forceinline__ void get(F2 (&v)[4]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = f2(w[2 * i], w[2 * i + 1]);
+  }
+  template <bool HALF>
+  __device__ __forceinline__ void partner(F2 (&v)[4], bool in, int lane) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float x = HALF ? __shfl_sync(0xffffffffu, w[2 * i], lane) : w[2 * i + 1];
+      float y = HALF ? __shfl_sync(0xffffffffu, w[2 * i + 1], lane) : w[2 * i];
+      v[i] = f2(in ? x : 0.f, in ? y : 0.f);
+    }
+  }
+  __device__ __forceinline__ static void store(float* p, const F2 (&v)[4]) {
+    const float2 a = split(v[0]), b = split(v[1]), c = split(v[2]), d = split(v[3]);
+    reinterpret_cast<float4*>(p)[0] = make_float4(a.x, a.y, b.x, b.y);
+    reinterpret_cast<float4*>(p)[1] = make_float4(c.x, c.y, d.x, d.y);
+  }
+};
+
+__device__ __forceinline__ float sum_of_squares(const F2 (&v)[4]) {
+  F2 s = mul(v[0], v[0]);
+#pragma unroll
+  for (int i = 1; i < 4; ++i) s = fma2(v[i], v[i], s);
+  const float2 f = split(s);
+  return f.x + f.y;
 }
 
 // Sum over the group of L lanes.
@@ -87,16 +157,16 @@ __device__ __forceinline__ float group_sum(float x) {
   return x;
 }
 
-// A lane's rotation: half layout, cosine and sine of its eight values; interleaved, of its four
-// pairs. Lanes past the rotated part hold the identity.
+// A lane's rotation: its value i becomes own[i]·value + other[i]·partner. Lanes past the rotated part
+// hold own = 1 and other = 0.
 struct Turn {
-  float c[8], s[8];
-  bool in;      // whether this lane's values are rotated
+  F2 own[4], other[4];
+  bool in;
   int partner;  // half layout: the lane of the other values of the pairs
-  float sign;   // half layout: −1 in the lanes of the pairs' first values, +1 in the others
 };
 
-template <bool HALF>
+// BACK: turned back (the sines' sign).
+template <bool HALF, bool BACK>
 __device__ __forceinline__ Turn make_turn(const QkArgs& a, int64_t pos, int lane_in, int lane) {
   Turn t;
   const int lanes_rot = a.rot / 8, half = a.rot / 16;
@@ -104,41 +174,45 @@ __device__ __forceinline__ Turn make_turn(const QkArgs& a, int64_t pos, int lane
   const bool first = lane_in < half;
   t.in = in;
   t.partner = HALF && in ? lane + (first ? half : -half) : lane;
-  t.sign = first ? -1.f : 1.f;
+  // Half layout: both lanes of a pair of lanes need the same eight angles; each makes four of them.
+  const int at = HALF ? 8 * (first ? lane_in : lane_in - half) + (first ? 0 : 4) : 4 * lane_in;
+  float c[4], s[4];
 #pragma unroll
-  for (int i = 0; i < (HALF ? 8 : 4); ++i) {
-    t.c[i] = 1.f;
-    t.s[i] = 0.f;
+  for (int i = 0; i < 4; ++i) {
+    c[i] = 1.f;
+    s[i] = 0.f;
     if (in) {
-      const int at = HALF ? 8 * (first ? lane_in : lane_in - half) + i : 4 * lane_in + i;
-      double turns = (double)pos * (a.freqs[at] * 0.15915494309189533577);
+      double turns = (double)pos * (a.freqs[at + i] * 0.15915494309189533577);
       turns -= rint(turns);
-      float sn, cs;
-      sincospif(2.f * (float)turns, &sn, &cs);
-      t.c[i] = cs * a.magnitude;
-      t.s[i] = sn * a.magnitude;
+      sincospif(2.f * (float)turns, &s[i], &c[i]);
+      c[i] *= a.magnitude;
+      s[i] *= BACK ? -a.magnitude : a.magnitude;
+    }
+  }
+  if constexpr (HALF) {
+    const float sign = first ? -1.f : 1.f;
+    float cc[8], ss[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float co = __shfl_sync(0xffffffffu, c[i], t.partner), so = __shfl_sync(0xffffffffu, s[i], t.partner);
+      cc[i] = first ? c[i] : co;
+      ss[i] = sign * (first ? s[i] : so);
+      cc[i + 4] = first ? co : c[i];
+      ss[i + 4] = sign * (first ? so : s[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      t.own[i] = f2(cc[2 * i], cc[2 * i + 1]);
+      t.other[i] = f2(ss[2 * i], ss[2 * i + 1]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      t.own[i] = f2(c[i], c[i]);
+      t.other[i] = f2(-s[i], s[i]);
     }
   }
   return t;
-}
-
-// Rotates a lane's eight values; BACK turns the rotation back. Every lane of the warp takes part.
-template <bool HALF, bool BACK>
-__device__ __forceinline__ void rotate(float (&v)[8], const Turn& t) {
-  if constexpr (HALF) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float other = __shfl_sync(0xffffffffu, v[i], t.partner);
-      if (t.in) v[i] = fmaf(v[i], t.c[i], other * (BACK ? -t.sign : t.sign) * t.s[i]);
-    }
-  } else if (t.in) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float x = v[2 * i], y = v[2 * i + 1], s = BACK ? -t.s[i] : t.s[i];
-      v[2 * i] = fmaf(x, t.c[i], -(y * s));
-      v[2 * i + 1] = fmaf(y, t.c[i], x * s);
-    }
-  }
 }
 
 // The group's token and its part of the heads.
@@ -159,108 +233,193 @@ struct Item {
   }
 };
 
-// grid: items / groups per CTA.
+// A group walks over its part of the heads in batches of one side, with the loads of a batch in
+// flight at once: four heads forward, four (of two rows each) backward. The first batch is on its way
+// while the angles are made.
+constexpr int kFly = 4, kFlyBack = 4;
+
+// One side's heads of the item, and the batches that the longest walk in the warp takes (all lanes
+// take part in the shuffles).
+template <int FLY>
+struct Walk {
+  int h0, h1, n;
+  template <int L>
+  __device__ __forceinline__ Walk(const QkArgs& a, const Item<L>& it, int sd) {
+    const int base = sd ? a.side[0].heads : 0;
+    h0 = max(it.h0 - base, 0);
+    h1 = min(it.h1 - base, a.side[sd].heads);
+    n = __reduce_max_sync(0xffffffffu, max(0, h1 - h0 + FLY - 1) / FLY);
+  }
+};
+
+// The gains of a lane's eight values (1 without).
+__device__ __forceinline__ void load_gain(const QkSide& S, bool live, int lane_in, Raw<float>& w) {
+  if (S.w != nullptr && live) {
+    w.load(S.w + 8 * lane_in);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w.w[j] = 1.f;
+  }
+}
+
+// grid: items / groups per CTA. y = r·(own·w·x + other·w'·x'), x' and w' the partner's.
 template <class T, int L, bool HALF>
-__global__ void __launch_bounds__(kThreadsQK) k_qk_norm_rope(const QkArgs a) {
+__global__ void __launch_bounds__(kThreadsQK, 4) k_qk_norm_rope(const QkArgs a) {
   const int lane = threadIdx.x & 31, lane_in = threadIdx.x % L;
   const Item<L> it(a, (int64_t)blockIdx.x * (kThreadsQK / L) + threadIdx.x / L);
-  const int64_t pos = !it.valid ? 0 : a.positions != nullptr ? a.positions[it.b * a.positions_stride + it.t] : a.position0 + it.t;
-  const Turn turn = make_turn<HALF>(a, pos, lane_in, lane);
   const bool live = it.valid && 8 * lane_in < a.width;
   const float inv = a.norm == TTT_NORM_RMS ? 1.f / a.width : 1.f;
-  float w[8];
-  int wside = -1;
-  // The trip count is the same for every group of the warp: all its lanes take part in the shuffles.
-  for (int i = 0; i < a.heads_per; ++i) {
-    const int h = it.h0 + i;
-    const bool ok = live && h < it.h1;
-    const int sd = h >= a.side[0].heads ? 1 : 0;
+  const int64_t pos = !it.valid ? 0 : a.positions != nullptr ? a.positions[it.b * a.positions_stride + it.t] : a.position0 + it.t;
+  Turn turn;
+  bool made = false;
+#pragma unroll 1
+  for (int sd = 0; sd < 2; ++sd) {
+    const Walk<kFly> wk(a, it, sd);
+    if (wk.n == 0) continue;
     const QkSide& S = a.side[sd];
-    const int64_t hh = h - (sd ? a.side[0].heads : 0);
-    float v[8];
-    if (ok) {
-      load8<T>(static_cast<const T*>(S.x) + it.b * S.xb + hh * S.xh + it.t * S.xt + 8 * lane_in, v);
-    } else {
+    const T* x = static_cast<const T*>(S.x) + it.b * S.xb + it.t * S.xt + 8 * lane_in + wk.h0 * S.xh;
+    T* y = static_cast<T*>(S.y) + it.b * S.yb + it.t * S.yt + 8 * lane_in + wk.h0 * S.yh;
+    int left = live ? wk.h1 - wk.h0 : 0;
+    Raw<T> raw[kFly];
+    auto fetch = [&](int n) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = 0.f;
+      for (int u = 0; u < kFly; ++u) {
+        if (u < n)
+          raw[u].load(x + u * S.xh);
+        else
+          raw[u].zero();
+      }
+      x += kFly * S.xh;
+    };
+    fetch(left);
+    if (!made) {
+      turn = make_turn<HALF, false>(a, pos, lane_in, lane);
+      made = true;
     }
-    if (a.norm != TTT_NORM_NONE) {
-      float ss = 0.f;
+    F2 A[4], B[4];
+    {
+      Raw<float> w;
+      F2 own[4], other[4];
+      load_gain(S, live, lane_in, w);
+      w.get(own);
+      w.template partner<HALF>(other, true, turn.partner);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) ss = fmaf(v[j], v[j], ss);
-      const float r = rsqrtf(fmaf(group_sum<L>(ss), inv, a.eps));
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] *= r;
-      if (S.w != nullptr && ok) {
-        if (wside != sd) {
-          load8<float>(S.w + 8 * lane_in, w);
-          wside = sd;
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] *= w[j];
+      for (int i = 0; i < 4; ++i) {
+        A[i] = mul(turn.own[i], own[i]);
+        B[i] = mul(turn.other[i], other[i]);
       }
     }
-    rotate<HALF, false>(v, turn);
-    if (ok) store8<T>(static_cast<T*>(S.y) + it.b * S.yb + hh * S.yh + it.t * S.yt + 8 * lane_in, v);
+#pragma unroll 1
+    for (int b = 0; b < wk.n; ++b) {
+      F2 v[kFly][4];
+#pragma unroll
+      for (int u = 0; u < kFly; ++u) {
+        F2 p[4], q[4];
+        raw[u].get(p);
+        raw[u].template partner<HALF>(q, turn.in, turn.partner);
+        float r = 1.f;
+        if (a.norm != TTT_NORM_NONE) r = rsqrtf(fmaf(group_sum<L>(sum_of_squares(p)), inv, a.eps));
+        const F2 rr = f2(r, r);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[u][i] = mul(rr, fma2(q[i], B[i], mul(p[i], A[i])));
+        if (u < left) Raw<T>::store(y + u * S.yh, v[u]);
+      }
+      y += kFly * S.yh;
+      left -= kFly;
+      if (b + 1 < wk.n) fetch(left);
+    }
   }
 }
 
 // The gradients of the inputs, and the gains' gradients summed over what the CTA takes. Grid-stride
 // over the items.
 template <class T, int L, bool HALF>
-__global__ void __launch_bounds__(kThreadsQK) k_qk_norm_rope_bwd(const QkArgs a) {
+__global__ void __launch_bounds__(kThreadsQK, 2) k_qk_norm_rope_bwd(const QkArgs a) {
   constexpr int kGroups = kThreadsQK / L;
   __shared__ float part[kGroups][8 * L];
   const int lane = threadIdx.x & 31, lane_in = threadIdx.x % L, group = threadIdx.x / L;
   const float inv = a.norm == TTT_NORM_RMS ? 1.f / a.width : 1.f;
-  float dw[2][8] = {};
+  F2 dw[2][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) dw[0][i] = dw[1][i] = f2(0.f, 0.f);
   const int64_t step = (int64_t)gridDim.x * kGroups;
-  for (int64_t base = (int64_t)blockIdx.x * kGroups; base < a.items; base += step) {
-    const Item<L> it(a, base + group);
-    const int64_t pos = !it.valid ? 0 : a.positions != nullptr ? a.positions[it.b * a.positions_stride + it.t] : a.position0 + it.t;
-    const Turn turn = make_turn<HALF>(a, pos, lane_in, lane);
+  for (int64_t at = (int64_t)blockIdx.x * kGroups; at < a.items; at += step) {
+    const Item<L> it(a, at + group);
     const bool live = it.valid && 8 * lane_in < a.width;
-    for (int i = 0; i < a.heads_per; ++i) {
-      const int h = it.h0 + i;
-      const bool ok = live && h < it.h1;
-      const int sd = h >= a.side[0].heads ? 1 : 0;
+    const int64_t pos = !it.valid ? 0 : a.positions != nullptr ? a.positions[it.b * a.positions_stride + it.t] : a.position0 + it.t;
+    Turn turn;
+    bool made = false;
+#pragma unroll
+    for (int sd = 0; sd < 2; ++sd) {
+      const Walk<kFlyBack> wk(a, it, sd);
+      if (wk.n == 0) continue;
       const QkSide& S = a.side[sd];
-      const int64_t hh = h - (sd ? a.side[0].heads : 0);
-      float e[8], n[8];
+      const T* x = static_cast<const T*>(S.x) + it.b * S.xb + it.t * S.xt + 8 * lane_in + wk.h0 * S.xh;
+      const T* g = static_cast<const T*>(S.dy) + it.b * S.gb + it.t * S.gt + 8 * lane_in + wk.h0 * S.gh;
+      T* y = static_cast<T*>(S.y) + it.b * S.yb + it.t * S.yt + 8 * lane_in + wk.h0 * S.yh;
+      int left = live ? wk.h1 - wk.h0 : 0;
+      Raw<T> gr[kFlyBack], xr[kFlyBack];
+      auto fetch = [&](int n) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) e[j] = n[j] = 0.f;
-      if (ok) {
-        load8<T>(static_cast<const T*>(S.dy) + it.b * S.gb + hh * S.gh + it.t * S.gt + 8 * lane_in, e);
-        if (a.norm != TTT_NORM_NONE)
-          load8<T>(static_cast<const T*>(S.x) + it.b * S.xb + hh * S.xh + it.t * S.xt + 8 * lane_in, n);
-      }
-      rotate<HALF, true>(e, turn);
-      if (a.norm != TTT_NORM_NONE) {
-        float ss = 0.f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) ss = fmaf(n[j], n[j], ss);
-        const float r = rsqrtf(fmaf(group_sum<L>(ss), inv, a.eps));
-#pragma unroll
-        for (int j = 0; j < 8; ++j) n[j] *= r;
-        if (S.w != nullptr && ok) {
-          float w[8];
-          load8<float>(S.w + 8 * lane_in, w);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float d = e[j] * n[j];
-            dw[0][j] += sd ? 0.f : d;
-            dw[1][j] += sd ? d : 0.f;
-            e[j] *= w[j];
-          }
+        for (int u = 0; u < kFlyBack; ++u) {
+          if (u < n)
+            gr[u].load(g + u * S.gh);
+          else
+            gr[u].zero();
+          if (u < n && a.norm != TTT_NORM_NONE)
+            xr[u].load(x + u * S.xh);
+          else
+            xr[u].zero();
         }
-        float dot = 0.f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) dot = fmaf(e[j], n[j], dot);
-        dot = group_sum<L>(dot) * inv;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) e[j] = r * fmaf(-dot, n[j], e[j]);
+        g += kFlyBack * S.gh;
+        x += kFlyBack * S.xh;
+      };
+      fetch(left);
+      if (!made) {
+        turn = make_turn<HALF, true>(a, pos, lane_in, lane);
+        made = true;
       }
-      if (ok) store8<T>(static_cast<T*>(S.y) + it.b * S.yb + hh * S.yh + it.t * S.yt + 8 * lane_in, e);
+      F2 w[4];
+      {
+        Raw<float> wr;
+        load_gain(S, live, lane_in, wr);
+        wr.get(w);
+      }
+#pragma unroll 1
+      for (int b = 0; b < wk.n; ++b) {
+#pragma unroll
+        for (int u = 0; u < kFlyBack; ++u) {
+          F2 e[4], o[4];
+          gr[u].get(e);
+          gr[u].template partner<HALF>(o, turn.in, turn.partner);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) e[i] = fma2(o[i], turn.other[i], mul(e[i], turn.own[i]));
+          if (a.norm != TTT_NORM_NONE) {
+            F2 n[4];
+            xr[u].get(n);
+            const float size = fmaf(group_sum<L>(sum_of_squares(n)), inv, a.eps);
+            const float r = u < left ? rsqrtf(size) : 0.f;  // a slot past the heads adds nothing
+            const F2 rr = f2(r, r);
+            F2 d = f2(0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              n[i] = mul(n[i], rr);
+              dw[sd][i] = fma2(e[i], n[i], dw[sd][i]);
+              e[i] = mul(e[i], w[i]);
+              d = fma2(e[i], n[i], d);
+            }
+            const float2 ds = split(d);
+            const float dot = -group_sum<L>(ds.x + ds.y) * inv;
+            const F2 dd = f2(dot, dot);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) e[i] = mul(rr, fma2(dd, n[i], e[i]));
+          }
+          if (u < left) Raw<T>::store(y + u * S.yh, e);
+        }
+        y += kFlyBack * S.yh;
+        left -= kFlyBack;
+        if (b + 1 < wk.n) fetch(left);
+      }
     }
   }
   if (a.partial == nullptr) return;
@@ -268,7 +427,11 @@ __global__ void __launch_bounds__(kThreadsQK) k_qk_norm_rope_bwd(const QkArgs a)
   for (int sd = 0; sd < 2; ++sd) {
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < 8; ++j) part[group][8 * lane_in + j] = dw[sd][j];
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = split(dw[sd][i]);
+      part[group][8 * lane_in + 2 * i] = f.x;
+      part[group][8 * lane_in + 2 * i + 1] = f.y;
+    }
     __syncthreads();
     for (int j = threadIdx.x; j < a.width; j += kThreadsQK) {
       float s = 0.f;
@@ -279,16 +442,19 @@ __global__ void __launch_bounds__(kThreadsQK) k_qk_norm_rope_bwd(const QkArgs a)
   }
 }
 
-// Sums over the CTAs: one warp per value, grid (width, 2).
-__global__ void __launch_bounds__(32) k_qk_gain_sum(const float* __restrict__ partial, int n, int width, float* dwq, float* dwk) {
+// Sums over the CTAs: one CTA of 128 threads per value, grid (width, 2).
+__global__ void __launch_bounds__(128) k_qk_gain_sum(const float* __restrict__ partial, int n, int width, float* dwq, float* dwk) {
   const int j = blockIdx.x, sd = blockIdx.y;
   float* out = sd ? dwk : dwq;
   if (out == nullptr) return;
+  __shared__ double warp_sum[4];
   double s = 0.0;
-  for (int i = threadIdx.x; i < n; i += 32) s += (double)partial[((size_t)i * 2 + sd) * width + j];
+  for (int i = threadIdx.x; i < n; i += 128) s += (double)partial[((size_t)i * 2 + sd) * width + j];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  if (threadIdx.x == 0) out[j] = (float)s;
+  if ((threadIdx.x & 31) == 0) warp_sum[threadIdx.x >> 5] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) out[j] = (float)((warp_sum[0] + warp_sum[1]) + (warp_sum[2] + warp_sum[3]));
 }
 
 template <class T, int L, bool HALF>
@@ -322,13 +488,17 @@ int lanes_of(int width) { return width <= 64 ? 8 : width <= 128 ? 16 : 32; }
 int64_t groups_per_block(int width) { return kThreadsQK / lanes_of(width); }
 
 // Parts of a token's heads: one, unless the tokens alone give the GPU fewer than 512 threads an SM.
-int splits_of(const ttt_qk_desc* d, int num_sms) {
+// Backward, two where there are 16 heads or more: its CTAs walk over several items each, and
+// smaller ones end closer together (4 x 8192 tokens of 32 heads: 83 us against 89; three: 102, as
+// the parts no longer end where the queries do, four: 90).
+int splits_of(const ttt_qk_desc* d, bool back, int num_sms) {
   const int64_t rows = (int64_t)d->batch * d->tokens, heads = (int64_t)d->q_heads + d->k_heads;
   const int64_t want = (int64_t)num_sms * 512 / lanes_of(d->width);
-  return (int)std::max<int64_t>(1, std::min(heads, want / std::max<int64_t>(1, rows)));
+  return (int)std::max<int64_t>(back && heads >= 16 ? 2 : 1, std::min(heads, want / std::max<int64_t>(1, rows)));
 }
 
-constexpr int kBwdCtasPerSm = 4;
+// Resident CTAs of the backward kernel (its registers allow two).
+constexpr int kBwdCtasPerSm = 2;
 
 int64_t bwd_blocks(int64_t items, int width, int num_sms) {
   const int64_t g = groups_per_block(width);
@@ -340,7 +510,7 @@ QkSide side_of(const void* x, const ttt_strides& xs, const void* dy, const ttt_s
   return QkSide{x, dy, y, xs.batch, xs.head, xs.token, ys.batch, ys.head, ys.token, gs.batch, gs.head, gs.token, w, heads};
 }
 
-QkArgs args_of(const ttt_qk_desc* d, const int64_t* positions, const double* freqs, int num_sms) {
+QkArgs args_of(const ttt_qk_desc* d, bool back, const int64_t* positions, const double* freqs, int num_sms) {
   QkArgs a = {};
   a.width = d->width;
   a.rot = d->rot;
@@ -349,7 +519,8 @@ QkArgs args_of(const ttt_qk_desc* d, const int64_t* positions, const double* fre
   a.magnitude = d->magnitude;
   a.tokens = d->tokens;
   const int heads = d->q_heads + d->k_heads;
-  a.heads_per = (heads + splits_of(d, num_sms) - 1) / splits_of(d, num_sms);
+  const int splits = splits_of(d, back, num_sms);
+  a.heads_per = (heads + splits - 1) / splits;
   a.splits = (heads + a.heads_per - 1) / a.heads_per;
   a.items = (int64_t)d->batch * d->tokens * a.splits;
   a.positions = positions;
@@ -375,7 +546,7 @@ size_t qk_norm_rope_workspace(const ttt_qk_desc* d, int num_sms) {
 
 ttt_status qk_norm_rope(const ttt_qk_desc* d, const void* q, const void* k, const float* qw, const float* kw,
                         const int64_t* positions, const double* freqs, void* qo, void* ko, int num_sms, cudaStream_t s) {
-  QkArgs a = args_of(d, positions, freqs, num_sms);
+  QkArgs a = args_of(d, false, positions, freqs, num_sms);
   a.side[0] = side_of(q, d->q, nullptr, d->q, qo, d->q_out, qw, d->q_heads);
   a.side[1] = side_of(k, d->k, nullptr, d->k, ko, d->k_out, kw, d->k_heads);
   const int64_t g = groups_per_block(d->width), blocks = (a.items + g - 1) / g;
@@ -388,7 +559,7 @@ ttt_status qk_norm_rope(const ttt_qk_desc* d, const void* q, const void* k, cons
 ttt_status qk_norm_rope_backward(const ttt_qk_desc* d, const void* dqo, const void* dko, const void* q, const void* k,
                                  const float* qw, const float* kw, const int64_t* positions, const double* freqs, void* dq,
                                  void* dk, float* dqw, float* dkw, void* ws, int num_sms, cudaStream_t s) {
-  QkArgs a = args_of(d, positions, freqs, num_sms);
+  QkArgs a = args_of(d, true, positions, freqs, num_sms);
   a.side[0] = side_of(q, d->q, dqo, d->q_out, dq, d->q_grad, qw, d->q_heads);
   a.side[1] = side_of(k, d->k, dko, d->k_out, dk, d->k_grad, kw, d->k_heads);
   const bool gains = dqw != nullptr || dkw != nullptr;
@@ -397,7 +568,7 @@ ttt_status qk_norm_rope_backward(const ttt_qk_desc* d, const void* dqo, const vo
   run(a, d, true, blocks, s);
   TTT_CUDA(cudaGetLastError());
   if (gains) {
-    k_qk_gain_sum<<<dim3(d->width, 2), 32, 0, s>>>(a.partial, (int)blocks, d->width, dqw, dkw);
+    k_qk_gain_sum<<<dim3(d->width, 2), 128, 0, s>>>(a.partial, (int)blocks, d->width, dqw, dkw);
     TTT_CUDA(cudaGetLastError());
   }
   return TTT_OK;

@@ -16,7 +16,6 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
-from functools import lru_cache
 
 import torch
 
@@ -50,20 +49,22 @@ def _refuse(t, name, want, dev):
 
 
 def _rows(t, name, dtype, shape, dev, last=True):
-    """Address of ``t`` once it has this type, shape and device, and (``last``) a dense last dimension."""
+    """Checks that ``t`` has this type, shape and device, and (``last``) a dense last dimension."""
     if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or t.get_device() != dev
             or (last and t.stride(-1) != 1 and shape[-1] > 1)):
         _refuse(t, name, f"{tuple(shape)} {dtype}" + (" with a dense last dimension" if last else ""), dev)
-    return t.data_ptr()
 
 
 def _dense(t, name, dtype, shape, dev):
-    if t is None:
-        return None
+    """Checks that ``t`` is a contiguous tensor of this type, shape and device."""
     if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or t.get_device() != dev
             or not t.is_contiguous()):
         _refuse(t, name, f"contiguous {tuple(shape)} {dtype}", dev)
-    return t.data_ptr()
+
+
+def _dense_or_none(t, *how):
+    if t is not None:
+        _dense(t, *how)
 
 
 def _strides(shape, stride):
@@ -72,10 +73,38 @@ def _strides(shape, stride):
     return tuple(s if n > 1 else 0 for n, s in zip(shape[:3], stride[:3]))
 
 
+# Checking every tensor of a call and filling its descriptor costs more host time than a small
+# call's kernel takes. What both depend on is the tensors' metadata (shape, strides, type, device) and
+# the options alone, so a call whose metadata has been checked before takes the descriptor and
+# workspace size made then; addresses are read, and their alignment checked, at every call.
+
+
+def _meta(t):
+    return None if t is None else (t.shape, t.stride(), t.dtype, t.get_device())
+
+
+class _Plans(dict):
+    """Checked calls by their metadata; emptied when it has grown past ``most``."""
+
+    most = 1024
+
+    def find(self, key):
+        try:
+            return self.get(key)
+        except TypeError:  # an option that cannot be hashed: the checks will name it
+            return None
+
+    def keep(self, key, plan):
+        if len(self) >= self.most:
+            self.clear()
+        self[key] = plan
+        return plan
+
+
 def _place(stream, dev):
     """The raw stream a call runs on, and a context in which torch allocates on that stream."""
     if stream is None:
-        return (_raw(dev) if _raw is not None else torch.cuda.current_stream().cuda_stream) or None, None
+        return (_raw(dev) if _raw is not None else torch.cuda.current_stream().cuda_stream) or None, _nothing
     return stream.cuda_stream or None, torch.cuda.stream(stream)
 
 
@@ -83,24 +112,19 @@ _nothing = contextlib.nullcontext()
 
 
 def _workspace(nbytes, dev):
-    return torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+    return torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", dev)) if nbytes else None
 
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def _like(t):
+    """A new dense tensor of t's shape and type."""
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
+
+
 # ---- queries and keys ---------------------------------------------------------------------
-
-
-@lru_cache(maxsize=256)
-def _qk_desc(io, batch, hq, hk, width, rot, norm, layout, eps, magnitude, tokens, position0, pos_stride, *strides):
-    d = abi.ttt_qk_desc(io, batch, hq, hk, width, rot, norm, layout, eps, magnitude, tokens, position0, pos_stride,
-                        *(abi.ttt_strides(*s) for s in strides))
-    return d
-
-
-_qk_workspaces = lru_cache(maxsize=256)(lambda dev, *key: abi.load().ttt_qk_norm_rope_workspace(ctypes.byref(_qk_desc(*key))))
 
 
 def rope_frequencies(rot, base=10000.0, scaling="none", factor=1.0, trained=0.0, beta_fast=32.0, beta_slow=1.0):
@@ -115,31 +139,47 @@ def rope_frequencies(rot, base=10000.0, scaling="none", factor=1.0, trained=0.0,
     return torch.tensor(list(out), dtype=_F64, device=torch.device("cuda", _current_device())), magnitude.value
 
 
-def _qk_args(q, k, positions, freqs, q_weight, k_weight, dev):
-    x = q if q is not None else k
+_qk_plans, _qk_back_plans = _Plans(), _Plans()
+
+
+def _qk_call(q, k, positions, freqs, q_weight, k_weight, norm, layout, eps, magnitude, position0, dev):
+    """Checks what the two calls share and returns (descriptor without strides, dtype, q's shape, k's shape);
+    ``q`` and ``k`` stand for the tensors that give the shapes."""
+    x, name = (q, "q") if q is not None else (k, "k")
     if not isinstance(x, torch.Tensor) or x.dim() != 4 or x.dtype not in (_BF16, _F32):
-        _refuse(x, "q" if q is not None else "k", "[batch, heads, tokens, width] torch.bfloat16 or torch.float32", dev)
+        _refuse(x, name, "[batch, heads, tokens, width] torch.bfloat16 or torch.float32", dev)
     batch, _, tokens, width = x.shape
     hq, hk = 0 if q is None else q.shape[1], 0
     if k is not None:
         if not isinstance(k, torch.Tensor) or k.dim() != 4:
             _refuse(k, "k", "[batch, heads, tokens, width]", dev)
         hk = k.shape[1]
-    rot = 0
+    rot, pos_stride = 0, 0
     if freqs is not None:
         if not isinstance(freqs, torch.Tensor) or freqs.dim() != 1:
             _refuse(freqs, "freqs", "[rot/2] torch.float64", dev)
         rot = 2 * freqs.shape[0]
-    pos_stride = 0
+        _dense(freqs, "freqs", _F64, freqs.shape, dev)
     if positions is not None:
         if not isinstance(positions, torch.Tensor) or positions.shape not in ((tokens,), (batch, tokens)):
             _refuse(positions, "positions", f"[{tokens}] or [{batch}, {tokens}] torch.int64", dev)
+        _dense(positions, "positions", _I64, positions.shape, dev)
         if positions.dim() == 2:
             pos_stride = tokens
-    ptrs = (_dense(q_weight, "q_weight", _F32, (width,), dev), _dense(k_weight, "k_weight", _F32, (width,), dev),
-            None if positions is None else _dense(positions, "positions", _I64, positions.shape, dev),
-            None if rot == 0 else _dense(freqs, "freqs", _F64, (rot // 2,), dev))
-    return x.dtype, batch, hq, hk, tokens, width, rot, pos_stride, ptrs
+    _dense_or_none(q_weight, "q_weight", _F32, (width,), dev)
+    _dense_or_none(k_weight, "k_weight", _F32, (width,), dev)
+    d = abi.ttt_qk_desc(1 if x.dtype is _BF16 else 0, batch, hq, hk, width, rot, _choice(NORMS, norm, "norm"),
+                        _choice(LAYOUTS, layout, "layout"), float(eps), float(magnitude), tokens, int(position0), pos_stride)
+    return d, x.dtype, (batch, hq, tokens, width), (batch, hk, tokens, width)
+
+
+def _set(d, field, shape, t):
+    if t is not None:
+        setattr(d, field, abi.ttt_strides(*_strides(shape, t.stride())))
+
+
+def _freqs_ptr(freqs):
+    return freqs.data_ptr() if freqs is not None and freqs.numel() else None
 
 
 def qk_norm_rope(q, k, *, positions=None, freqs=None, magnitude=1.0, norm="rms", eps=1e-6, layout="half",
@@ -153,29 +193,32 @@ def qk_norm_rope(q, k, *, positions=None, freqs=None, magnitude=1.0, norm="rms",
     ``layout`` "half" or "interleaved". ``q_weight``, ``k_weight`` fp32 [width] (RMS). Returns (q, k),
     dense [batch, heads, tokens, width] or the pair ``out`` (which may be the inputs)."""
     dev = _current_device()
-    dtype, batch, hq, hk, tokens, width, rot, pos_stride, ptrs = _qk_args(q, k, positions, freqs, q_weight, k_weight, dev)
     raw, ctx = _place(stream, dev)
-    qs, ks = (batch, hq, tokens, width), (batch, hk, tokens, width)
-    pq = None if q is None else _rows(q, "q", dtype, qs, dev)
-    pk = None if k is None else _rows(k, "k", dtype, ks, dev)
-    if out is None:
-        with ctx or _nothing:
-            qo = None if q is None else torch.empty(qs, dtype=dtype, device=q.device)
-            ko = None if k is None else torch.empty(ks, dtype=dtype, device=k.device)
-    else:
-        qo, ko = out
+    try:
+        key = (dev, _meta(q), _meta(k), _meta(positions), _meta(freqs), _meta(q_weight), _meta(k_weight), norm, layout, eps,
+               magnitude, position0, None if out is None else (_meta(out[0]), _meta(out[1])))
+    except (AttributeError, TypeError, IndexError):  # something that is no tensor: the checks will name it
+        key = None
+    d = _qk_plans.find(key) if key is not None else None
+    if d is None:
+        d, dtype, qs, ks = _qk_call(q, k, positions, freqs, q_weight, k_weight, norm, layout, eps, magnitude, position0, dev)
+        qo, ko = out if out is not None else (q, k)
         if (qo is None) != (q is None) or (ko is None) != (k is None):
             raise ValueError("out: expected a tensor for each of q and k that is given")
-    pqo = None if qo is None else _rows(qo, "out[0]", dtype, qs, dev)
-    pko = None if ko is None else _rows(ko, "out[1]", dtype, ks, dev)
-    sq = (0, 0, 0) if q is None else _strides(qs, q.stride())
-    sk = (0, 0, 0) if k is None else _strides(ks, k.stride())
-    so = (0, 0, 0) if qo is None else _strides(qs, qo.stride())
-    sp = (0, 0, 0) if ko is None else _strides(ks, ko.stride())
-    d = _qk_desc(1 if dtype is _BF16 else 0, batch, hq, hk, width, rot, _choice(NORMS, norm, "norm"),
-                 _choice(LAYOUTS, layout, "layout"), float(eps), float(magnitude), tokens, int(position0),
-                 pos_stride, sq, sk, so, sp, (0, 0, 0), (0, 0, 0))
-    check(abi.load().ttt_qk_norm_rope(ctypes.byref(d), pq, pk, *ptrs, pqo, pko, raw))
+        for x, y, shape, n, i in ((q, qo, qs, "q", 0), (k, ko, ks, "k", 1)):
+            if x is not None:
+                _rows(x, n, dtype, shape, dev)
+                _rows(y, f"out[{i}]", dtype, shape, dev)
+                _set(d, n, shape, x)
+                _set(d, n + "_out", shape, y if out is not None else torch.empty(shape, device="meta"))
+        if key is not None:
+            _qk_plans.keep(key, d)
+    if out is None:
+        with ctx:
+            out = (None if q is None else _like(q), None if k is None else _like(k))
+    qo, ko = out
+    check(abi.load().ttt_qk_norm_rope(ctypes.byref(d), _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight), _ptr(positions),
+                                      _freqs_ptr(freqs), _ptr(qo), _ptr(ko), raw))
     return qo, ko
 
 
@@ -185,51 +228,49 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, *, positions=None, freqs=None, m
     the inputs of :func:`qk_norm_rope`; dq and dk are dense, the weights' gradients fp32 [width]
     (None for a weight that is None). With norm "none" ``q`` and ``k`` are not read."""
     dev = _current_device()
-    dtype, batch, hq, hk, tokens, width, rot, pos_stride, ptrs = _qk_args(
-        dq_out, dk_out, positions, freqs, q_weight, k_weight, dev)
     raw, ctx = _place(stream, dev)
-    qs, ks = (batch, hq, tokens, width), (batch, hk, tokens, width)
-    kind = _choice(NORMS, norm, "norm")
-    none = (0, 0, 0)
-    grads, outs, xs, places = [], [], [], []
-    with ctx or _nothing:
-        for g, x, shape, name in ((dq_out, q, qs, "q"), (dk_out, k, ks, "k")):
+    try:
+        key = (dev, _meta(dq_out), _meta(dk_out), _meta(q), _meta(k), _meta(positions), _meta(freqs), _meta(q_weight),
+               _meta(k_weight), norm, layout, eps, magnitude, position0)
+    except AttributeError:
+        key = None
+    plan = _qk_back_plans.find(key) if key is not None else None
+    if plan is None:
+        d, dtype, qs, ks = _qk_call(dq_out, dk_out, positions, freqs, q_weight, k_weight, norm, layout, eps, magnitude,
+                                    position0, dev)
+        read = d.norm != abi.TTT_NORM_NONE
+        for g, x, shape, n in ((dq_out, q, qs, "q"), (dk_out, k, ks, "k")):
             if g is None:
                 if x is not None:
-                    raise ValueError(f"{name}: given without the gradient of its output")
-                grads.append(None), outs.append(None), xs.append(None), places.append((none, none, none))
+                    raise ValueError(f"{n}: given without the gradient of its output")
                 continue
-            grads.append(_rows(g, f"d{name}_out", dtype, shape, dev))
-            read = kind != abi.TTT_NORM_NONE
-            xs.append(_rows(x, name, dtype, shape, dev) if read else None)
-            y = torch.empty(shape, dtype=dtype, device=g.device)
-            outs.append(y)
-            places.append((_strides(shape, x.stride()) if read else none, _strides(shape, g.stride()),
-                           _strides(shape, y.stride())))
-        dqw = None if q_weight is None else torch.empty(width, dtype=_F32, device=q_weight.device)
-        dkw = None if k_weight is None else torch.empty(width, dtype=_F32, device=k_weight.device)
-        key = (1 if dtype is _BF16 else 0, batch, hq, hk, width, rot, kind, _choice(LAYOUTS, layout, "layout"), float(eps),
-               float(magnitude), tokens, int(position0), pos_stride, places[0][0], places[1][0], places[0][1],
-               places[1][1], places[0][2], places[1][2])
-        d = _qk_desc(*key)
-        nbytes = _qk_workspaces(dev, *key) if dqw is not None or dkw is not None else 0
+            _rows(g, f"d{n}_out", dtype, shape, dev)
+            _set(d, n + "_out", shape, g)
+            _set(d, n + "_grad", shape, torch.empty(shape, device="meta"))
+            if read:
+                _rows(x, n, dtype, shape, dev)
+                _set(d, n, shape, x)
+        gains = q_weight is not None or k_weight is not None
+        plan = d, read, abi.load().ttt_qk_norm_rope_workspace(ctypes.byref(d)) if gains else 0
+        if key is not None:
+            _qk_back_plans.keep(key, plan)
+    d, read, nbytes = plan
+    with ctx:
+        dq = None if dq_out is None else _like(dq_out)
+        dk = None if dk_out is None else _like(dk_out)
+        dqw = None if q_weight is None else _like(q_weight)
+        dkw = None if k_weight is None else _like(k_weight)
         ws = _workspace(nbytes, dev)
-    check(abi.load().ttt_qk_norm_rope_backward(ctypes.byref(d), *grads, *xs, *ptrs, _ptr(outs[0]), _ptr(outs[1]), _ptr(dqw), _ptr(dkw),
-                                               _ptr(ws), nbytes, raw))
-    return outs[0], outs[1], dqw, dkw
+    check(abi.load().ttt_qk_norm_rope_backward(
+        ctypes.byref(d), _ptr(dq_out), _ptr(dk_out), _ptr(q) if read else None, _ptr(k) if read else None, _ptr(q_weight),
+        _ptr(k_weight), _ptr(positions), _freqs_ptr(freqs), _ptr(dq), _ptr(dk), _ptr(dqw), _ptr(dkw), _ptr(ws), nbytes, raw))
+    return dq, dk, dqw, dkw
 
 
 # ---- the gated scan -------------------------------------------------------------------------
 
 
-@lru_cache(maxsize=256)
-def _scan_desc(batch, heads, tokens, scale, *strides):
-    return abi.ttt_gated_scan_desc(batch, heads, tokens, scale, *(abi.ttt_strides(*s) for s in strides))
-
-
-_scan_workspaces = lru_cache(maxsize=256)(lambda dev, *key: abi.load().ttt_gated_scan_workspace(ctypes.byref(_scan_desc(*key))))
-_scan_back_workspaces = lru_cache(maxsize=256)(
-    lambda dev, *key: abi.load().ttt_gated_scan_backward_workspace(ctypes.byref(_scan_desc(*key))))
+_scan_plans, _scan_back_plans, _step_plans = _Plans(), _Plans(), _Plans()
 
 
 def _scan_shape(q, dims, dev):
@@ -239,6 +280,16 @@ def _scan_shape(q, dims, dev):
     return q.shape
 
 
+def _scan_desc(shape, scale, q, k, v, o, g):
+    """The descriptor of a call; ``o`` may be None (a dense tensor)."""
+    o = torch.empty(shape, device="meta") if o is None else o
+    if len(shape) == 3:  # one token
+        two = lambda t: (*_strides(shape[:2], t.stride()[:2]), 0)  # noqa: E731
+        return abi.ttt_gated_scan_desc(shape[0], shape[1], 1, float(scale), *(abi.ttt_strides(*two(t)) for t in (q, k, v, o, g)))
+    return abi.ttt_gated_scan_desc(shape[0], shape[1], shape[2], float(scale),
+                                   *(abi.ttt_strides(*_strides(shape, t.stride())) for t in (q, k, v, o, g)))
+
+
 def gated_scan(q, k, v, g, *, scale=1.0, initial=None, out=None, final=None, stream=None):
     """ttt_gated_scan: S_t = e^{g_t}·S_{t-1} + k_tᵀ·v_t, o_t = scale·q_t·S_t per (sequence, head). ``q``,
     ``k``, ``v`` bf16 [batch, heads, tokens, 64] (any strides, dense rows), ``g`` fp32 [batch, heads,
@@ -246,24 +297,33 @@ def gated_scan(q, k, v, g, *, scale=1.0, initial=None, out=None, final=None, str
     (o, state): o in ``out`` or a new dense tensor; the state after the last token, fp32 [batch,
     heads, 64, 64], in ``final`` (which may be ``initial``) or a new tensor."""
     dev = _current_device()
-    shape = _scan_shape(q, 4, dev)
-    batch, heads, tokens, _ = shape
-    st = (batch, heads, 64, 64)
     raw, ctx = _place(stream, dev)
-    pq, pk, pv = (_rows(t, n, _BF16, shape, dev) for t, n in ((q, "q"), (k, "k"), (v, "v")))
-    pg = _rows(g, "g", _F32, shape[:3], dev, last=False)
-    pi = _dense(initial, "initial", _F32, st, dev)
-    with ctx or _nothing:
+    try:
+        key = (dev, _meta(q), _meta(k), _meta(v), _meta(g), _meta(initial), _meta(out), _meta(final), scale)
+    except AttributeError:  # something that is no tensor: the checks will name it
+        key = None
+    plan = _scan_plans.find(key) if key is not None else None
+    if plan is None:
+        shape = _scan_shape(q, 4, dev)
+        st = (shape[0], shape[1], 64, 64)
+        for t, n in ((q, "q"), (k, "k"), (v, "v")) + (((out, "out"),) if out is not None else ()):
+            _rows(t, n, _BF16, shape, dev)
+        _rows(g, "g", _F32, shape[:3], dev, last=False)
+        _dense_or_none(initial, "initial", _F32, st, dev)
+        _dense_or_none(final, "final", _F32, st, dev)
+        d = _scan_desc(shape, scale, q, k, v, out, g)
+        plan = d, st, abi.load().ttt_gated_scan_workspace(ctypes.byref(d))
+        if key is not None:
+            _scan_plans.keep(key, plan)
+    d, st, nbytes = plan
+    with ctx:
         if out is None:
-            out = torch.empty(shape, dtype=_BF16, device=q.device)
+            out = _like(q)
         if final is None:
             final = torch.empty(st, dtype=_F32, device=q.device)
-        key = (batch, heads, tokens, float(scale), _strides(shape, q.stride()), _strides(shape, k.stride()),
-               _strides(shape, v.stride()), _strides(shape, out.stride()), _strides(shape, g.stride()))
-        nbytes = _scan_workspaces(dev, *key)
         ws = _workspace(nbytes, dev)
-    check(abi.load().ttt_gated_scan(ctypes.byref(_scan_desc(*key)), pq, pk, pv, pg, pi, _rows(out, "out", _BF16, shape, dev),
-                                    _dense(final, "final", _F32, st, dev), _ptr(ws), nbytes, raw))
+    check(abi.load().ttt_gated_scan(ctypes.byref(d), q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), _ptr(initial),
+                                    out.data_ptr(), final.data_ptr(), _ptr(ws), nbytes, raw))
     return out, final
 
 
@@ -272,23 +332,32 @@ def gated_scan_backward(do, q, k, v, g, *, scale=1.0, initial=None, dfinal=None,
     ``dfinal`` of the final state (None: zero). All are dense; dinitial is None where ``initial``
     is."""
     dev = _current_device()
-    shape = _scan_shape(q, 4, dev)
-    batch, heads, tokens, _ = shape
-    st = (batch, heads, 64, 64)
     raw, ctx = _place(stream, dev)
-    pd, pq, pk, pv = (_rows(t, n, _BF16, shape, dev) for t, n in ((do, "do"), (q, "q"), (k, "k"), (v, "v")))
-    pg = _rows(g, "g", _F32, shape[:3], dev, last=False)
-    pi, pf = _dense(initial, "initial", _F32, st, dev), _dense(dfinal, "dfinal", _F32, st, dev)
-    key = (batch, heads, tokens, float(scale), _strides(shape, q.stride()), _strides(shape, k.stride()),
-           _strides(shape, v.stride()), _strides(shape, do.stride()), _strides(shape, g.stride()))
-    with ctx or _nothing:
-        dq, dk, dv = (torch.empty(shape, dtype=_BF16, device=q.device) for _ in range(3))
-        dg = torch.empty(shape[:3], dtype=_F32, device=q.device)
-        di = None if initial is None else torch.empty(st, dtype=_F32, device=q.device)
-        nbytes = _scan_back_workspaces(dev, *key)
+    try:
+        key = (dev, _meta(do), _meta(q), _meta(k), _meta(v), _meta(g), _meta(initial), _meta(dfinal), scale)
+    except AttributeError:
+        key = None
+    plan = _scan_back_plans.find(key) if key is not None else None
+    if plan is None:
+        shape = _scan_shape(q, 4, dev)
+        st = (shape[0], shape[1], 64, 64)
+        for t, n in ((do, "do"), (q, "q"), (k, "k"), (v, "v")):
+            _rows(t, n, _BF16, shape, dev)
+        _rows(g, "g", _F32, shape[:3], dev, last=False)
+        _dense_or_none(initial, "initial", _F32, st, dev)
+        _dense_or_none(dfinal, "dfinal", _F32, st, dev)
+        d = _scan_desc(shape, scale, q, k, v, do, g)
+        plan = d, abi.load().ttt_gated_scan_backward_workspace(ctypes.byref(d))
+        if key is not None:
+            _scan_back_plans.keep(key, plan)
+    d, nbytes = plan
+    with ctx:
+        dq, dk, dv, dg = _like(q), _like(k), _like(v), _like(g)
+        di = None if initial is None else _like(initial)
         ws = _workspace(nbytes, dev)
-    check(abi.load().ttt_gated_scan_backward(ctypes.byref(_scan_desc(*key)), pd, pq, pk, pv, pg, pi, pf, dq.data_ptr(), dk.data_ptr(),
-                                             dv.data_ptr(), dg.data_ptr(), _ptr(di), _ptr(ws), nbytes, raw))
+    check(abi.load().ttt_gated_scan_backward(
+        ctypes.byref(d), do.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), _ptr(initial), _ptr(dfinal),
+        dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dg.data_ptr(), _ptr(di), _ptr(ws), nbytes, raw))
     return dq, dk, dv, dg, di
 
 
@@ -297,32 +366,44 @@ def gated_scan_step(state, q, k, v, g, *, scale=1.0, out=None, stream=None):
     in place; ``q``, ``k``, ``v`` bf16 [batch, heads, 64], ``g`` fp32 [batch, heads] (any strides, dense
     rows). Returns o, bf16 [batch, heads, 64]."""
     dev = _current_device()
-    shape = _scan_shape(q, 3, dev)
-    batch, heads, _ = shape
     raw, ctx = _place(stream, dev)
-    pq, pk, pv = (_rows(t, n, _BF16, shape, dev) for t, n in ((q, "q"), (k, "k"), (v, "v")))
-    pg = _rows(g, "g", _F32, shape[:2], dev, last=False)
-    if state is None:
-        _refuse(state, "state", f"contiguous {(batch, heads, 64, 64)} {_F32}", dev)
-    ps = _dense(state, "state", _F32, (batch, heads, 64, 64), dev)
+    try:
+        key = (dev, _meta(state), _meta(q), _meta(k), _meta(v), _meta(g), _meta(out), scale)
+    except AttributeError:
+        key = None
+    d = _step_plans.find(key) if key is not None else None
+    if d is None:
+        shape = _scan_shape(q, 3, dev)
+        for t, n in ((q, "q"), (k, "k"), (v, "v")) + (((out, "out"),) if out is not None else ()):
+            _rows(t, n, _BF16, shape, dev)
+        _rows(g, "g", _F32, shape[:2], dev, last=False)
+        _dense(state, "state", _F32, (shape[0], shape[1], 64, 64), dev)
+        d = _scan_desc(shape, scale, q, k, v, out, g)
+        if key is not None:
+            _step_plans.keep(key, d)
     if out is None:
-        with ctx or _nothing:
-            out = torch.empty(shape, dtype=_BF16, device=q.device)
-    two = lambda t: (t.stride(0) if batch > 1 else 0, t.stride(1) if heads > 1 else 0, 0)  # noqa: E731
-    d = _scan_desc(batch, heads, 1, float(scale), two(q), two(k), two(v), two(out), two(g))
-    check(abi.load().ttt_gated_scan_step(ctypes.byref(d), pq, pk, pv, pg, ps, _rows(out, "out", _BF16, shape, dev), raw))
+        with ctx:
+            out = _like(q)
+    check(abi.load().ttt_gated_scan_step(ctypes.byref(d), q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
+                                         state.data_ptr(), out.data_ptr(), raw))
     return out
 
 
 # ---- the gated feed-forward block -------------------------------------------------------------
 
 
-def _ffn_shape(x, w_gate, dev):
-    if not isinstance(x, torch.Tensor) or x.dim() != 2:
-        _refuse(x, "x", "[tokens, d] torch.bfloat16", dev)
-    if not isinstance(w_gate, torch.Tensor) or w_gate.dim() != 2:
-        _refuse(w_gate, "w_gate", "[f, d] torch.bfloat16", dev)
-    return x.shape[0], x.shape[1], w_gate.shape[0]
+_ffn_plans, _ffn_back_plans = _Plans(), _Plans()
+
+
+def _ffn_shape(x, w_gate, w_up, dev):
+    for t, n, want in ((x, "x", "[tokens, d]"), (w_gate, "w_gate", "[f, d]"), (w_up, "w_up", "[f, d]")):
+        if not isinstance(t, torch.Tensor) or t.dim() != 2:
+            _refuse(t, n, want + " torch.bfloat16", dev)
+    T, d, f = x.shape[0], x.shape[1], w_gate.shape[0]
+    _dense(x, "x", _BF16, (T, d), dev)
+    _dense(w_gate, "w_gate", _BF16, (f, d), dev)
+    _dense(w_up, "w_up", _BF16, (f, d), dev)
+    return T, d, f
 
 
 def gated_ffn(x, w_gate, w_up, *, activation="silu", save=False, out=None, status=None, stream=None):
@@ -332,23 +413,29 @@ def gated_ffn(x, w_gate, w_up, *, activation="silu", save=False, out=None, statu
     ``status`` (int32 device tensor of one element, optional) is set to 0, or to TTT_ERR_TIMEOUT if
     a bounded device-side wait ran out."""
     dev = _current_device()
-    T, d, f = _ffn_shape(x, w_gate, dev)
     raw, ctx = _place(stream, dev)
-    px, pg, pu = (_dense(x, "x", _BF16, (T, d), dev), _dense(w_gate, "w_gate", _BF16, (f, d), dev),
-                  _dense(w_up, "w_up", _BF16, (f, d), dev))
-    act = _choice(ACTIVATIONS, activation, "activation")
+    try:
+        key = (dev, _meta(x), _meta(w_gate), _meta(w_up), _meta(out), _meta(status), activation)
+    except AttributeError:  # something that is no tensor: the checks will name it
+        key = None
+    plan = _ffn_plans.find(key) if key is not None else None
+    if plan is None:
+        T, d, f = _ffn_shape(x, w_gate, w_up, dev)
+        _dense_or_none(out, "out", _BF16, (T, f), dev)
+        _dense_or_none(status, "status", _I32, (1,), dev)
+        plan = T, d, f, _choice(ACTIVATIONS, activation, "activation")
+        if key is not None:
+            _ffn_plans.keep(key, plan)
+    T, d, f, act = plan
     gate = up = None
-    with ctx or _nothing:
+    with ctx:
         if out is None:
-            out = torch.empty((T, f), dtype=_BF16, device=x.device)
+            out = x.new_empty((T, f))
         if save:
             gate, up = torch.empty_like(out), torch.empty_like(out)
-    check(abi.load().ttt_gated_ffn(px, pg, pu, T, d, f, act, _dense(out, "out", _BF16, (T, f), dev), _ptr(gate), _ptr(up),
-                                   _dense(status, "status", _I32, (1,), dev), raw))
+    check(abi.load().ttt_gated_ffn(x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), T, d, f, act, out.data_ptr(), _ptr(gate),
+                                   _ptr(up), _ptr(status), raw))
     return (out, gate, up) if save else out
-
-
-_ffn_workspaces = lru_cache(maxsize=256)(lambda dev, *key: abi.load().ttt_gated_ffn_backward_workspace(*key))
 
 
 def gated_ffn_backward(dz, x, w_gate, w_up, gate, up, *, activation="silu", need_dx=True, need_dw=True, status=None,
@@ -357,17 +444,26 @@ def gated_ffn_backward(dz, x, w_gate, w_up, gate, up, *, activation="silu", need
     pre-activations ``gate`` and ``up``, all bf16 and contiguous; ``need_dx`` or ``need_dw`` false
     leaves those out (None)."""
     dev = _current_device()
-    T, d, f = _ffn_shape(x, w_gate, dev)
     raw, ctx = _place(stream, dev)
-    act = _choice(ACTIVATIONS, activation, "activation")
-    pz, pga, pup = (_dense(t, n, _BF16, (T, f), dev) for t, n in ((dz, "dz"), (gate, "gate"), (up, "up")))
-    px, pg, pu = (_dense(x, "x", _BF16, (T, d), dev), _dense(w_gate, "w_gate", _BF16, (f, d), dev),
-                  _dense(w_up, "w_up", _BF16, (f, d), dev))
-    with ctx or _nothing:
-        dx = torch.empty((T, d), dtype=_BF16, device=x.device) if need_dx else None
-        dwg, dwu = (torch.empty((f, d), dtype=_BF16, device=x.device) if need_dw else None for _ in range(2))
-        nbytes = _ffn_workspaces(dev, T, d, f)
+    try:
+        key = (dev, _meta(dz), _meta(x), _meta(w_gate), _meta(w_up), _meta(gate), _meta(up), _meta(status), activation)
+    except AttributeError:
+        key = None
+    plan = _ffn_back_plans.find(key) if key is not None else None
+    if plan is None:
+        T, d, f = _ffn_shape(x, w_gate, w_up, dev)
+        for t, n in ((dz, "dz"), (gate, "gate"), (up, "up")):
+            _dense(t, n, _BF16, (T, f), dev)
+        _dense_or_none(status, "status", _I32, (1,), dev)
+        plan = (T, d, f, _choice(ACTIVATIONS, activation, "activation"), abi.load().ttt_gated_ffn_backward_workspace(T, d, f))
+        if key is not None:
+            _ffn_back_plans.keep(key, plan)
+    T, d, f, act, nbytes = plan
+    with ctx:
+        dx = torch.empty_like(x) if need_dx else None
+        dwg, dwu = (torch.empty_like(w_gate) if need_dw else None for _ in range(2))
         ws = _workspace(nbytes, dev)
-    check(abi.load().ttt_gated_ffn_backward(pz, px, pg, pu, pga, pup, T, d, f, act, _ptr(dx), _ptr(dwg), _ptr(dwu), _ptr(ws),
-                                            nbytes, _dense(status, "status", _I32, (1,), dev), raw))
+    check(abi.load().ttt_gated_ffn_backward(
+        dz.data_ptr(), x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), gate.data_ptr(), up.data_ptr(), T, d, f, act, _ptr(dx),
+        _ptr(dwg), _ptr(dwu), _ptr(ws), nbytes, _ptr(status), raw))
     return dx, dwg, dwu

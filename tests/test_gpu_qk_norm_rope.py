@@ -144,6 +144,17 @@ def test_rows_of_zeros_and_infinities(cwl):
     assert torch.equal(y[0, 0, 0], x[0, 0, 0])
 
 
+def test_no_epsilon(cwl):
+    """eps 0: finite rows stay finite, and so do the gains' gradients with heads left over."""
+    q, k, dq, dk, pos, f, w = _case(1, 3, 3, 1, 64, 64, 8)
+    args = dict(positions=pos.cuda(), freqs=f.cuda(), q_weight=w[0].cuda(), k_weight=w[1].cuda(), eps=0.0)
+    got = cwl.qk_norm_rope(q.cuda(), k.cuda(), **args)
+    ref = op.norm_rope(to_np(q), pos.numpy(), to_np(f), eps=0.0, weight=to_np(w[0]))
+    _near(got[0], ref, 2.0 ** -18 * _row_max(ref), torch.bfloat16, "q")
+    back = cwl.qk_norm_rope_backward(dq.cuda(), dk.cuda(), q.cuda(), k.cuda(), **args)
+    assert all(torch.isfinite(t).all() for t in back)
+
+
 def test_many_rows_and_repeated_bits(cwl):
     """More rows than the GPU holds threads for, against torch in 64 bits; the gains' gradients come
     out the same every time."""
