@@ -13,11 +13,14 @@
 //   FWD  rows: tokens; columns: 128 of Wg's rows (loaded by the first CTA) and the same 128 of
 //        Wu's (by the second), so every thread of the epilogue finds g and u of one output in
 //        its own TMEM lane and no pre-activation goes through memory. A, B K-major.
+//        Tiles take 128 columns of f, or fewer where that fills the SM pairs' last round better
+//        (columns_of).
 //   DX   rows: tokens; columns: 256 of d; the sum runs over dG·Wg and then dU·Wu in the same
-//        accumulator. A K-major, B MN-major. With fewer tiles than SM pairs the sum is cut into
-//        parts, whose fp32 results a second launch adds in order.
+//        accumulator. A K-major, B MN-major.
 //   DW   rows: 256 of f, gate tiles and then up tiles; columns: 256 of d; the sum runs over the
 //        tokens. A, B MN-major: X, dG and dU are read as they lie, nothing is transposed.
+// The pairs take whole tiles in rounds; DX and DW cut the sums of the tiles left for a last, unfilled
+// round into as many parts as there are pairs, whose fp32 results a small launch adds in order.
 // Sizes need not be multiples of the tiles: TMA reads zeros past the ends, stores are clipped.
 //
 // k_ffn_few takes up to 32 tokens, where the weights' bytes are all that counts: see there.
@@ -44,6 +47,7 @@ enum : int { FWD = 0, DX = 1, DW = 2 };
 
 struct __align__(1024) FfnSmem {
   uint8_t ring[kFStages][2 * kHalf];
+  uint8_t out[kFEpi][32 * 64];  // a warp's 32 rows x 32 bf16 columns on their way out
   uint64_t full[kFStages], empty[kFStages];
   uint64_t tfull[2], tempty[2];
   uint32_t tmem;
@@ -53,41 +57,81 @@ struct __align__(1024) FfnSmem {
 struct FfnArgs {
   int M, N;           // rows and columns of the result (FWD: T, f; DX: T, d; DW: f, d)
   int kblocks;        // k-blocks of one product (DX: of each of the two)
-  int tiles_m, tiles_n, splits, per_split;
+  int tiles_m, tiles_n;
+  int cols;           // FWD: columns of f in a tile, a multiple of 8 up to 128
+  int whole;          // tiles whose sum one pair makes alone: the first of the order
+  int splits, per_split;  // parts of the sums of the tiles after them, and k-blocks of a part
   int act;
   __nv_bfloat16 *z, *g, *u;  // FWD: outputs (g and u or null); DX: z = dX; DW: g = dWg, u = dWu
-  float* part;               // DX with splits > 1: [splits][M][N]
+  float* part;               // [tiles after the whole ones][splits][256][256]
   DevStatus status;
 };
 
 __device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
-__device__ __forceinline__ float normal_cdf(float x) { return 0.5f * (1.f + erff(x * 0.70710678118654752f)); }
+
+// Φ(x) = 1 − erfc(x/√2)/2, erfc by the rational approximation 7.1.26 of Abramowitz and Stegun
+// (|error| <= 1.5e-7), from the side where it is small. erff took the forward epilogue over.
+__device__ __forceinline__ float normal_cdf(float x) {
+  const float z = fabsf(x) * 0.70710678118654752f;
+  const float t = __fdividef(1.f, fmaf(0.3275911f, z, 1.f));
+  const float p = t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 1.061405429f, -1.453152027f), 1.421413741f), -0.284496736f), 0.254829592f);
+  const float tail = 0.5f * p * __expf(-z * z);
+  return x < 0.f ? tail : 1.f - tail;
+}
 
 __device__ __forceinline__ float act_of(float x, int act) {
   return act == TTT_ACT_SILU ? x * sigmoid(x) : x * normal_cdf(x);
 }
 
-// Stores 32 bf16 values of one row, clipped to ncols (a multiple of 8).
-__device__ __forceinline__ void store32(__nv_bfloat16* row, int col0, int ncols, const float (&v)[32]) {
+// A warp's 32 rows (one a lane) of 32 bf16 values out to rows row0 .., columns col0 .. of `out` (row
+// length ld), clipped to `rows` and `cols` (a multiple of 8): through shared memory, so that four
+// lanes write 64 bytes of one row and not each lane its own row.
+__device__ __forceinline__ void store_tile(uint8_t* stage, int lane, const float (&v)[32], __nv_bfloat16* out, size_t ld, int row0,
+                                           int rows, int col0, int cols) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (col0 + 8 * i < ncols)
-      *reinterpret_cast<uint4*>(row + col0 + 8 * i) =
-          make_uint4(pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]),
-                     pack_bf16(v[8 * i + 4], v[8 * i + 5]), pack_bf16(v[8 * i + 6], v[8 * i + 7]));
+  for (int c = 0; c < 4; ++c)
+    *reinterpret_cast<uint4*>(stage + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) =
+        make_uint4(pack_bf16(v[8 * c], v[8 * c + 1]), pack_bf16(v[8 * c + 2], v[8 * c + 3]),
+                   pack_bf16(v[8 * c + 4], v[8 * c + 5]), pack_bf16(v[8 * c + 6], v[8 * c + 7]));
+  __syncwarp();
+  const int c = lane & 3;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = 8 * i + (lane >> 2);
+    if (row0 + r < rows && col0 + 8 * c < cols)
+      *reinterpret_cast<uint4*>(out + (size_t)(row0 + r) * ld + col0 + 8 * c) =
+          *reinterpret_cast<const uint4*>(stage + r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+  }
+  __syncwarp();
 }
 
-// Tile t of the order that keeps the running tiles on few rows and columns at once (L2): blocks of
-// eight row tiles, down the rows first.
-__device__ __forceinline__ void tile_at(const FfnArgs& a, int t, int& m, int& n, int& split) {
-  const int per = a.tiles_m * a.tiles_n;
-  split = t / per;
-  t %= per;
+// What unit u of the order is: tile (m, n) and k-blocks k0 .. k1. The order keeps the running tiles
+// on few rows and columns at once (L2): blocks of eight row tiles, down the rows first. After the
+// whole tiles come the parts of the others.
+struct Unit {
+  int m, n, k0, k1, part;  // part: index of the part's result, -1 for a whole tile
+};
+
+__device__ __forceinline__ Unit unit_at(const FfnArgs& a, int u, int total_k) {
+  Unit r;
+  int t = u;
+  r.k0 = 0;
+  r.k1 = total_k;
+  r.part = -1;
+  if (u >= a.whole) {
+    r.part = u - a.whole;
+    t = a.whole + r.part / a.splits;
+    r.k0 = (r.part % a.splits) * a.per_split;
+    r.k1 = min(total_k, r.k0 + a.per_split);
+  }
   const int block = t / (8 * a.tiles_n), m0 = 8 * block, rows = min(8, a.tiles_m - m0);
-  const int r = t - block * 8 * a.tiles_n;
-  m = m0 + r % rows;
-  n = r / rows;
+  const int at = t - block * 8 * a.tiles_n;
+  r.m = m0 + at % rows;
+  r.n = at / rows;
+  return r;
 }
+
+__host__ __device__ inline int units_of(const FfnArgs& a) { return a.whole + (a.tiles_m * a.tiles_n - a.whole) * a.splits; }
 
 // FWD: tmA0 = X, tmB0 = Wg, tmB1 = Wu. DX: tmA0 = dG, tmA1 = dU, tmB0 = Wg, tmB1 = Wu.
 // DW: tmA0 = dG, tmA1 = dU, tmB0 = X.
@@ -100,7 +144,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)pair::rank();
   const int npairs = gridDim.x / 2, me = blockIdx.x / 2;
-  const int ntiles = a.tiles_m * a.tiles_n * a.splits;
+  const int units = units_of(a);
   const int total_k = MODE == DX ? 2 * a.kblocks : a.kblocks;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kFStages; ++i) {
@@ -121,10 +165,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
   tc::fence_after();
   const uint32_t tmem = sm.tmem;
   volatile int* abort = &sm.abort;
-  auto k_range = [&](int split, int& k0, int& k1) {
-    k0 = split * a.per_split;
-    k1 = min(total_k, k0 + a.per_split);
-  };
+  const int bcols = MODE == FWD ? a.cols : FM;  // columns of B that each CTA loads
 
   if (warp == 0) {
     if (lane == 0) {
@@ -132,11 +173,10 @@ __global__ void __launch_bounds__(kFThreads, 1)
       tma_prefetch_desc(&tmB0);
       uint32_t it = 0;
       bool ok = true;
-      for (int t = me; t < ntiles && ok; t += npairs) {
-        int m, n, split, k0, k1;
-        tile_at(a, t, m, n, split);
-        k_range(split, k0, k1);
-        for (int kb = k0; kb < k1; ++kb, ++it) {
+      for (int t = me; t < units && ok; t += npairs) {
+        const Unit un = unit_at(a, t, total_k);
+        const int m = un.m, n = un.n;
+        for (int kb = un.k0; kb < un.k1; ++kb, ++it) {
           const int s = it % kFStages;
           if (*abort || (it >= (uint32_t)kFStages && !mbar_wait(&sm.empty[s], ((it / kFStages) - 1) & 1, a.status, abort))) {
             ok = false;
@@ -144,11 +184,11 @@ __global__ void __launch_bounds__(kFThreads, 1)
           }
           uint8_t *sa = sm.ring[s], *sb = sa + kHalf;
           // Both CTAs' loads complete on the first CTA's barrier, which expects the bytes of both.
-          if (rank == 0) mbar_arrive_expect_tx(&sm.full[s], 4 * kHalf);
+          if (rank == 0) mbar_arrive_expect_tx(&sm.full[s], 2 * kHalf + 2 * bcols * FK * 2);
           const uint32_t bar = pair::in_first(&sm.full[s]);
           if constexpr (MODE == FWD) {
             pair::load_2d(sa, &tmA0, bar, kb * FK, m * kTileM + rank * FM);
-            pair::load_2d(sb, rank ? &tmB1 : &tmB0, bar, kb * FK, n * (kTileN / 2));
+            pair::load_2d(sb, rank ? &tmB1 : &tmB0, bar, kb * FK, n * a.cols);
           } else if constexpr (MODE == DX) {
             const bool up = kb >= a.kblocks;
             const int k = (up ? kb - a.kblocks : kb) * FK;
@@ -179,20 +219,18 @@ __global__ void __launch_bounds__(kFThreads, 1)
     }
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
-      constexpr uint32_t idesc = tc::idesc_bf16(kTileM, kTileN, MODE == DW, MODE != FWD);
+      const uint32_t idesc = tc::idesc_bf16(kTileM, 2 * bcols, MODE == DW, MODE != FWD);
       uint32_t it = 0, tcount = 0;
       bool ok = true;
-      for (int t = me; t < ntiles && ok; t += npairs) {
-        int m, n, split, k0, k1;
-        tile_at(a, t, m, n, split);
-        k_range(split, k0, k1);
+      for (int t = me; t < units && ok; t += npairs) {
+        const Unit un = unit_at(a, t, total_k);
         const int acc = tcount & 1;
         if (tcount >= 2 && !mbar_wait<true>(&sm.tempty[acc], ((tcount >> 1) - 1) & 1, a.status, abort)) {
           ok = false;
           break;
         }
         tc::fence_after();
-        for (int kb = k0; kb < k1; ++kb, ++it) {
+        for (int kb = un.k0; kb < un.k1; ++kb, ++it) {
           const int s = it % kFStages;
           if (!mbar_wait<true>(&sm.full[s], (it / kFStages) & 1, a.status, abort)) {
             ok = false;
@@ -204,7 +242,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
           for (int kk = 0; kk < FK / 16; ++kk) {
             const uint64_t ad = MODE == DW ? tc::smem_desc(a0 + kk * 2048, 8192, 1024) : tc::smem_desc(a0 + kk * 32, 16, 1024);
             const uint64_t bd = MODE == FWD ? tc::smem_desc(b0 + kk * 32, 16, 1024) : tc::smem_desc(b0 + kk * 2048, 8192, 1024);
-            pair::mma(tmem + acc * kTileN, ad, bd, idesc, (kb != k0 || kk != 0));
+            pair::mma(tmem + acc * kTileN, ad, bd, idesc, (kb != un.k0 || kk != 0));
           }
           pair::commit(&sm.empty[s]);
         }
@@ -219,24 +257,25 @@ __global__ void __launch_bounds__(kFThreads, 1)
         mbar_wait(&sm.empty[(it - 1) % kFStages], ((it - 1) / kFStages) & 1, a.status, nullptr);
     }
   } else {
-    const int lq = warp & 3, half = (warp - 2) >> 2;  // TMEM lane quarter, half of the columns
+    const int lq = warp & 3, half = (warp - 2) >> 2;  // TMEM lane quarter; every other 32 columns
+    uint8_t* stage = sm.out[warp - 2];
     uint32_t tcount = 0;
-    for (int t = me; t < ntiles; t += npairs) {
-      int m, n, split;
-      tile_at(a, t, m, n, split);
+    for (int t = me; t < units; t += npairs) {
+      const Unit un = unit_at(a, t, total_k);
       const int acc = tcount & 1;
       const bool ok = mbar_wait(&sm.tfull[acc], (tcount >> 1) & 1, a.status, nullptr);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc::fence_after();
       const uint32_t tb = tmem + ((uint32_t)(lq * 32) << 16) + (uint32_t)(acc * kTileN);
-      int row = m * kTileM + rank * FM + lq * 32 + lane;
+      int row0 = un.m * kTileM + rank * FM + lq * 32;
       if constexpr (MODE == FWD) {
+        const int col_end = min(a.N, (un.n + 1) * a.cols);
 #pragma unroll 1
-        for (int j = 0; j < 2; ++j) {
-          const int c = half * 64 + j * 32, col = n * (kTileN / 2) + c;
+        for (int c = half * 32; c < a.cols; c += 64) {
+          const int col = un.n * a.cols + c;
           uint32_t rg[32], ru[32];
           tc::ld32(tb + c, rg);
-          tc::ld32(tb + kTileN / 2 + c, ru);
+          tc::ld32(tb + a.cols + c, ru);
           tc::wait_ld();
           float g[32], u[32];
 #pragma unroll
@@ -244,44 +283,40 @@ __global__ void __launch_bounds__(kFThreads, 1)
             g[i] = __uint_as_float(rg[i]);
             u[i] = __uint_as_float(ru[i]);
           }
-          if (row < a.M) {
-            const size_t at = (size_t)row * a.N;
-            if (a.g != nullptr) {
-              store32(a.g + at, col, a.N, g);
-              store32(a.u + at, col, a.N, u);
-            }
-#pragma unroll
-            for (int i = 0; i < 32; ++i) g[i] = act_of(g[i], a.act) * u[i];
-            store32(a.z + at, col, a.N, g);
+          if (a.g != nullptr) {
+            store_tile(stage, lane, g, a.g, a.N, row0, a.M, col, col_end);
+            store_tile(stage, lane, u, a.u, a.N, row0, a.M, col, col_end);
           }
+          if (a.act == TTT_ACT_SILU) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) g[i] = g[i] * sigmoid(g[i]) * u[i];
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) g[i] = g[i] * normal_cdf(g[i]) * u[i];
+          }
+          store_tile(stage, lane, g, a.z, a.N, row0, a.M, col, col_end);
         }
       } else {
         __nv_bfloat16* out = a.z;
-        int mrow = row;
         if constexpr (MODE == DW) {
           const int half_m = a.tiles_m / 2;
-          out = m >= half_m ? a.u : a.g;
-          mrow = m >= half_m ? row - half_m * kTileM : row;
+          out = un.m >= half_m ? a.u : a.g;
+          row0 -= un.m >= half_m ? half_m * kTileM : 0;
         }
 #pragma unroll 1
-        for (int j = 0; j < 4; ++j) {
-          const int c = half * 128 + j * 32, col = n * kTileN + c;
+        for (int c = half * 32; c < kTileN; c += 64) {
           uint32_t r[32];
           tc::ld32(tb + c, r);
           tc::wait_ld();
-          if (mrow < a.M) {
-            if (MODE == DX && a.splits > 1) {
-              float* p = a.part + ((size_t)split * a.M + mrow) * a.N + col;
+          if (un.part >= 0) {
+            uint4* p = reinterpret_cast<uint4*>(a.part + ((size_t)un.part * kTileM + rank * FM + lq * 32 + lane) * kTileN + c);
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
-                if (col + 4 * i < a.N)
-                  *reinterpret_cast<uint4*>(p + 4 * i) = make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
-            } else {
-              float v[32];
+            for (int i = 0; i < 8; ++i) p[i] = make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+          } else {
+            float v[32];
 #pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-              store32(out + (size_t)mrow * a.N, col, a.N, v);
-            }
+            for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+            store_tile(stage, lane, v, out, a.N, row0, a.M, un.n * kTileN + c, a.N);
           }
         }
       }
@@ -300,16 +335,29 @@ __global__ void __launch_bounds__(kFThreads, 1)
   if (warp == 1) pair::dealloc(tmem, kFTmem);
 }
 
-// out = Σ over the parts, in order, as bf16; eight values a thread.
-__global__ void __launch_bounds__(256) k_ffn_join(const float* __restrict__ part, int splits, size_t n, __nv_bfloat16* __restrict__ out) {
-  const size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * 8;
-  if (i >= n) return;
+// The tiles made in parts: the sums of their parts, in order, as bf16. grid (32, tiles after the whole
+// ones), eight values a thread, eight rows a CTA.
+template <int MODE>
+__global__ void __launch_bounds__(256) k_ffn_join(const FfnArgs a) {
+  const Unit un = unit_at(a, a.whole + blockIdx.y * a.splits, 0);
+  const int r = blockIdx.x * 8 + (threadIdx.x >> 5), c = (threadIdx.x & 31) * 8;
+  __nv_bfloat16* out = a.z;
+  int row = un.m * kTileM + r;
+  if (MODE == DW) {
+    const int half_m = a.tiles_m / 2;
+    out = un.m >= half_m ? a.u : a.g;
+    row -= un.m >= half_m ? half_m * kTileM : 0;
+  }
+  const int col = un.n * kTileN + c;
+  if (row >= a.M || col >= a.N) return;
+  const float* p = a.part + ((size_t)blockIdx.y * a.splits * kTileM + r) * kTileN + c;
   float v[8] = {};
-  for (int s = 0; s < splits; ++s) {
-    const float4 x = *reinterpret_cast<const float4*>(part + s * n + i), y = *reinterpret_cast<const float4*>(part + s * n + i + 4);
+#pragma unroll 4
+  for (int s = 0; s < a.splits; ++s, p += kTileM * kTileN) {
+    const float4 x = *reinterpret_cast<const float4*>(p), y = *reinterpret_cast<const float4*>(p + 4);
     v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w, v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
   }
-  *reinterpret_cast<uint4*>(out + i) =
+  *reinterpret_cast<uint4*>(out + (size_t)row * a.N + col) =
       make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
 }
 
@@ -356,71 +404,86 @@ __global__ void __launch_bounds__(256) k_ffn_act_bwd(const __nv_bfloat16* __rest
 
 // The weights' bytes bound it, so they go from HBM straight into the registers that the tensor
 // cores read (mma.sync: with at most 32 columns its rate is far from counting), with no stage in
-// shared memory and no barrier on the way. A CTA of eight warps takes 16 rows of Wg and the same 16
-// of Wu; warp w takes every eighth 32-wide slice of the sum, and the warps' results are added in
-// order at the end. A lane's 16-byte load holds eight consecutive k of one row; the products' k
-// slots are filled in that order for the weights and for X alike, which a sum does not mind.
-// NT: token blocks of eight.
+// shared memory and no barrier on the way. A CTA of four warps takes eight rows of Wg and the same
+// eight of Wu as the 16 rows of one product, so a thread ends with g and u of the same outputs; warp
+// w takes every fourth 32-wide slice of the sum, the next slices' loads in flight while it works on
+// these, and the warps' results are added in order at the end. A lane's 16-byte load holds eight
+// consecutive k of one row; the products' k slots are filled in that order for the weights and for X
+// alike, which a sum does not mind. NT: token blocks of eight.
+constexpr int kFewWarps = 4;
+
+__device__ __forceinline__ uint4 load_once(const __nv_bfloat16* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+
 template <int NT>
-__global__ void __launch_bounds__(256) k_ffn_few(const __nv_bfloat16* __restrict__ X, const __nv_bfloat16* __restrict__ Wg,
-                                                 const __nv_bfloat16* __restrict__ Wu, int T, int d, int f, int act,
-                                                 __nv_bfloat16* __restrict__ z, __nv_bfloat16* __restrict__ gout,
-                                                 __nv_bfloat16* __restrict__ uout) {
-  __shared__ float part[8][2][NT][8][17];  // [warp][gate, up][token block][token][row]
+__global__ void __launch_bounds__(32 * kFewWarps) k_ffn_few(const __nv_bfloat16* __restrict__ X, const __nv_bfloat16* __restrict__ Wg,
+                                                            const __nv_bfloat16* __restrict__ Wu, int T, int d, int f, int act,
+                                                            __nv_bfloat16* __restrict__ z, __nv_bfloat16* __restrict__ gout,
+                                                            __nv_bfloat16* __restrict__ uout) {
+  __shared__ float part[kFewWarps][2][8 * NT][9];  // [warp][gate, up][token][row]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-  const int f0 = blockIdx.x * 16;
+  const int f0 = blockIdx.x * 8;  // f is a multiple of 8
   const int steps = (d + 31) / 32;
-  float ag[NT][4] = {}, au[NT][4] = {};
-  const bool lo = f0 + g < f, hi = f0 + g + 8 < f;
-  const __nv_bfloat16* pg = Wg + (size_t)(f0 + (lo ? g : 0)) * d + 8 * q;
-  const __nv_bfloat16* pu = Wu + (size_t)(f0 + (lo ? g : 0)) * d + 8 * q;
-  const size_t down = hi ? (size_t)8 * d : 0;
+  constexpr int UN = NT == 4 ? 2 : 4;
+  const __nv_bfloat16* pg = Wg + (size_t)(f0 + g) * d + 8 * q;
+  const __nv_bfloat16* pu = Wu + (size_t)(f0 + g) * d + 8 * q;
+  const __nv_bfloat16* px = X + (size_t)g * d + 8 * q;
   const uint4 none = make_uint4(0, 0, 0, 0);
-  constexpr int UN = NT == 1 ? 4 : 2;
-  for (int st = warp; st < steps; st += 8 * UN) {
-    uint4 wg[UN][2], wu[UN][2], x[UN][NT];
+  uint4 wg[2][UN], wu[2][UN];
+  auto fetch = [&](int st, uint4 (&G)[UN], uint4 (&U)[UN]) {
 #pragma unroll
     for (int i = 0; i < UN; ++i) {
-      const int k = (st + 8 * i) * 32;
+      const int k = (st + kFewWarps * i) * 32;
       const bool in = k + 8 * q < d;
-      wg[i][0] = in && lo ? __ldcs(reinterpret_cast<const uint4*>(pg + k)) : none;
-      wg[i][1] = in && hi ? __ldcs(reinterpret_cast<const uint4*>(pg + down + k)) : none;
-      wu[i][0] = in && lo ? __ldcs(reinterpret_cast<const uint4*>(pu + k)) : none;
-      wu[i][1] = in && hi ? __ldcs(reinterpret_cast<const uint4*>(pu + down + k)) : none;
+      G[i] = in ? load_once(pg + k) : none;
+      U[i] = in ? load_once(pu + k) : none;
+    }
+  };
+  float acc[NT][4] = {};
+  auto work = [&](int st, const uint4 (&G)[UN], const uint4 (&U)[UN]) {
+    uint4 x[UN][NT];
+#pragma unroll
+    for (int i = 0; i < UN; ++i) {
+      const int k = (st + kFewWarps * i) * 32;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
-        x[i][nt] = in && 8 * nt + g < T ? *reinterpret_cast<const uint4*>(X + (size_t)(8 * nt + g) * d + k + 8 * q) : none;
+        x[i][nt] = k + 8 * q < d && 8 * nt + g < T ? *reinterpret_cast<const uint4*>(px + (size_t)(8 * nt) * d + k) : none;
     }
 #pragma unroll
     for (int i = 0; i < UN; ++i) {
-      const uint32_t a0[4] = {wg[i][0].x, wg[i][1].x, wg[i][0].y, wg[i][1].y}, a1[4] = {wg[i][0].z, wg[i][1].z, wg[i][0].w, wg[i][1].w};
-      const uint32_t b0[4] = {wu[i][0].x, wu[i][1].x, wu[i][0].y, wu[i][1].y}, b1[4] = {wu[i][0].z, wu[i][1].z, wu[i][0].w, wu[i][1].w};
+      const uint32_t a0[4] = {G[i].x, U[i].x, G[i].y, U[i].y}, a1[4] = {G[i].z, U[i].z, G[i].w, U[i].w};
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        wm::mma(ag[nt], a0, x[i][nt].x, x[i][nt].y);
-        wm::mma(ag[nt], a1, x[i][nt].z, x[i][nt].w);
-        wm::mma(au[nt], b0, x[i][nt].x, x[i][nt].y);
-        wm::mma(au[nt], b1, x[i][nt].z, x[i][nt].w);
+        wm::mma(acc[nt], a0, x[i][nt].x, x[i][nt].y);
+        wm::mma(acc[nt], a1, x[i][nt].z, x[i][nt].w);
       }
     }
+  };
+  constexpr int kStep = kFewWarps * UN;
+  fetch(warp, wg[0], wu[0]);
+  for (int st = warp; st < steps; st += 2 * kStep) {
+    fetch(st + kStep, wg[1], wu[1]);  // past the end: zeros, no loads
+    work(st, wg[0], wu[0]);
+    fetch(st + 2 * kStep, wg[0], wu[0]);
+    work(st + kStep, wg[1], wu[1]);
   }
-  // A lane holds rows g, g + 8 (of the 16) and tokens 2q, 2q + 1 of each block.
+  // A lane holds row g of the gate (0, 1) and of up (2, 3) for tokens 2q, 2q + 1 of each block.
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      part[warp][0][nt][2 * q + (e & 1)][g + 8 * (e >> 1)] = ag[nt][e];
-      part[warp][1][nt][2 * q + (e & 1)][g + 8 * (e >> 1)] = au[nt][e];
-    }
+    for (int e = 0; e < 4; ++e) part[warp][e >> 1][8 * nt + 2 * q + (e & 1)][g] = acc[nt][e];
   __syncthreads();
-  for (int i = threadIdx.x; i < NT * 128; i += 256) {
-    const int r = i & 15, t = i >> 4;
-    if (t >= T || f0 + r >= f) continue;
+  for (int i = threadIdx.x; i < NT * 64; i += 32 * kFewWarps) {
+    const int r = i & 7, t = i >> 3;
+    if (t >= T) continue;
     float sg = 0.f, su = 0.f;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) {
-      sg += part[w][0][t >> 3][t & 7][r];
-      su += part[w][1][t >> 3][t & 7][r];
+    for (int w = 0; w < kFewWarps; ++w) {
+      sg += part[w][0][t][r];
+      su += part[w][1][t][r];
     }
     const size_t at = (size_t)t * f + f0 + r;
     if (gout != nullptr) {
@@ -443,13 +506,73 @@ ttt_status map_bf16(CUtensorMap* m, const void* base, int64_t inner, int64_t out
   return encode_tmap(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
+
+int pairs_of(int num_sms) { return std::max(1, num_sms / 2); }
+
+// Columns of f in a forward tile. The pairs take `rounds` tiles each; a k-block of a tile costs the
+// loads of its 128 rows and c columns a CTA (2·(128 + c) cycles at the 64 bytes a cycle that an SM
+// takes in; at c = 128 the 512 cycles that its products take as well), and a tile some 1500
+// cycles besides. The fewest cycles win: 777 x 1000 x 2744 takes two rounds of 80 columns instead of
+// two of 128.
+int columns_of(int tiles_m, int f, int kblocks, int num_sms) {
+  int best = kTileN / 2;
+  double least = 0;
+  for (int c = kTileN / 2; c >= 32; c -= 8) {
+    const int rounds = cdiv((int64_t)tiles_m * cdiv(f, c), pairs_of(num_sms));
+    const double cost = (double)rounds * (kblocks * 2.0 * (128 + c) + 1500);
+    if (c == kTileN / 2 || cost < least) {
+      best = c;
+      least = cost;
+    }
+  }
+  return best;
+}
+
+// DX and DW: whole tiles in full rounds, and the sums of the tiles left cut so that their parts make
+// at most one more (4096 tokens, d 2560, f 9728: DX's 160 tiles take 2 rounds and a sixth of one
+// instead of 3).
+void plan_parts(FfnArgs& a, int total_k, int num_sms) {
+  const int tiles = a.tiles_m * a.tiles_n, pairs = pairs_of(num_sms), rest = tiles % pairs;
+  a.whole = tiles;
+  a.splits = 1;
+  a.per_split = total_k;
+  if (rest == 0) return;
+  const int splits = std::min(pairs / rest, total_k / 8);
+  if (splits < 2) return;
+  a.per_split = cdiv(total_k, splits);
+  a.splits = cdiv(total_k, a.per_split);  // none empty
+  a.whole = tiles - rest;
+}
+
+void plan_dx(FfnArgs& a, int64_t T, int d, int f, int num_sms) {
+  a.M = (int)T;
+  a.N = d;
+  a.kblocks = cdiv(f, FK);
+  a.tiles_m = cdiv(T, kTileM);
+  a.tiles_n = cdiv(d, kTileN);
+  plan_parts(a, 2 * a.kblocks, num_sms);
+}
+
+void plan_dw(FfnArgs& a, int64_t T, int d, int f, int num_sms) {
+  a.M = f;
+  a.N = d;
+  a.kblocks = cdiv(T, FK);
+  a.tiles_m = 2 * cdiv(f, kTileM);
+  a.tiles_n = cdiv(d, kTileN);
+  plan_parts(a, a.kblocks, num_sms);
+}
+
+size_t part_bytes(const FfnArgs& a) {
+  return (size_t)(a.tiles_m * a.tiles_n - a.whole) * a.splits * kTileM * kTileN * sizeof(float);
+}
+
 template <int MODE>
 ttt_status launch_pair(const CUtensorMap& A0, const CUtensorMap& A1, const CUtensorMap& B0, const CUtensorMap& B1, FfnArgs& a,
                        int num_sms, cudaStream_t s) {
   TTT_CUDA(cudaFuncSetAttribute(k_ffn_pair<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kFfnSmem));
-  const int64_t tiles = (int64_t)a.tiles_m * a.tiles_n * a.splits;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * (unsigned)std::min<int64_t>(tiles, std::max(1, num_sms / 2)));
+  cfg.gridDim = dim3(2 * (unsigned)std::min(units_of(a), pairs_of(num_sms)));
   cfg.blockDim = dim3(kFThreads);
   cfg.dynamicSmemBytes = kFfnSmem;
   cfg.stream = s;
@@ -461,16 +584,12 @@ ttt_status launch_pair(const CUtensorMap& A0, const CUtensorMap& A1, const CUten
   cfg.attrs = &at;
   cfg.numAttrs = 1;
   TTT_CUDA(cudaLaunchKernelEx(&cfg, k_ffn_pair<MODE>, A0, A1, B0, B1, a));
+  const int rest = a.tiles_m * a.tiles_n - a.whole;
+  if (MODE != FWD && rest > 0) {
+    k_ffn_join<MODE><<<dim3(kTileM / 8, rest), 256, 0, s>>>(a);
+    TTT_CUDA(cudaGetLastError());
+  }
   return TTT_OK;
-}
-
-int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
-
-// Parts of dX's sum: as many as give every SM pair a tile, each of at least 16 k-blocks.
-int dx_splits(int64_t T, int d, int f, int num_sms) {
-  const int64_t tiles = (int64_t)cdiv(T, kTileM) * cdiv(d, kTileN), pairs = std::max(1, num_sms / 2);
-  const int64_t kb = 2 * (int64_t)cdiv(f, FK);
-  return (int)std::max<int64_t>(1, std::min<int64_t>(pairs / std::max<int64_t>(1, tiles), kb / 16));
 }
 
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
@@ -483,27 +602,29 @@ ttt_status gated_ffn(const void* X, const void* Wg, const void* Wu, int64_t T, i
                       *wu = static_cast<const __nv_bfloat16*>(Wu);
   __nv_bfloat16 *z = static_cast<__nv_bfloat16*>(Z), *g = static_cast<__nv_bfloat16*>(G), *u = static_cast<__nv_bfloat16*>(U);
   if (T <= 32) {
-    const int grid = cdiv(f, 16);
+    const int grid = f / 8, threads = 32 * kFewWarps;
     if (T <= 8)
-      k_ffn_few<1><<<grid, 256, 0, s>>>(x, wg, wu, (int)T, d, f, act, z, g, u);
+      k_ffn_few<1><<<grid, threads, 0, s>>>(x, wg, wu, (int)T, d, f, act, z, g, u);
     else if (T <= 16)
-      k_ffn_few<2><<<grid, 256, 0, s>>>(x, wg, wu, (int)T, d, f, act, z, g, u);
+      k_ffn_few<2><<<grid, threads, 0, s>>>(x, wg, wu, (int)T, d, f, act, z, g, u);
     else
-      k_ffn_few<4><<<grid, 256, 0, s>>>(x, wg, wu, (int)T, d, f, act, z, g, u);
+      k_ffn_few<4><<<grid, threads, 0, s>>>(x, wg, wu, (int)T, d, f, act, z, g, u);
     TTT_CUDA(cudaGetLastError());
     return TTT_OK;
   }
-  CUtensorMap tx, tg, tu;
-  TTT_TRY(map_bf16(&tx, X, d, T, FK, FM));
-  TTT_TRY(map_bf16(&tg, Wg, d, f, FK, FM));
-  TTT_TRY(map_bf16(&tu, Wu, d, f, FK, FM));
   FfnArgs a = {};
   a.M = (int)T;
   a.N = f;
   a.kblocks = cdiv(d, FK);
   a.tiles_m = cdiv(T, kTileM);
-  a.tiles_n = cdiv(f, kTileN / 2);
+  a.cols = columns_of(a.tiles_m, f, a.kblocks, num_sms);
+  a.tiles_n = cdiv(f, a.cols);
+  a.whole = a.tiles_m * a.tiles_n;
   a.splits = 1;
+  CUtensorMap tx, tg, tu;
+  TTT_TRY(map_bf16(&tx, X, d, T, FK, FM));
+  TTT_TRY(map_bf16(&tg, Wg, d, f, FK, a.cols));
+  TTT_TRY(map_bf16(&tu, Wu, d, f, FK, a.cols));
   a.per_split = a.kblocks;
   a.act = act;
   a.z = z;
@@ -514,8 +635,10 @@ ttt_status gated_ffn(const void* X, const void* Wg, const void* Wu, int64_t T, i
 }
 
 size_t gated_ffn_backward_workspace(int64_t T, int d, int f, int num_sms) {
-  const int splits = dx_splits(T, d, f, num_sms);
-  return 2 * round256((size_t)T * f * 2) + (splits > 1 ? (size_t)splits * T * d * 4 : 0);
+  FfnArgs x = {}, w = {};
+  plan_dx(x, T, d, f, num_sms);
+  plan_dw(w, T, d, f, num_sms);
+  return 2 * round256((size_t)T * f * 2) + std::max(part_bytes(x), part_bytes(w));
 }
 
 ttt_status gated_ffn_backward(const void* dZ, const void* X, const void* Wg, const void* Wu, const void* G, const void* U,
@@ -536,40 +659,22 @@ ttt_status gated_ffn_backward(const void* dZ, const void* X, const void* Wg, con
   TTT_CUDA(cudaGetLastError());
   FfnArgs a = {};
   a.status = DevStatus{status, kWaitLimitNs};
+  a.part = part;
   CUtensorMap A0, A1, B0, B1;
   if (dX != nullptr) {
     TTT_TRY(map_bf16(&A0, dg, f, T, FK, FM));
     TTT_TRY(map_bf16(&A1, du, f, T, FK, FM));
     TTT_TRY(map_bf16(&B0, Wg, d, f, 64, FK));
     TTT_TRY(map_bf16(&B1, Wu, d, f, 64, FK));
-    a.M = (int)T;
-    a.N = d;
-    a.kblocks = cdiv(f, FK);
-    a.tiles_m = cdiv(T, kTileM);
-    a.tiles_n = cdiv(d, kTileN);
-    a.splits = dx_splits(T, d, f, num_sms);
-    a.per_split = cdiv(2 * a.kblocks, a.splits);
-    a.splits = cdiv(2 * a.kblocks, a.per_split);  // none empty
+    plan_dx(a, T, d, f, num_sms);
     a.z = static_cast<__nv_bfloat16*>(dX);
-    a.part = part;
     TTT_TRY(launch_pair<DX>(A0, A1, B0, B1, a, num_sms, s));
-    if (a.splits > 1) {
-      const size_t nx = (size_t)T * d;
-      k_ffn_join<<<(unsigned)((nx / 8 + 255) / 256), 256, 0, s>>>(part, a.splits, nx, a.z);
-      TTT_CUDA(cudaGetLastError());
-    }
   }
   if (dWg != nullptr) {
     TTT_TRY(map_bf16(&A0, dg, f, T, 64, FK));
     TTT_TRY(map_bf16(&A1, du, f, T, 64, FK));
     TTT_TRY(map_bf16(&B0, X, d, T, 64, FK));
-    a.M = f;
-    a.N = d;
-    a.kblocks = cdiv(T, FK);
-    a.tiles_m = 2 * cdiv(f, kTileM);
-    a.tiles_n = cdiv(d, kTileN);
-    a.splits = 1;
-    a.per_split = a.kblocks;
+    plan_dw(a, T, d, f, num_sms);
     a.g = static_cast<__nv_bfloat16*>(dWg);
     a.u = static_cast<__nv_bfloat16*>(dWu);
     TTT_TRY(launch_pair<DW>(A0, A1, B0, B0, a, num_sms, s));
