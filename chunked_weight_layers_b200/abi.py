@@ -152,9 +152,9 @@ _SIGNATURES = {
     "ttt_qk_norm_rope_backward": (_st, [_vp] * 14 + [_sz, _vp]),
     "ttt_rope_frequencies": (_st, [_i32, ctypes.c_double, _i32, ctypes.c_double, ctypes.c_double, ctypes.c_double,
                                    ctypes.c_double, _vp, _vp]),
-    "ttt_gated_scan": (_st, [_vp] * 9 + [_sz, _vp]),
+    "ttt_gated_scan": (_st, [_vp] * 9 + [_sz, _vp, _vp]),
     "ttt_gated_scan_workspace": (_sz, [_vp]),
-    "ttt_gated_scan_backward": (_st, [_vp] * 14 + [_sz, _vp]),
+    "ttt_gated_scan_backward": (_st, [_vp] * 14 + [_sz, _vp, _vp]),
     "ttt_gated_scan_backward_workspace": (_sz, [_vp]),
     "ttt_gated_scan_step": (_st, [_vp] * 8),
     "ttt_gated_ffn": (_st, [_vp, _vp, _vp, _i64, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp]),

@@ -29,7 +29,9 @@
 // segment runs from its own start.
 #include <algorithm>
 
+#include "f32x2.cuh"
 #include "internal.h"
+#include "tc_common.cuh"
 #include "warp_mma.cuh"
 
 namespace ttt {
@@ -65,6 +67,7 @@ struct GsArgs {
   __nv_bfloat16* ckpt;                // state before every chunk, as two bf16 planes [pairs][nchunk][2][64][64]
   __nv_bfloat16 *dq, *dk, *dv;        // dense [pairs][T][64]
   float* dg;                          // dense [pairs][T]
+  DevStatus status;
 };
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -240,184 +243,552 @@ __global__ void __launch_bounds__(128, 4) k_gs_state(const GsArgs a) {
 }
 
 // The states the segments start from, in place of what they add: start[s + 1] =
-// 2^decay[s]·start[s] + local[s], from `first` (or zero); REV: start[s − 1] from start[s].
-// grid (pairs, 64·64 / 4 / 128), one float4 a thread.
+// 2^decay[s]·start[s] + local[s], from `first` (or zero); REV: start[s − 1] from start[s]. One element
+// a thread, 16 segments' loads in flight. grid (pairs, 64·64 / 128).
 template <bool REV>
 __global__ void __launch_bounds__(128) k_gs_combine(float* local, const float* __restrict__ decay,
                                                     const float* __restrict__ first, int nseg) {
-  const int at = (blockIdx.y * 128 + threadIdx.x) * 4;
+  constexpr int kAhead = 16;
+  const int at = blockIdx.y * 128 + threadIdx.x;
   const size_t pair = blockIdx.x;
-  float4 s = first != nullptr ? *reinterpret_cast<const float4*>(first + pair * kState + at) : make_float4(0.f, 0.f, 0.f, 0.f);
+  float s = first != nullptr ? first[pair * kState + at] : 0.f;
   float* p = local + pair * nseg * kState + at;
   const float* d = decay + pair * nseg;
-#pragma unroll 4
-  for (int i = 0; i < nseg; ++i) {
-    const int seg = REV ? nseg - 1 - i : i;
-    float4* at_seg = reinterpret_cast<float4*>(p + (size_t)seg * kState);
-    const float4 x = *at_seg;
-    const float f = exp2_fast(d[seg]);
-    *at_seg = s;
-    s.x = fmaf(f, s.x, x.x);
-    s.y = fmaf(f, s.y, x.y);
-    s.z = fmaf(f, s.z, x.z);
-    s.w = fmaf(f, s.w, x.w);
+  for (int i0 = 0; i0 < nseg; i0 += kAhead) {
+    float x[kAhead], f[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int seg = REV ? nseg - 1 - (i0 + i) : i0 + i;
+      const bool in = i0 + i < nseg;
+      x[i] = in ? p[(size_t)seg * kState] : 0.f;
+      f[i] = in ? d[seg] : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int seg = REV ? nseg - 1 - (i0 + i) : i0 + i;
+      if (i0 + i < nseg) p[(size_t)seg * kState] = s;
+      s = fmaf(exp2_fast(f[i]), s, x[i]);
+    }
   }
 }
 
-// ---- forward -------------------------------------------------------------------------------
+// ---- tensor-core (tcgen05) chunks of 128 tokens ------------------------------------------------
 
-struct __align__(1024) OutSmem {
-  uint8_t Q[2][kTile], K[2][kTile], V[2][kTile];
-  uint8_t S[2][kTile];  // bf16 copy of the state before the chunk
-  float b[4][kC];
+constexpr int kL = 128;                   // tokens per chunk
+constexpr int kLTile = kL * 128;          // bytes of a [128][64] bf16 tile with 128-byte rows
+
+// A chunk's gates, made by one warp a chunk ahead. Every decay is the sum of the gates it spans,
+// never a difference of longer sums, except within a block of 32 tokens.
+struct __align__(16) Gates {
+  float b[kL];    // sum from the chunk's start up to and with token t
+  float end[kL];  // 2^(sum of the gates after t to the end of t's block of 32)
+  float w[kL];    // 2^(sum of the gates after t to the chunk's end)
+  float total;    // sum of all
 };
 
-// 128 threads; warp w holds rows 16w .. 16w + 15 of the state and of each chunk's outputs.
+struct GateRegs {
+  float x[4];  // raw gates of tokens 4·lane .. + 3
+};
+
+__device__ __forceinline__ GateRegs fetch_gates(const GsArgs& a, const float* gp, int64_t t0, int lane) {
+  GateRegs r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t t = t0 + 4 * lane + i;
+    r.x[i] = t < a.T ? gp[t * a.gt] : 0.f;
+  }
+  return r;
+}
+
+__device__ __forceinline__ void make_gates(const GateRegs& r, Gates& s, int lane) {
+  float x[4], pre[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[i] = r.x[i] * kLog2e;
+    x[i] = x[i] < kMinGate ? kMinGate : x[i];  // NaN stays
+  }
+  pre[0] = x[0];
+#pragma unroll
+  for (int i = 1; i < 4; ++i) pre[i] = pre[i - 1] + x[i];
+  const float mine = pre[3];
+  float up = mine, down = mine, seg = mine;  // inclusive sums over the lanes before, after, after in the block of eight
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const float u = __shfl_up_sync(0xffffffffu, up, o), d = __shfl_down_sync(0xffffffffu, down, o);
+    if (lane >= o) up += u;
+    if (lane + o < 32) down += d;
+    if (o < 8) {
+      const float e = __shfl_down_sync(0xffffffffu, seg, o);
+      if ((lane & 7) + o < 8) seg += e;
+    }
+  }
+  const float before = lane == 0 ? 0.f : up - mine;
+  // Sums of what comes after this lane, without the lane's own (a subtraction would cancel).
+  float after = __shfl_down_sync(0xffffffffu, down, 1), after8 = __shfl_down_sync(0xffffffffu, seg, 1);
+  if (lane == 31) after = 0.f;
+  if ((lane & 7) == 7) after8 = 0.f;
+  const float prev = __shfl_up_sync(0xffffffffu, up, 1);
+  (void)before;
+  const float base = lane == 0 ? 0.f : prev;
+  float suf = 0.f;
+#pragma unroll
+  for (int i = 3; i >= 0; --i) {
+    s.b[4 * lane + i] = base + pre[i];
+    s.w[4 * lane + i] = exp2_fast(after + suf);
+    s.end[4 * lane + i] = exp2_fast(after8 + suf);
+    suf += x[i];
+  }
+  if (lane == 31) s.total = up;
+}
+
+// x ⊙ w (two values) as two bf16 terms: the product rounded, and what the rounding left.
+__device__ __forceinline__ void weigh(uint32_t x, F2 w, uint32_t& hi, uint32_t& lo) {
+  const F2 p = mul(from_bf16(x), w);
+  hi = to_bf16(p);
+  lo = to_bf16(fma2(from_bf16(hi), f2(-1.f, -1.f), p));
+}
+
+// Token t's row of X (a [128][64] tile), weighted by w, as two bf16 terms into the rows of hi and lo.
+__device__ __forceinline__ void weigh_row(const uint8_t* X, uint8_t* hi, uint8_t* lo, int t, float w) {
+  const F2 ww = f2(w, w);
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    const uint32_t at = t * 128 + ((c ^ (t & 7)) << 4);
+    const uint4 x = *reinterpret_cast<const uint4*>(X + at);
+    uint4 h, l;
+    weigh(x.x, ww, h.x, l.x);
+    weigh(x.y, ww, h.y, l.y);
+    weigh(x.z, ww, h.z, l.z);
+    weigh(x.w, ww, h.w, l.w);
+    *reinterpret_cast<uint4*>(hi + at) = h;
+    *reinterpret_cast<uint4*>(lo + at) = l;
+  }
+}
+
+// [XW_hi | XW_lo]ᵀ·Y over 128 tokens into 64 TMEM columns: rows 0 .. 63 the first term's sums, 64 .. 127
+// the second's. Both operands MN-major; the two terms' tiles lie kLTile apart.
+__device__ __forceinline__ void outer_mma(uint32_t tmem_d, uint32_t xw, uint32_t y) {
+  constexpr uint32_t idesc = tc::idesc_bf16(128, 64, 1, 1);
+#pragma unroll
+  for (int kk = 0; kk < kL / 16; ++kk)
+    tc::mma(tmem_d, tc::smem_desc(xw + kk * 2048, kLTile, 1024), tc::smem_desc(y + kk * 2048, kLTile, 1024), idesc, kk != 0);
+}
+
+__device__ __forceinline__ void group_sync(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
+
+// The state's update from the sums that outer_mma left in TMEM, by a group of four warps: the lanes of
+// the second term hand theirs over through `swap` (16 KB), those of the first keep one row of S each (32
+// pairs): S ← keep·S + both.
+__device__ __forceinline__ void update_state(F2 (&S)[32], uint32_t tmem, uint8_t* swap, int row, float keep, int bar) {
+  const bool second = row >= 64;
+  const int r = row & 63;
+  uint4* at = reinterpret_cast<uint4*>(swap + r * 256);
+  uint32_t d[32];
+  if (second) {
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      tc::ld32(tmem + 32 * half, d);
+      tc::wait_ld();
+#pragma unroll
+      for (int c = 0; c < 8; ++c) at[(8 * half + c) ^ (r & 7)] = make_uint4(d[4 * c], d[4 * c + 1], d[4 * c + 2], d[4 * c + 3]);
+    }
+  }
+  group_sync(bar);
+  if (!second) {
+    const F2 k = f2(keep, keep);
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      tc::ld32(tmem + 32 * half, d);
+      tc::wait_ld();
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const uint4 x = at[(8 * half + c) ^ (r & 7)];
+        const int i = 16 * half + 2 * c;
+        S[i] = fma2(k, S[i], add(f2u(d[4 * c], d[4 * c + 1]), f2u(x.x, x.y)));
+        S[i + 1] = fma2(k, S[i + 1], add(f2u(d[4 * c + 2], d[4 * c + 3]), f2u(x.z, x.w)));
+      }
+    }
+  }
+}
+
+// One row of a state between registers and global memory (null: zeros).
+__device__ __forceinline__ void load_row(F2 (&S)[32], const float* p) {
+#pragma unroll
+  for (int c = 0; c < 16; ++c) {
+    const float4 x = p != nullptr ? reinterpret_cast<const float4*>(p)[c] : make_float4(0.f, 0.f, 0.f, 0.f);
+    S[2 * c] = f2(x.x, x.y);
+    S[2 * c + 1] = f2(x.z, x.w);
+  }
+}
+
+__device__ __forceinline__ void store_row(const F2 (&S)[32], float* p) {
+#pragma unroll
+  for (int c = 0; c < 16; ++c) {
+    const float2 x = split(S[2 * c]), y = split(S[2 * c + 1]);
+    reinterpret_cast<float4*>(p)[c] = make_float4(x.x, x.y, y.x, y.y);
+  }
+}
+
+// Row r of a state, rounded to bf16, into a [64][64] tile.
+__device__ __forceinline__ void put_state_row(uint8_t* tile, const F2 (&S)[32], int r) {
+#pragma unroll
+  for (int c = 0; c < 8; ++c)
+    *reinterpret_cast<uint4*>(tile + r * 128 + ((c ^ (r & 7)) << 4)) =
+        make_uint4(to_bf16(S[4 * c]), to_bf16(S[4 * c + 1]), to_bf16(S[4 * c + 2]), to_bf16(S[4 * c + 3]));
+}
+
+// TMA copies of a [128 tokens][64] tile of one (sequence, head): rows past the last token read as
+// zeros and are not written.
+__device__ __forceinline__ void tma_load_tile(void* dst, const CUtensorMap* map, uint64_t* bar, int t, int h, int b) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(0), "r"(t), "r"(h), "r"(b)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_store_tile(const CUtensorMap* map, const void* src, int t, int h, int b) {
+  asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%2, %3, %4, %5}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(smem_u32(src)), "r"(0), "r"(t), "r"(h), "r"(b)
+               : "memory");
+}
+
+// A tensor map of [batch, heads, tokens, 64] rows, and where its (sequence, head) coordinates count (a
+// dimension with stride 0 is one element for the map).
+struct Tiles {
+  CUtensorMap map;
+  int head, batch;  // 0 or 1: factors of the coordinates
+};
+
+// After a wait that ran out, copies may still be on their way into this CTA's shared memory: 50 us, far
+// beyond the latency of a TMA load, before it may exit.
+__device__ __forceinline__ void let_land(const volatile int* abort) {
+  if (*abort) {
+    const uint64_t t0 = globaltimer();
+    while (globaltimer() - t0 < 50000) __nanosleep(1000);
+  }
+}
+
+struct __align__(1024) SegSmem {
+  uint8_t X[2][kLTile], Y[2][kLTile];
+  uint8_t W[2][kLTile];  // the weighted X, two terms
+  Gates gates[2];
+  uint64_t full[2], done;
+  uint32_t tmem;
+  int abort;
+};
+
+// Runs the state alone over a segment. Forward: X = K, Y = V, weights w; REV: from the last chunk to
+// the first, X = Q, Y = dO, weights scale·2^b. 128 threads; threads 0 .. 63 hold a row of the state each.
+// CKPT: writes the state before every chunk, as two bf16 planes (forward). grid: pairs · nseg.
+template <bool REV, bool CKPT>
+__global__ void __launch_bounds__(128, 2)
+    k_gs_segment(const __grid_constant__ Tiles tx, const __grid_constant__ Tiles ty, const GsArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  SegSmem& sm = *reinterpret_cast<SegSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int pair = blockIdx.x / a.nseg, seg = blockIdx.x % a.nseg;
+  if (!CKPT && seg == (REV ? 0 : a.nseg - 1)) return;  // no segment starts from what this one adds
+  const int bi = pair / a.heads, hi_ = pair % a.heads;
+  const float* gp = a.g + bi * a.gb + hi_ * a.gh;
+  const int c0 = seg * a.per_seg, c1 = min(a.nchunk, c0 + a.per_seg), n = c1 - c0;
+  auto chunk_of = [&](int i) { return REV ? c1 - 1 - i : c0 + i; };
+  auto load = [&](int i) {
+    uint64_t* bar = &sm.full[i & 1];
+    mbar_arrive_expect_tx(bar, 2 * kLTile);
+    tma_load_tile(sm.X[i & 1], &tx.map, bar, chunk_of(i) * kL, hi_ * tx.head, bi * tx.batch);
+    tma_load_tile(sm.Y[i & 1], &ty.map, bar, chunk_of(i) * kL, hi_ * ty.head, bi * ty.batch);
+  };
+  if (tid == 0) {
+    mbar_init(&sm.full[0], 1);
+    mbar_init(&sm.full[1], 1);
+    mbar_init(&sm.done, 1);
+    sm.abort = 0;
+    fence_barrier_init();
+    load(0);
+    if (n > 1) load(1);
+  }
+  if (warp == 0) tc::alloc(&sm.tmem, 64);
+  GateRegs raw;
+  if (warp == 3) {
+    make_gates(fetch_gates(a, gp, (int64_t)chunk_of(0) * kL, lane), sm.gates[0], lane);
+    if (n > 1) raw = fetch_gates(a, gp, (int64_t)chunk_of(1) * kL, lane);
+  }
+  F2 S[32];
+  if (tid < 64) load_row(S, a.start != nullptr ? a.start + ((size_t)blockIdx.x * kD + tid) * kD : nullptr);
+  float decay = 0.f;
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = sm.tmem + ((uint32_t)(warp * 32) << 16);
+  for (int i = 0; i < n; ++i) {
+    const int ph = i & 1;
+    const Gates& gt = sm.gates[ph];
+    const float w = REV ? a.scale * exp2_fast(gt.b[tid]) : gt.w[tid];
+    mbar_wait(&sm.full[ph], (i >> 1) & 1, a.status, &sm.abort);
+    weigh_row(sm.X[ph], sm.W[0], sm.W[1], tid, w);
+    fence_proxy_async_smem();
+    tc::fence_before();
+    __syncthreads();
+    if (tid == 0) {
+      tc::fence_after();
+      outer_mma(sm.tmem, smem_u32(sm.W[0]), smem_u32(sm.Y[ph]));
+      tc::commit(&sm.done);
+    }
+    if (warp == 3 && i + 1 < n) {
+      make_gates(raw, sm.gates[ph ^ 1], lane);
+      if (i + 2 < n) raw = fetch_gates(a, gp, (int64_t)chunk_of(i + 2) * kL, lane);
+    }
+    if (CKPT && tid < 64) {
+      __nv_bfloat16* p = a.ckpt + ((size_t)pair * a.nchunk + chunk_of(i)) * 2 * kState + tid * kD;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        uint32_t h[4], l[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          h[e] = to_bf16(S[4 * c + e]);
+          l[e] = to_bf16(fma2(from_bf16(h[e]), f2(-1.f, -1.f), S[4 * c + e]));
+        }
+        reinterpret_cast<uint4*>(p)[c] = make_uint4(h[0], h[1], h[2], h[3]);
+        reinterpret_cast<uint4*>(p + kState)[c] = make_uint4(l[0], l[1], l[2], l[3]);
+      }
+    }
+    mbar_wait(&sm.done, ph, a.status, &sm.abort);
+    tc::fence_after();
+    if (tid == 0 && i + 2 < n) load(i + 2);  // X and Y of this chunk have been read
+    update_state(S, tmem, sm.W[1], tid, exp2_fast(gt.total), 1);
+    decay += gt.total;
+    tc::fence_before();
+    __syncthreads();
+  }
+  if (a.local != nullptr) {
+    if (tid < 64) store_row(S, a.local + ((size_t)blockIdx.x * kD + tid) * kD);
+    if (tid == 0) a.seg_decay[blockIdx.x] = decay;
+  }
+  tc::fence_after();
+  if (warp == 0) {
+    let_land(&sm.abort);
+    __syncwarp();
+    tc::dealloc(sm.tmem, 64);
+  }
+}
+
+struct __align__(1024) OutSmem {
+  uint8_t Q[kLTile], K[kLTile];
+  uint8_t V[2][kLTile];    // a chunk's V; after its products its outputs on their way out
+  uint8_t W[2][kLTile];    // the weighted K, two terms
+  uint8_t S[kTile];        // bf16 copy of the state before the chunk
+  Gates gates[2];
+  uint64_t qk, v[2];             // loads
+  uint64_t scores, outs, added;  // Q·Kᵀ and Q·S; P·V; (w ⊙ K)ᵀ·V
+  uint32_t tmem;
+  int abort;
+};
+
+// TMEM columns of k_gs_out: the scores, whose first half P then takes and whose second half P·V; Q·S;
+// the state's sums.
+constexpr int kColP = 0, kColO = 64, kColQS = 128, kColD = 192, kOutCols = 256;
+
+// 256 threads, two CTAs an SM, so that one's products and loads run under the other's arithmetic.
+// Threads 0 .. 127 take a row of the chunk's outputs each: Q·Kᵀ comes from TMEM, is weighted, rounded
+// and put back as the first operand of P·V without passing through shared memory. Threads 128 .. 255
+// weigh K and carry the state (the first 64 hold a row each). Tiles come and go by TMA: the next
+// chunk's Q and K as soon as the tensor cores have read these, V into the other of two buffers.
 // grid: pairs · nseg.
-__global__ void __launch_bounds__(128, 3) k_gs_out(const GsArgs a) {
+__global__ void __launch_bounds__(256, 2)
+    k_gs_out(const __grid_constant__ Tiles tq, const __grid_constant__ Tiles tk, const __grid_constant__ Tiles tv,
+             const __grid_constant__ Tiles to, const GsArgs a) {
   extern __shared__ uint8_t smem_raw[];
   OutSmem& sm = *reinterpret_cast<OutSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, id = tid & 127;
+  const bool rows_side = tid < 128;
   const int pair = blockIdx.x / a.nseg, seg = blockIdx.x % a.nseg;
-  const int64_t bi = pair / a.heads, hi_ = pair % a.heads;
-  const __nv_bfloat16* Q = a.q.p + bi * a.q.sb + hi_ * a.q.sh;
-  const __nv_bfloat16* K = a.k.p + bi * a.k.sb + hi_ * a.k.sh;
-  const __nv_bfloat16* V = a.v.p + bi * a.v.sb + hi_ * a.v.sh;
-  __nv_bfloat16* O = a.o + bi * a.ob + hi_ * a.oh;
+  const int bi = pair / a.heads, hi_ = pair % a.heads;
   const float* gp = a.g + bi * a.gb + hi_ * a.gh;
-  const int c0 = seg * a.per_seg, c1 = min(a.nchunk, c0 + a.per_seg);
-  const int row0 = 16 * warp;
-  auto load = [&](int c) {
-    const int64_t t0 = (int64_t)c * kC;
-    load_rows<128>(smem_u32(sm.Q[c & 1]), Q, a.q.st, t0, a.T);
-    load_rows<128>(smem_u32(sm.K[c & 1]), K, a.k.st, t0, a.T);
-    load_rows<128>(smem_u32(sm.V[c & 1]), V, a.v.st, t0, a.T);
-    wm::cp_commit();
+  const int c0 = seg * a.per_seg, c1 = min(a.nchunk, c0 + a.per_seg), n = c1 - c0;
+  auto load_qk = [&](int i) {
+    mbar_arrive_expect_tx(&sm.qk, 2 * kLTile);
+    tma_load_tile(sm.Q, &tq.map, &sm.qk, (c0 + i) * kL, hi_ * tq.head, bi * tq.batch);
+    tma_load_tile(sm.K, &tk.map, &sm.qk, (c0 + i) * kL, hi_ * tk.head, bi * tk.batch);
   };
-  float S[8][4];
-  load_state(S, a.start != nullptr ? a.start + (size_t)blockIdx.x * kState : nullptr, row0, lane);
-  float g0 = 0.f, g1 = 0.f;
-  if (c0 < c1) {
-    load(c0);
-    load_gates(a, gp, (int64_t)c0 * kC, lane, g0, g1);
+  auto load_v = [&](int i) {
+    mbar_arrive_expect_tx(&sm.v[i & 1], kLTile);
+    tma_load_tile(sm.V[i & 1], &tv.map, &sm.v[i & 1], (c0 + i) * kL, hi_ * tv.head, bi * tv.batch);
+  };
+  if (tid == 128) {
+    mbar_init(&sm.qk, 1);
+    mbar_init(&sm.v[0], 1);
+    mbar_init(&sm.v[1], 1);
+    mbar_init(&sm.scores, 1);
+    mbar_init(&sm.outs, 1);
+    mbar_init(&sm.added, 1);
+    sm.abort = 0;
+    fence_barrier_init();
+    load_qk(0);
+    load_v(0);
   }
-  for (int c = c0; c < c1; ++c) {
-    const int64_t t0 = (int64_t)c * kC;
-    gate_sums(g0, g1, sm.b[warp], lane);
-    uint8_t* Ss = sm.S[c & 1];
-#pragma unroll
-    for (int nt = 0; nt < 8; ++nt)
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        *reinterpret_cast<uint32_t*>(Ss + swz128_bf16(row0 + g + 8 * h, 8 * nt + 2 * q)) =
-            pack_bf16(S[nt][2 * h], S[nt][2 * h + 1]);
-    wm::cp_wait<0>();
-    __syncthreads();  // the chunk's rows and the state's copy are visible; the other buffers are free
-    if (c + 1 < c1) {
-      load(c + 1);
-      load_gates(a, gp, t0 + kC, lane, g0, g1);
+  if (warp == 0) tc::alloc(&sm.tmem, kOutCols);
+  F2 S[32];
+  GateRegs raw;
+  if (!rows_side) {
+    if (warp == 7) {
+      make_gates(fetch_gates(a, gp, (int64_t)c0 * kL, lane), sm.gates[0], lane);
+      if (n > 1) raw = fetch_gates(a, gp, (int64_t)(c0 + 1) * kL, lane);
     }
-    const uint32_t Qs = smem_u32(sm.Q[c & 1]), Ks = smem_u32(sm.K[c & 1]), Vs = smem_u32(sm.V[c & 1]);
-    const float* b = sm.b[warp];
-    uint32_t qa[4][4];
-#pragma unroll
-    for (int ks = 0; ks < 4; ++ks) wm::frag_a(Qs, row0, 16 * ks, lane, qa[ks]);
-    const float bi0 = b[row0 + g], bi1 = b[row0 + g + 8];
-
-    // u ⊙ (Q·S).
-    float o[8][4];
-#pragma unroll
-    for (int nt = 0; nt < 8; ++nt)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[nt][e] = 0.f;
-    const uint32_t Sa = smem_u32(Ss);
-#pragma unroll
-    for (int ks = 0; ks < 4; ++ks)
-#pragma unroll
-      for (int np = 0; np < 4; ++np) {
-        uint32_t y[4];
-        wm::frag_b_t(Sa, 16 * ks, 16 * np, lane, y);
-        wm::mma(o[2 * np], qa[ks], y[0], y[1]);
-        wm::mma(o[2 * np + 1], qa[ks], y[2], y[3]);
-      }
-    const float u0 = a.scale * exp2_fast(bi0), u1 = a.scale * exp2_fast(bi1);
-#pragma unroll
-    for (int nt = 0; nt < 8; ++nt) {
-      o[nt][0] *= u0;
-      o[nt][1] *= u0;
-      o[nt][2] *= u1;
-      o[nt][3] *= u1;
-    }
-
-    // P·V over blocks of 16 keys, up to this warp's own tokens.
-#pragma unroll
-    for (int kb = 0; kb < 4; ++kb) {
-      if (kb > warp) break;
-      float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-#pragma unroll
-      for (int ks = 0; ks < 4; ++ks) {
-        uint32_t y[4];
-        wm::frag_b(Ks, 16 * kb, 16 * ks, lane, y);
-        wm::mma(s[0], qa[ks], y[0], y[1]);
-        wm::mma(s[1], qa[ks], y[2], y[3]);
-      }
-      uint32_t pa[4];
-#pragma unroll
-      for (int nt = 0; nt < 2; ++nt) {
-        const int j = 16 * kb + 8 * nt + 2 * q;
-        const float2 bj = *reinterpret_cast<const float2*>(b + j);
-        const int i0 = row0 + g;
-        const float p0 = j <= i0 ? a.scale * s[nt][0] * exp2_fast(bi0 - bj.x) : 0.f;
-        const float p1 = j + 1 <= i0 ? a.scale * s[nt][1] * exp2_fast(bi0 - bj.y) : 0.f;
-        const float p2 = j <= i0 + 8 ? a.scale * s[nt][2] * exp2_fast(bi1 - bj.x) : 0.f;
-        const float p3 = j + 1 <= i0 + 8 ? a.scale * s[nt][3] * exp2_fast(bi1 - bj.y) : 0.f;
-        pa[2 * nt] = pack_bf16(p0, p1);
-        pa[2 * nt + 1] = pack_bf16(p2, p3);
-      }
-#pragma unroll
-      for (int np = 0; np < 4; ++np) {
-        uint32_t y[4];
-        wm::frag_b_t(Vs, 16 * kb, 16 * np, lane, y);
-        wm::mma(o[2 * np], pa, y[0], y[1]);
-        wm::mma(o[2 * np + 1], pa, y[2], y[3]);
-      }
-    }
-
-    // S ← e^{b_64}·S + (w ⊙ K)ᵀ·V.
-    {
-      const float bC = b[kC - 1];
-      float w[16];
-#pragma unroll
-      for (int ks = 0; ks < 4; ++ks)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) w[4 * ks + e] = exp2_fast(bC - b[16 * ks + 2 * q + (e & 1) + 8 * (e >> 1)]);
-      const float keep = exp2_fast(bC);
-#pragma unroll
-      for (int nt = 0; nt < 8; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) S[nt][e] *= keep;
-      add_outer(S, Ks, Vs, w, row0, lane);
-    }
-
-    // Outputs through this warp's own rows of the query tile (no other warp reads them).
-    __syncwarp();
-    uint8_t* Qt = sm.Q[c & 1];
-#pragma unroll
-    for (int nt = 0; nt < 8; ++nt)
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        *reinterpret_cast<uint32_t*>(Qt + swz128_bf16(row0 + g + 8 * h, 8 * nt + 2 * q)) =
-            pack_bf16(o[nt][2 * h], o[nt][2 * h + 1]);
-    __syncwarp();
-#pragma unroll
-    for (int i = lane; i < 128; i += 32) {
-      const int r = row0 + (i >> 3), x = i & 7;
-      if (t0 + r < a.T)
-        *reinterpret_cast<uint4*>(O + (t0 + r) * a.ot + 8 * x) =
-            *reinterpret_cast<const uint4*>(Qt + r * 128 + ((x ^ (r & 7)) << 4));
+    if (id < 64) {
+      load_row(S, a.start != nullptr ? a.start + ((size_t)blockIdx.x * kD + id) * kD : nullptr);
+      put_state_row(sm.S, S, id);
     }
   }
-  if (a.end != nullptr && seg == a.nseg - 1) store_state(S, a.end + (size_t)pair * kState, row0, lane);
+  fence_proxy_async_smem();
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = sm.tmem + ((uint32_t)((warp & 3) * 32) << 16);
+
+  for (int i = 0; i < n; ++i) {
+    const int ph = i & 1;
+    const Gates& gt = sm.gates[ph];
+    if (rows_side) {
+      if (tid == 0) {
+        mbar_wait(&sm.qk, ph, a.status, &sm.abort);
+        const uint32_t q = smem_u32(sm.Q), k = smem_u32(sm.K), s = smem_u32(sm.S);
+#pragma unroll
+        for (int kk = 0; kk < kD / 16; ++kk)
+          tc::mma(sm.tmem, tc::smem_desc(q + kk * 32, 16, 1024), tc::smem_desc(k + kk * 32, 16, 1024),
+                  tc::idesc_bf16(128, 128, 0, 0), kk != 0);
+#pragma unroll
+        for (int kk = 0; kk < kD / 16; ++kk)
+          tc::mma(sm.tmem + kColQS, tc::smem_desc(q + kk * 32, 16, 1024), tc::smem_desc(s + kk * 2048, kTile, 1024),
+                  tc::idesc_bf16(128, 64, 0, 1), kk != 0);
+        tc::commit(&sm.scores);
+        if (i + 1 < n) {
+          bulk_wait_read<0>();  // the outputs two chunks back have left the buffer
+          load_v(i + 1);
+        }
+      }
+      __syncwarp();
+      const float bi_ = gt.b[id];
+      const float u = a.scale * exp2_fast(bi_);
+      mbar_wait(&sm.scores, ph, a.status, &sm.abort);
+      tc::fence_after();
+      // P over blocks of 32 keys: before this warp's own tokens the decay is a product of the key's to
+      // its block's end and the query's from there; in its own block one exponential each; none after.
+#pragma unroll 1
+      for (int jb = 0; jb < 4; ++jb) {
+        uint32_t p[16];
+        if (jb < warp) {
+          uint32_t s[32];
+          tc::ld32(tmem + 32 * jb, s);
+          const float f = a.scale * exp2_fast(bi_ - gt.b[32 * jb + 31]);
+          const F2 ff = f2(f, f);
+          tc::wait_ld();
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const ulonglong2 e = *reinterpret_cast<const ulonglong2*>(gt.end + 32 * jb + 4 * c);
+            p[2 * c] = to_bf16(mul(mul(ff, F2{e.x}), f2u(s[4 * c], s[4 * c + 1])));
+            p[2 * c + 1] = to_bf16(mul(mul(ff, F2{e.y}), f2u(s[4 * c + 2], s[4 * c + 3])));
+          }
+        } else if (jb == warp) {
+          uint32_t s[32];
+          tc::ld32(tmem + 32 * jb, s);
+          tc::wait_ld();
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const float4 bj = *reinterpret_cast<const float4*>(gt.b + 32 * jb + 4 * c);
+            const float x0 = 4 * c <= lane ? a.scale * exp2_fast(bi_ - bj.x) * __uint_as_float(s[4 * c]) : 0.f;
+            const float x1 = 4 * c + 1 <= lane ? a.scale * exp2_fast(bi_ - bj.y) * __uint_as_float(s[4 * c + 1]) : 0.f;
+            const float x2 = 4 * c + 2 <= lane ? a.scale * exp2_fast(bi_ - bj.z) * __uint_as_float(s[4 * c + 2]) : 0.f;
+            const float x3 = 4 * c + 3 <= lane ? a.scale * exp2_fast(bi_ - bj.w) * __uint_as_float(s[4 * c + 3]) : 0.f;
+            p[2 * c] = pack_bf16(x0, x1);
+            p[2 * c + 1] = pack_bf16(x2, x3);
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < 16; ++c) p[c] = 0;
+        }
+        tc::st16(tmem + kColP + 16 * jb, p);
+      }
+      tc::wait_st();
+      tc::fence_before();
+      group_sync(1);
+      if (tid == 0) {
+        tc::fence_after();
+        mbar_wait(&sm.v[ph], (i >> 1) & 1, a.status, &sm.abort);
+        const uint32_t v = smem_u32(sm.V[ph]);
+#pragma unroll
+        for (int kk = 0; kk < kL / 16; ++kk)
+          tc::mma_a_tmem(sm.tmem + kColO, sm.tmem + kColP + 8 * kk, tc::smem_desc(v + kk * 2048, kLTile, 1024),
+                         tc::idesc_bf16(128, 64, 0, 1), kk != 0);
+        tc::commit(&sm.outs);
+      }
+      __syncwarp();
+      mbar_wait(&sm.added, ph, a.status, &sm.abort);
+      mbar_wait(&sm.outs, ph, a.status, &sm.abort);  // both products of V are done: its buffer is free
+      tc::fence_after();
+      uint8_t* row = sm.V[ph] + id * 128;
+      const F2 uu = f2(u, u);
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t x[32], y[32];
+        tc::ld32(tmem + kColO + 32 * half, x);
+        tc::ld32(tmem + kColQS + 32 * half, y);
+        tc::wait_ld();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int j = 8 * c + 2 * e;
+            w[e] = to_bf16(fma2(uu, f2u(y[j], y[j + 1]), f2u(x[j], x[j + 1])));
+          }
+          *reinterpret_cast<uint4*>(row + (((4 * half + c) ^ (id & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+      fence_proxy_async_smem();
+    } else {
+      mbar_wait(&sm.qk, ph, a.status, &sm.abort);
+      weigh_row(sm.K, sm.W[0], sm.W[1], id, gt.w[id]);
+      fence_proxy_async_smem();
+      tc::fence_before();
+      group_sync(2);
+      if (id == 0) {
+        tc::fence_after();
+        mbar_wait(&sm.v[ph], (i >> 1) & 1, a.status, &sm.abort);
+        outer_mma(sm.tmem + kColD, smem_u32(sm.W[0]), smem_u32(sm.V[ph]));
+        tc::commit(&sm.added);
+      }
+      __syncwarp();
+      if (warp == 7 && i + 1 < n) {
+        make_gates(raw, sm.gates[ph ^ 1], lane);
+        if (i + 2 < n) raw = fetch_gates(a, gp, (int64_t)(c0 + i + 2) * kL, lane);
+      }
+      mbar_wait(&sm.scores, ph, a.status, &sm.abort);  // Q, K and the state's copy have been read
+      if (id == 0 && i + 1 < n) load_qk(i + 1);
+      __syncwarp();
+      mbar_wait(&sm.added, ph, a.status, &sm.abort);
+      tc::fence_after();
+      update_state(S, tmem + kColD, sm.W[1], id, exp2_fast(gt.total), 2);
+      if (id < 64) put_state_row(sm.S, S, id);
+      fence_proxy_async_smem();
+    }
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    if (tid == 0) {
+      tma_store_tile(&to.map, sm.V[ph], (c0 + i) * kL, hi_, bi);
+      bulk_commit();
+    }
+  }
+  if (a.end != nullptr && seg == a.nseg - 1 && !rows_side && id < 64) store_row(S, a.end + ((size_t)pair * kD + id) * kD);
+  if (tid == 0) bulk_wait_read<0>();
+  __syncthreads();
+  if (warp == 0) {
+    let_land(&sm.abort);
+    __syncwarp();
+    tc::dealloc(sm.tmem, kOutCols);
+  }
 }
 
 // ---- backward ------------------------------------------------------------------------------
@@ -831,16 +1202,16 @@ struct Plan {
   int nchunk, nseg, per_seg;
 };
 
-Plan plan_for(const ttt_gated_scan_desc* d, int num_sms, int per_sm) {
+Plan plan_for(const ttt_gated_scan_desc* d, int chunk, int num_sms, int per_sm) {
   Plan p;
-  p.nchunk = (int)((d->tokens + kC - 1) / kC);
+  p.nchunk = (int)((d->tokens + chunk - 1) / chunk);
   p.nseg = segments((int64_t)d->batch * d->heads, p.nchunk, num_sms * per_sm);
   p.per_seg = (p.nchunk + p.nseg - 1) / p.nseg;
   p.nseg = (p.nchunk + p.per_seg - 1) / p.per_seg;  // none empty
   return p;
 }
 
-constexpr int kOutPerSm = 3, kBwdPerSm = 2;  // resident CTAs the kernels are built for
+constexpr int kOutPerSm = 2, kBwdPerSm = 2;  // resident CTAs the kernels are built for
 
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
@@ -850,8 +1221,11 @@ ttt_status raise_smem(K* fn, size_t bytes) {
   return TTT_OK;
 }
 
+constexpr size_t kSegSmem = sizeof(SegSmem) + 1024;
 constexpr size_t kStateSmem = sizeof(StateSmem) + 1024, kOutSmem = sizeof(OutSmem) + 1024, kBwdSmem = sizeof(BwdSmem) + 1024;
 static_assert(2 * (kBwdSmem + 1024) <= 233472, "two CTAs of k_gs_bwd do not fit an SM");
+static_assert(2 * (kOutSmem + 1024) <= 233472, "two CTAs of k_gs_out do not fit an SM");
+static_assert(2 * (kSegSmem + 1024) <= 233472, "two CTAs of k_gs_segment do not fit an SM");
 
 Rows rows_of(const void* p, const ttt_strides& s) {
   return Rows{static_cast<const __nv_bfloat16*>(p), s.batch, s.head, s.token};
@@ -880,7 +1254,7 @@ ttt_status segment_starts(GsArgs a, const float* first, int64_t pairs, cudaStrea
   TTT_TRY(raise_smem(k_gs_state<REV, false>, kStateSmem));
   k_gs_state<REV, false><<<(unsigned)(pairs * a.nseg), 128, kStateSmem, s>>>(a);
   TTT_CUDA(cudaGetLastError());
-  k_gs_combine<REV><<<dim3((unsigned)pairs, kState / 4 / 128), 128, 0, s>>>(a.local, a.seg_decay, first, a.nseg);
+  k_gs_combine<REV><<<dim3((unsigned)pairs, kState / 128), 128, 0, s>>>(a.local, a.seg_decay, first, a.nseg);
   TTT_CUDA(cudaGetLastError());
   return TTT_OK;
 }
@@ -889,15 +1263,33 @@ ttt_status segment_starts(GsArgs a, const float* first, int64_t pairs, cudaStrea
 
 size_t gated_scan_workspace(const ttt_gated_scan_desc* d, bool backward, int num_sms) {
   const size_t pairs = (size_t)d->batch * d->heads;
-  const Plan p = plan_for(d, num_sms, backward ? kBwdPerSm : kOutPerSm);
+  const Plan p = plan_for(d, backward ? kC : kL, num_sms, backward ? kBwdPerSm : kOutPerSm);
   const size_t seg = p.nseg > 1 ? round256(pairs * p.nseg * kState * 4) + round256(pairs * p.nseg * 4) : 0;
   return seg + (backward ? round256(pairs * p.nchunk * 2 * kState * 2) : 0);
 }
 
+// The tensor map of [batch, heads, tokens, 64] rows in tiles of 128 tokens.
+static ttt_status tiles_of(Tiles* t, const void* p, const ttt_strides& s, const ttt_gated_scan_desc* d) {
+  const uint64_t n[3] = {(uint64_t)d->tokens, (uint64_t)d->heads, (uint64_t)d->batch};
+  const int64_t st[3] = {s.token, s.head, s.batch};
+  uint64_t dims[4] = {kD, 1, 1, 1}, strides[3];
+  for (int i = 0; i < 3; ++i) {
+    // A stride of 0 (one row for all) is a dimension of one element; its stride is then never used.
+    const bool one = st[i] == 0;
+    dims[i + 1] = one ? 1 : n[i];
+    strides[i] = one ? kD * 2 : (uint64_t)st[i] * 2;
+    if (strides[i] >= ((uint64_t)1 << 40)) return fail(TTT_ERR_UNSUPPORTED, "a stride of 2^39 elements or more");
+  }
+  t->head = s.head != 0;
+  t->batch = s.batch != 0;
+  const uint32_t box[4] = {kD, kL, 1, 1};
+  return encode_tmap(&t->map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, p, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
 ttt_status gated_scan(const ttt_gated_scan_desc* d, const void* q, const void* k, const void* v, const float* g,
-                      const float* S0, void* o, float* S_end, void* ws, int num_sms, cudaStream_t s) {
+                      const float* S0, void* o, float* S_end, void* ws, int32_t* status, int num_sms, cudaStream_t s) {
   const int64_t pairs = (int64_t)d->batch * d->heads;
-  const Plan p = plan_for(d, num_sms, kOutPerSm);
+  const Plan p = plan_for(d, kL, num_sms, kOutPerSm);
   GsArgs a = base_args(d, q, k, v, g);
   a.nchunk = p.nchunk;
   a.nseg = p.nseg;
@@ -906,30 +1298,42 @@ ttt_status gated_scan(const ttt_gated_scan_desc* d, const void* q, const void* k
   a.ob = d->o.batch;
   a.oh = d->o.head;
   a.ot = d->o.token;
+  a.status = DevStatus{status, kWaitLimitNs};
   a.start = S0;
+  Tiles tq, tk, tv, to;
+  TTT_TRY(tiles_of(&tq, q, d->q, d));
+  TTT_TRY(tiles_of(&tk, k, d->k, d));
+  TTT_TRY(tiles_of(&tv, v, d->v, d));
+  TTT_TRY(tiles_of(&to, o, d->o, d));
   if (p.nseg > 1) {
     a.local = static_cast<float*>(ws);
     a.seg_decay = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + round256((size_t)pairs * p.nseg * kState * 4));
-    TTT_TRY(segment_starts<false>(a, S0, pairs, s));
+    a.start = nullptr;
+    TTT_TRY(raise_smem(k_gs_segment<false, false>, kSegSmem));
+    k_gs_segment<false, false><<<(unsigned)(pairs * a.nseg), 128, kSegSmem, s>>>(tk, tv, a);
+    TTT_CUDA(cudaGetLastError());
+    k_gs_combine<false><<<dim3((unsigned)pairs, kState / 128), 128, 0, s>>>(a.local, a.seg_decay, S0, a.nseg);
+    TTT_CUDA(cudaGetLastError());
     a.start = a.local;
   }
   a.end = S_end;
   TTT_TRY(raise_smem(k_gs_out, kOutSmem));
-  k_gs_out<<<(unsigned)(pairs * p.nseg), 128, kOutSmem, s>>>(a);
+  k_gs_out<<<(unsigned)(pairs * p.nseg), 256, kOutSmem, s>>>(tq, tk, tv, to, a);
   TTT_CUDA(cudaGetLastError());
   return TTT_OK;
 }
 
 ttt_status gated_scan_backward(const ttt_gated_scan_desc* d, const void* dout, const void* q, const void* k,
                                const void* v, const float* g, const float* S0, const float* dS_end, void* dq, void* dk,
-                               void* dv, float* dg, float* dS0, void* ws, int num_sms, cudaStream_t s) {
+                               void* dv, float* dg, float* dS0, void* ws, int32_t* status, int num_sms, cudaStream_t s) {
   const int64_t pairs = (int64_t)d->batch * d->heads;
-  const Plan p = plan_for(d, num_sms, kBwdPerSm);
+  const Plan p = plan_for(d, kC, num_sms, kBwdPerSm);
   GsArgs a = base_args(d, q, k, v, g);
   a.nchunk = p.nchunk;
   a.nseg = p.nseg;
   a.per_seg = p.per_seg;
   a.dout = rows_of(dout, d->o);
+  a.status = DevStatus{status, kWaitLimitNs};
   uint8_t* w = static_cast<uint8_t*>(ws);
   a.ckpt = reinterpret_cast<__nv_bfloat16*>(w);
   w += round256((size_t)pairs * p.nchunk * 2 * kState * 2);

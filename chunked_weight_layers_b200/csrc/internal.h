@@ -241,10 +241,11 @@ ttt_status qk_norm_rope_backward(const ttt_qk_desc* d, const void* dqo, const vo
 size_t qk_norm_rope_workspace(const ttt_qk_desc* d, int num_sms);
 
 ttt_status gated_scan(const ttt_gated_scan_desc* d, const void* q, const void* k, const void* v, const float* g,
-                      const float* S0, void* o, float* S_end, void* ws, int num_sms, cudaStream_t s);
+                      const float* S0, void* o, float* S_end, void* ws, int32_t* status, int num_sms,
+                      cudaStream_t s);
 ttt_status gated_scan_backward(const ttt_gated_scan_desc* d, const void* dout, const void* q, const void* k,
                                const void* v, const float* g, const float* S0, const float* dS_end, void* dq, void* dk,
-                               void* dv, float* dg, float* dS0, void* ws, int num_sms, cudaStream_t s);
+                               void* dv, float* dg, float* dS0, void* ws, int32_t* status, int num_sms, cudaStream_t s);
 ttt_status gated_scan_step(const ttt_gated_scan_desc* d, const void* q, const void* k, const void* v, const float* g,
                            float* state, void* o, cudaStream_t s);
 size_t gated_scan_workspace(const ttt_gated_scan_desc* d, bool backward, int num_sms);

@@ -128,10 +128,17 @@ ttt_status check_scan(const ttt_gated_scan_desc* d) {
   if (d->batch < 1 || d->heads < 1 || d->tokens < 0)
     return fail(TTT_ERR_INVALID_ARG, "batch and heads must be positive and tokens non-negative");
   if ((int64_t)d->batch * d->heads > (1 << 24)) return fail(TTT_ERR_UNSUPPORTED, "batch times heads above 2^24");
-  if (d->tokens > ((int64_t)1 << 36)) return fail(TTT_ERR_UNSUPPORTED, "more than 2^36 tokens");
-  TTT_TRY(check_strides(d->q, 8, "q"));
-  TTT_TRY(check_strides(d->k, 8, "k"));
-  TTT_TRY(check_strides(d->v, 8, "v"));
+  if (d->tokens > ((int64_t)1 << 30)) return fail(TTT_ERR_UNSUPPORTED, "more than 2^30 tokens");
+  const struct {
+    const ttt_strides* s;
+    const char* name;
+  } in[4] = {{&d->q, "q"}, {&d->k, "k"}, {&d->v, "v"}, {&d->o, "o"}};
+  for (const auto& x : in) {
+    TTT_TRY(check_strides(*x.s, 8, x.name));
+    if (x.s->token == 0 && d->tokens > 1) return fail(TTT_ERR_UNSUPPORTED, "%s: one row for all tokens (token stride 0)", x.name);
+    for (int64_t v : {x.s->batch, x.s->head, x.s->token})
+      if (v >= (int64_t)1 << 39) return fail(TTT_ERR_UNSUPPORTED, "%s: a stride of 2^39 elements or more", x.name);
+  }
   TTT_TRY(check_strides(d->g, 1, "g"));
   return TTT_OK;
 }
@@ -288,12 +295,14 @@ extern "C" size_t ttt_gated_scan_backward_workspace(const ttt_gated_scan_desc* d
 
 extern "C" ttt_status ttt_gated_scan(const ttt_gated_scan_desc* d, const void* q, const void* k, const void* v,
                                      const float* g, const float* S0, void* o, float* S_end, void* ws, size_t ws_bytes,
-                                     ttt_stream stream) {
+                                     int32_t* status, ttt_stream stream) {
   Range range("ttt_gated_scan");
   TTT_TRY(check_scan(d));
   TTT_TRY(optional(S0, "S0"));
   TTT_TRY(optional(S_end, "S_end"));
+  TTT_TRY(check_status(status));
   if (d->tokens == 0) {
+    if (status != nullptr) TTT_CUDA(cudaMemsetAsync(status, 0, sizeof(int32_t), cs(stream)));
     const size_t bytes = (size_t)d->batch * d->heads * 64 * 64 * sizeof(float);
     if (S_end != nullptr && S0 == nullptr) TTT_CUDA(cudaMemsetAsync(S_end, 0, bytes, cs(stream)));
     if (S_end != nullptr && S0 != nullptr && S_end != S0)
@@ -306,19 +315,22 @@ extern "C" ttt_status ttt_gated_scan(const ttt_gated_scan_desc* d, const void* q
   int sms;
   TTT_TRY(need_device(&sms));
   TTT_TRY(check_workspace(ws, ws_bytes, gated_scan_workspace(d, false, sms)));
-  return gated_scan(d, q, k, v, g, S0, o, S_end, ws, sms, cs(stream));
+  if (status != nullptr) TTT_CUDA(cudaMemsetAsync(status, 0, sizeof(int32_t), cs(stream)));
+  return gated_scan(d, q, k, v, g, S0, o, S_end, ws, status, sms, cs(stream));
 }
 
 extern "C" ttt_status ttt_gated_scan_backward(const ttt_gated_scan_desc* d, const void* d_o, const void* q, const void* k,
                                               const void* v, const float* g, const float* S0, const float* dS_end, void* dq,
                                               void* dk, void* dv, float* dg, float* dS0, void* ws, size_t ws_bytes,
-                                              ttt_stream stream) {
+                                              int32_t* status, ttt_stream stream) {
   Range range("ttt_gated_scan_backward");
   TTT_TRY(check_scan(d));
   TTT_TRY(optional(S0, "S0"));
   TTT_TRY(optional(dS_end, "dS_end"));
   TTT_TRY(optional(dS0, "dS0"));
+  TTT_TRY(check_status(status));
   if (d->tokens == 0) {
+    if (status != nullptr) TTT_CUDA(cudaMemsetAsync(status, 0, sizeof(int32_t), cs(stream)));
     const size_t bytes = (size_t)d->batch * d->heads * 64 * 64 * sizeof(float);
     if (dS0 != nullptr && dS_end == nullptr) TTT_CUDA(cudaMemsetAsync(dS0, 0, bytes, cs(stream)));
     if (dS0 != nullptr && dS_end != nullptr && dS0 != dS_end)
@@ -331,11 +343,11 @@ extern "C" ttt_status ttt_gated_scan_backward(const ttt_gated_scan_desc* d, cons
   TTT_TRY(need(dk, "dk"));
   TTT_TRY(need(dv, "dv"));
   TTT_TRY(need(dg, "dg"));
-  TTT_TRY(check_strides(d->o, 8, "d_o"));
   int sms;
   TTT_TRY(need_device(&sms));
   TTT_TRY(check_workspace(ws, ws_bytes, gated_scan_workspace(d, true, sms)));
-  return gated_scan_backward(d, d_o, q, k, v, g, S0, dS_end, dq, dk, dv, dg, dS0, ws, sms, cs(stream));
+  if (status != nullptr) TTT_CUDA(cudaMemsetAsync(status, 0, sizeof(int32_t), cs(stream)));
+  return gated_scan_backward(d, d_o, q, k, v, g, S0, dS_end, dq, dk, dv, dg, dS0, ws, status, sms, cs(stream));
 }
 
 extern "C" ttt_status ttt_gated_scan_step(const ttt_gated_scan_desc* d, const void* q, const void* k, const void* v,

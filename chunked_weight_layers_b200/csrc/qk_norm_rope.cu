@@ -18,6 +18,7 @@
 #include <algorithm>
 
 #include "common.cuh"
+#include "f32x2.cuh"
 #include "internal.h"
 
 namespace ttt {
@@ -47,32 +48,9 @@ struct QkArgs {
   float* partial;  // backward: [CTAs][2][width]
 };
 
-// Two fp32 values in one 64-bit register: sm_100a multiplies and adds them in one instruction,
-// each rounded as alone. The kernels were bound by instruction issue (185 a row and warp with
-// scalar arithmetic, 34 us where the bytes need 16), so all of a row's arithmetic is in pairs.
-struct F2 {
-  unsigned long long v;
-};
-__device__ __forceinline__ F2 f2(float x, float y) {
-  F2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(x), "f"(y));
-  return r;
-}
-__device__ __forceinline__ float2 split(F2 a) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
-  return r;
-}
-__device__ __forceinline__ F2 mul(F2 a, F2 b) {
-  F2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-  F2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-  return r;
-}
+// The kernels were bound by instruction issue (185 a row and warp with scalar arithmetic, 34 us over 8
+// x 2048 tokens of 24 heads of 64, where the bytes need 16), so all of a row's arithmetic is in
+// pairs.
 
 // Eight values of a row as they lie in memory, and as four pairs. partner(): the eight values that
 // are rotated with this lane's: the other lane's, or the same with each pair swapped.

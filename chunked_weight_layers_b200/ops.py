@@ -290,16 +290,17 @@ def _scan_desc(shape, scale, q, k, v, o, g):
                                    *(abi.ttt_strides(*_strides(shape, t.stride())) for t in (q, k, v, o, g)))
 
 
-def gated_scan(q, k, v, g, *, scale=1.0, initial=None, out=None, final=None, stream=None):
+def gated_scan(q, k, v, g, *, scale=1.0, initial=None, out=None, final=None, status=None, stream=None):
     """ttt_gated_scan: S_t = e^{g_t}·S_{t-1} + k_tᵀ·v_t, o_t = scale·q_t·S_t per (sequence, head). ``q``,
     ``k``, ``v`` bf16 [batch, heads, tokens, 64] (any strides, dense rows), ``g`` fp32 [batch, heads,
     tokens] (any strides; natural logarithms, -inf forgets everything before its token). Returns
     (o, state): o in ``out`` or a new dense tensor; the state after the last token, fp32 [batch,
-    heads, 64, 64], in ``final`` (which may be ``initial``) or a new tensor."""
+    heads, 64, 64], in ``final`` (which may be ``initial``) or a new tensor. ``status`` as for
+    :func:`gated_ffn`."""
     dev = _current_device()
     raw, ctx = _place(stream, dev)
     try:
-        key = (dev, _meta(q), _meta(k), _meta(v), _meta(g), _meta(initial), _meta(out), _meta(final), scale)
+        key = (dev, _meta(q), _meta(k), _meta(v), _meta(g), _meta(initial), _meta(out), _meta(final), _meta(status), scale)
     except AttributeError:  # something that is no tensor: the checks will name it
         key = None
     plan = _scan_plans.find(key) if key is not None else None
@@ -311,6 +312,7 @@ def gated_scan(q, k, v, g, *, scale=1.0, initial=None, out=None, final=None, str
         _rows(g, "g", _F32, shape[:3], dev, last=False)
         _dense_or_none(initial, "initial", _F32, st, dev)
         _dense_or_none(final, "final", _F32, st, dev)
+        _dense_or_none(status, "status", _I32, (1,), dev)
         d = _scan_desc(shape, scale, q, k, v, out, g)
         plan = d, st, abi.load().ttt_gated_scan_workspace(ctypes.byref(d))
         if key is not None:
@@ -323,18 +325,18 @@ def gated_scan(q, k, v, g, *, scale=1.0, initial=None, out=None, final=None, str
             final = torch.empty(st, dtype=_F32, device=q.device)
         ws = _workspace(nbytes, dev)
     check(abi.load().ttt_gated_scan(ctypes.byref(d), q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), _ptr(initial),
-                                    out.data_ptr(), final.data_ptr(), _ptr(ws), nbytes, raw))
+                                    out.data_ptr(), final.data_ptr(), _ptr(ws), nbytes, _ptr(status), raw))
     return out, final
 
 
-def gated_scan_backward(do, q, k, v, g, *, scale=1.0, initial=None, dfinal=None, stream=None):
+def gated_scan_backward(do, q, k, v, g, *, scale=1.0, initial=None, dfinal=None, status=None, stream=None):
     """ttt_gated_scan_backward: (dq, dk, dv, dg, dinitial) from the gradient ``do`` of the outputs and
     ``dfinal`` of the final state (None: zero). All are dense; dinitial is None where ``initial``
     is."""
     dev = _current_device()
     raw, ctx = _place(stream, dev)
     try:
-        key = (dev, _meta(do), _meta(q), _meta(k), _meta(v), _meta(g), _meta(initial), _meta(dfinal), scale)
+        key = (dev, _meta(do), _meta(q), _meta(k), _meta(v), _meta(g), _meta(initial), _meta(dfinal), _meta(status), scale)
     except AttributeError:
         key = None
     plan = _scan_back_plans.find(key) if key is not None else None
@@ -346,6 +348,7 @@ def gated_scan_backward(do, q, k, v, g, *, scale=1.0, initial=None, dfinal=None,
         _rows(g, "g", _F32, shape[:3], dev, last=False)
         _dense_or_none(initial, "initial", _F32, st, dev)
         _dense_or_none(dfinal, "dfinal", _F32, st, dev)
+        _dense_or_none(status, "status", _I32, (1,), dev)
         d = _scan_desc(shape, scale, q, k, v, do, g)
         plan = d, abi.load().ttt_gated_scan_backward_workspace(ctypes.byref(d))
         if key is not None:
@@ -357,7 +360,7 @@ def gated_scan_backward(do, q, k, v, g, *, scale=1.0, initial=None, dfinal=None,
         ws = _workspace(nbytes, dev)
     check(abi.load().ttt_gated_scan_backward(
         ctypes.byref(d), do.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), _ptr(initial), _ptr(dfinal),
-        dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dg.data_ptr(), _ptr(di), _ptr(ws), nbytes, raw))
+        dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dg.data_ptr(), _ptr(di), _ptr(ws), nbytes, _ptr(status), raw))
     return dq, dk, dv, dg, di
 
 

@@ -511,7 +511,7 @@ typedef struct {
   int32_t batch, heads;
   int64_t tokens;
   float scale;               /* factor on the outputs, e.g. 1/√64 */
-  ttt_strides q, k, v;
+  ttt_strides q, k, v;       /* of rows; token strides not 0 (batch and head strides may be) */
   ttt_strides o;             /* the outputs; backward: their gradients */
   ttt_strides g;             /* gates: strides need no alignment */
 } ttt_gated_scan_desc;
@@ -524,10 +524,12 @@ typedef struct {
  * Writes o (device bf16) and, where not NULL, S_end (device fp32 like S0: the state after the last
  * token; may be S0 itself). tokens = 0 writes S_end = S0 (or 0) and nothing else. States and sums
  * are fp32; one factor of each product is rounded to bf16, but those that make S_end keep 16 bits
- * or more. Errors: INVALID_ARG, UNSUPPORTED (batch·heads above 2^24), CUDA. */
+ * or more. `status` (device int32 or NULL): as for ttt_target_values_noalloc. Errors: INVALID_ARG,
+ * UNSUPPORTED (batch·heads above 2^24, tokens above 2^30, row strides from 2^39 on or, for tokens, 0),
+ * CUDA. */
 ttt_status ttt_gated_scan(const ttt_gated_scan_desc* desc, const void* q, const void* k, const void* v,
                           const float* g, const float* S0, void* o, float* S_end, void* workspace,
-                          size_t workspace_bytes, ttt_stream stream);
+                          size_t workspace_bytes, int32_t* status, ttt_stream stream);
 size_t ttt_gated_scan_workspace(const ttt_gated_scan_desc* desc);
 
 /* Gradients of ttt_gated_scan. d_o (strides o) is the gradient of its outputs, dS_end (device fp32
@@ -539,7 +541,7 @@ size_t ttt_gated_scan_workspace(const ttt_gated_scan_desc* desc);
 ttt_status ttt_gated_scan_backward(const ttt_gated_scan_desc* desc, const void* d_o, const void* q, const void* k,
                                    const void* v, const float* g, const float* S0, const float* dS_end, void* dq,
                                    void* dk, void* dv, float* dg, float* dS0, void* workspace,
-                                   size_t workspace_bytes, ttt_stream stream);
+                                   size_t workspace_bytes, int32_t* status, ttt_stream stream);
 size_t ttt_gated_scan_backward_workspace(const ttt_gated_scan_desc* desc);
 
 /* One token of every sequence and head: S ← e^g·S + kᵀ·v in place (device fp32 [batch, heads, 64,

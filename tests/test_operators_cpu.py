@@ -78,20 +78,20 @@ def _scan(abi, **over):
 
 @pytest.mark.parametrize("over,status,word", [
     (dict(batch=0), 1, "batch"), (dict(heads=-1), 1, "heads"), (dict(tokens=-1), 1, "tokens"),
-    (dict(batch=1 << 20, heads=1 << 10), 2, "2^24"), (dict(tokens=1 << 40), 2, "2^36"),
+    (dict(batch=1 << 20, heads=1 << 10), 2, "2^24"), (dict(tokens=1 << 40), 2, "2^30"),
 ])
 def test_scan_sizes(lib, abi, over, status, word):
     d = _scan(abi, **over)
-    assert lib.ttt_gated_scan(ctypes.byref(d), A, A, A, A, None, A, None, None, 0, None) == status
+    assert lib.ttt_gated_scan(ctypes.byref(d), A, A, A, A, None, A, None, None, 0, None, None) == status
     assert word in _message(lib)
-    assert lib.ttt_gated_scan_backward(ctypes.byref(d), A, A, A, A, A, None, None, A, A, A, A, None, None, 0, None) == status
+    assert lib.ttt_gated_scan_backward(ctypes.byref(d), A, A, A, A, A, None, None, A, A, A, A, None, None, 0, None, None) == status
     assert lib.ttt_gated_scan_step(ctypes.byref(d), A, A, A, A, A, A, None) == status
     assert lib.ttt_gated_scan_workspace(ctypes.byref(d)) == 0
 
 
 def test_scan_pointers(lib, abi):
     d = _scan(abi)
-    call = lambda d, *a: lib.ttt_gated_scan(ctypes.byref(d), *a, None, 0, None)  # noqa: E731
+    call = lambda d, *a: lib.ttt_gated_scan(ctypes.byref(d), *a, None, 0, None, None)  # noqa: E731
     assert call(d, None, A, A, A, None, A, None) == 1 and "q must" in _message(lib)
     assert call(d, A, A, A + 2, A, None, A, None) == 1 and "v must" in _message(lib)
     assert call(d, A, A, A, None, None, A, None) == 1 and "g must" in _message(lib)
@@ -99,8 +99,10 @@ def test_scan_pointers(lib, abi):
     assert call(d, A, A, A, A, None, None, None) == 1 and "o must" in _message(lib)
     assert call(_scan(abi, o=abi.ttt_strides(0, 0, 64)), A, A, A, A, None, A, None) == 1 and "overlap" in _message(lib)
     assert call(_scan(abi, k=abi.ttt_strides(0, 0, 60)), A, A, A, A, None, A, None) == 1 and "k: strides" in _message(lib)
+    for bad, word in ((abi.ttt_strides(0, 0, 0), "token stride 0"), (abi.ttt_strides(1 << 40, 512, 64), "2^39")):
+        assert call(_scan(abi, q=bad), A, A, A, A, None, A, None) == 2 and word in _message(lib)
     assert lib.ttt_gated_scan_step(ctypes.byref(d), A, A, A, A, A, A, None) == 1 and "one token" in _message(lib)
-    assert lib.ttt_gated_scan(None, A, A, A, A, None, A, None, None, 0, None) == 1
+    assert lib.ttt_gated_scan(None, A, A, A, A, None, A, None, None, 0, None, None) == 1
 
 
 @pytest.mark.parametrize("args,status,word", [
