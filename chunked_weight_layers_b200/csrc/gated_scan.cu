@@ -63,6 +63,7 @@ struct GsArgs {
   const float* start;                 // [pairs][nseg or 1][64][64] states the segments start from, or null (zero)
   float* end;                         // final state [pairs][64][64] (the last segment's), or null
   float* local;                       // what each segment adds [pairs][nseg][64][64]
+  int few;                            // the outputs' CTAs combine `local` themselves (start: one state a pair)
   float* seg_decay;                   // sums of the segments' gates, base-2 units [pairs][nseg]
   __nv_bfloat16* ckpt;                // state before every chunk, as two bf16 planes [pairs][nchunk][2][64][64]
   __nv_bfloat16 *dq, *dk, *dv;        // dense [pairs][T][64]
@@ -286,32 +287,36 @@ struct __align__(16) Gates {
   float total;    // sum of all
 };
 
-struct GateRegs {
-  float x[4];  // raw gates of tokens 4·lane .. + 3
-};
-
-__device__ __forceinline__ GateRegs fetch_gates(const GsArgs& a, const float* gp, int64_t t0, int lane) {
-  GateRegs r;
+// Asynchronous copy of a chunk's raw gates to shared memory by one warp (zeros past T): they are asked
+// for two chunks ahead, and registers that wait for them would be stored away at once.
+__device__ __forceinline__ void fetch_gates(const GsArgs& a, const float* gp, int64_t t0, float* raw, int lane) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int64_t t = t0 + 4 * lane + i;
-    r.x[i] = t < a.T ? gp[t * a.gt] : 0.f;
+    const int64_t t = t0 + lane + 32 * i;
+    const bool ok = t < a.T;
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(raw + lane + 32 * i)), "l"(gp + (ok ? t * a.gt : 0)),
+                 "r"(ok ? 4 : 0)
+                 : "memory");
   }
-  return r;
+  wm::cp_commit();
 }
 
-__device__ __forceinline__ void make_gates(const GateRegs& r, Gates& s, int lane) {
-  float x[4], pre[4];
+// From the raw gates of the last fetch_gates of this warp.
+__device__ __forceinline__ void make_gates(const float* raw, Gates& s, int lane) {
+  wm::cp_wait<0>();
+  __syncwarp();
+  const float4 r = *reinterpret_cast<const float4*>(raw + 4 * lane);
+  float x[4] = {r.x, r.y, r.z, r.w}, pre[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    x[i] = r.x[i] * kLog2e;
+    x[i] *= kLog2e;
     x[i] = x[i] < kMinGate ? kMinGate : x[i];  // NaN stays
   }
   pre[0] = x[0];
 #pragma unroll
   for (int i = 1; i < 4; ++i) pre[i] = pre[i - 1] + x[i];
-  const float mine = pre[3];
-  float up = mine, down = mine, seg = mine;  // inclusive sums over the lanes before, after, after in the block of eight
+  // Inclusive sums over the lanes up to this one, from this one on, and from it to the end of its eight.
+  float up = pre[3], down = pre[3], seg = pre[3];
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const float u = __shfl_up_sync(0xffffffffu, up, o), d = __shfl_down_sync(0xffffffffu, down, o);
@@ -322,23 +327,24 @@ __device__ __forceinline__ void make_gates(const GateRegs& r, Gates& s, int lane
       if ((lane & 7) + o < 8) seg += e;
     }
   }
-  const float before = lane == 0 ? 0.f : up - mine;
-  // Sums of what comes after this lane, without the lane's own (a subtraction would cancel).
-  float after = __shfl_down_sync(0xffffffffu, down, 1), after8 = __shfl_down_sync(0xffffffffu, seg, 1);
+  // The neighbours' sums are those without this lane (a subtraction would cancel).
+  float base = __shfl_up_sync(0xffffffffu, up, 1), after = __shfl_down_sync(0xffffffffu, down, 1),
+        after8 = __shfl_down_sync(0xffffffffu, seg, 1);
+  if (lane == 0) base = 0.f;
   if (lane == 31) after = 0.f;
   if ((lane & 7) == 7) after8 = 0.f;
-  const float prev = __shfl_up_sync(0xffffffffu, up, 1);
-  (void)before;
-  const float base = lane == 0 ? 0.f : prev;
-  float suf = 0.f;
+  float w[4], e[4], suf = 0.f;
 #pragma unroll
   for (int i = 3; i >= 0; --i) {
-    s.b[4 * lane + i] = base + pre[i];
-    s.w[4 * lane + i] = exp2_fast(after + suf);
-    s.end[4 * lane + i] = exp2_fast(after8 + suf);
+    w[i] = exp2_fast(after + suf);
+    e[i] = exp2_fast(after8 + suf);
     suf += x[i];
   }
+  *reinterpret_cast<float4*>(s.b + 4 * lane) = make_float4(base + pre[0], base + pre[1], base + pre[2], base + pre[3]);
+  *reinterpret_cast<float4*>(s.w + 4 * lane) = make_float4(w[0], w[1], w[2], w[3]);
+  *reinterpret_cast<float4*>(s.end + 4 * lane) = make_float4(e[0], e[1], e[2], e[3]);
   if (lane == 31) s.total = up;
+  __syncwarp();  // the raw gates have been read
 }
 
 // x ⊙ w (two values) as two bf16 terms: the product rounded, and what the rounding left.
@@ -365,13 +371,31 @@ __device__ __forceinline__ void weigh_row(const uint8_t* X, uint8_t* hi, uint8_t
   }
 }
 
+// The low half of a tile's shared-memory descriptor (address and leading offset); moving along the tile
+// adds to it, and the other half (1024 bytes between groups of eight rows, 128-byte swizzle) is the same
+// for all. Building whole descriptors before every product took the issuing thread 140 cycles each.
+__device__ __forceinline__ uint32_t desc_of(const void* tile, uint32_t lbo = 16) {
+  return ((smem_u32(tile) & 0x3FFFFu) >> 4) | ((lbo >> 4) << 16);
+}
+__device__ __forceinline__ uint64_t desc_at(uint32_t low, int bytes) {
+  constexpr uint64_t high = (uint64_t)((1024u >> 4) | (1u << 14) | (2u << 29)) << 32;
+  return high | (low + (uint32_t)(bytes >> 4));
+}
+
 // [XW_hi | XW_lo]ᵀ·Y over 128 tokens into 64 TMEM columns: rows 0 .. 63 the first term's sums, 64 .. 127
-// the second's. Both operands MN-major; the two terms' tiles lie kLTile apart.
+// the second's. Both operands MN-major (xw with the distance of the two terms' tiles).
 __device__ __forceinline__ void outer_mma(uint32_t tmem_d, uint32_t xw, uint32_t y) {
-  constexpr uint32_t idesc = tc::idesc_bf16(128, 64, 1, 1);
 #pragma unroll
   for (int kk = 0; kk < kL / 16; ++kk)
-    tc::mma(tmem_d, tc::smem_desc(xw + kk * 2048, kLTile, 1024), tc::smem_desc(y + kk * 2048, kLTile, 1024), idesc, kk != 0);
+    tc::mma(tmem_d, desc_at(xw, kk * 2048), desc_at(y, kk * 2048), tc::idesc_bf16(128, 64, 1, 1), kk != 0);
+}
+
+// Of two bf16 values at columns 0 and 1: both where the row is 1 or more, the first where it is 0, none
+// before.
+__device__ __forceinline__ uint32_t causal(uint32_t pair, int row) {
+  uint32_t keep;
+  asm("bmsk.clamp.b32 %0, 0, %1;" : "=r"(keep) : "r"(max(row + 1, 0) * 16));
+  return pair & keep;
 }
 
 __device__ __forceinline__ void group_sync(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
@@ -473,21 +497,25 @@ __device__ __forceinline__ void let_land(const volatile int* abort) {
 struct __align__(1024) SegSmem {
   uint8_t X[2][kLTile], Y[2][kLTile];
   uint8_t W[2][kLTile];  // the weighted X, two terms
+  uint8_t swap[kTile];   // CKPT: the second terms' part of the state, 2^-9 of it, rounded to bf16
   Gates gates[2];
-  uint64_t full[2], done;
+  __align__(16) float raw[2][kL];
+  uint64_t full[2], done[2], taken[2];
   uint32_t tmem;
   int abort;
 };
 
 // Runs the state alone over a segment. Forward: X = K, Y = V, weights w; REV: from the last chunk to
-// the first, X = Q, Y = dO, weights scale·2^b. 128 threads; threads 0 .. 63 hold a row of the state each.
+// the first, X = Q, Y = dO, weights scale·2^b. Threads 0 .. 127 weigh a row of X each and hand the tile to
+// the tensor cores, threads 128 .. 255 add the results (two sets of TMEM columns) to a row of the state
+// each, rows 0 .. 63 the first terms' part of it and 64 .. 127 the second's, which are added at the end.
 // CKPT: writes the state before every chunk, as two bf16 planes (forward). grid: pairs · nseg.
 template <bool REV, bool CKPT>
-__global__ void __launch_bounds__(128, 2)
+__global__ void __launch_bounds__(256, 2)
     k_gs_segment(const __grid_constant__ Tiles tx, const __grid_constant__ Tiles ty, const GsArgs a) {
   extern __shared__ uint8_t smem_raw[];
   SegSmem& sm = *reinterpret_cast<SegSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, id = tid & 127;
   const int pair = blockIdx.x / a.nseg, seg = blockIdx.x % a.nseg;
   if (!CKPT && seg == (REV ? 0 : a.nseg - 1)) return;  // no segment starts from what this one adds
   const int bi = pair / a.heads, hi_ = pair % a.heads;
@@ -501,76 +529,134 @@ __global__ void __launch_bounds__(128, 2)
     tma_load_tile(sm.Y[i & 1], &ty.map, bar, chunk_of(i) * kL, hi_ * ty.head, bi * ty.batch);
   };
   if (tid == 0) {
-    mbar_init(&sm.full[0], 1);
-    mbar_init(&sm.full[1], 1);
-    mbar_init(&sm.done, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.full[i], 1);
+      mbar_init(&sm.done[i], 1);
+      mbar_init(&sm.taken[i], 128);
+    }
     sm.abort = 0;
     fence_barrier_init();
     load(0);
     if (n > 1) load(1);
   }
-  if (warp == 0) tc::alloc(&sm.tmem, 64);
-  GateRegs raw;
-  if (warp == 3) {
-    make_gates(fetch_gates(a, gp, (int64_t)chunk_of(0) * kL, lane), sm.gates[0], lane);
-    if (n > 1) raw = fetch_gates(a, gp, (int64_t)chunk_of(1) * kL, lane);
-  }
+  if (warp == 4) tc::alloc(&sm.tmem, 128);
   F2 S[32];
-  if (tid < 64) load_row(S, a.start != nullptr ? a.start + ((size_t)blockIdx.x * kD + tid) * kD : nullptr);
-  float decay = 0.f;
+  if (warp == 3) {
+    fetch_gates(a, gp, (int64_t)chunk_of(0) * kL, sm.raw[0], lane);
+    make_gates(sm.raw[0], sm.gates[0], lane);
+    if (n > 1) fetch_gates(a, gp, (int64_t)chunk_of(1) * kL, sm.raw[1], lane);
+  } else if (warp >= 4) {
+    load_row(S, a.start != nullptr && id < 64 ? a.start + ((size_t)blockIdx.x * kD + id) * kD : nullptr);
+  }
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
-  const uint32_t tmem = sm.tmem + ((uint32_t)(warp * 32) << 16);
-  for (int i = 0; i < n; ++i) {
-    const int ph = i & 1;
-    const Gates& gt = sm.gates[ph];
-    const float w = REV ? a.scale * exp2_fast(gt.b[tid]) : gt.w[tid];
-    mbar_wait(&sm.full[ph], (i >> 1) & 1, a.status, &sm.abort);
-    weigh_row(sm.X[ph], sm.W[0], sm.W[1], tid, w);
-    fence_proxy_async_smem();
-    tc::fence_before();
-    __syncthreads();
-    if (tid == 0) {
-      tc::fence_after();
-      outer_mma(sm.tmem, smem_u32(sm.W[0]), smem_u32(sm.Y[ph]));
-      tc::commit(&sm.done);
-    }
-    if (warp == 3 && i + 1 < n) {
-      make_gates(raw, sm.gates[ph ^ 1], lane);
-      if (i + 2 < n) raw = fetch_gates(a, gp, (int64_t)chunk_of(i + 2) * kL, lane);
-    }
-    if (CKPT && tid < 64) {
-      __nv_bfloat16* p = a.ckpt + ((size_t)pair * a.nchunk + chunk_of(i)) * 2 * kState + tid * kD;
-#pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        uint32_t h[4], l[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          h[e] = to_bf16(S[4 * c + e]);
-          l[e] = to_bf16(fma2(from_bf16(h[e]), f2(-1.f, -1.f), S[4 * c + e]));
-        }
-        reinterpret_cast<uint4*>(p)[c] = make_uint4(h[0], h[1], h[2], h[3]);
-        reinterpret_cast<uint4*>(p + kState)[c] = make_uint4(l[0], l[1], l[2], l[3]);
+  if (warp < 4) {
+    const uint32_t dw = desc_of(sm.W[0], kLTile), dy = desc_of(sm.Y[0]);
+    for (int i = 0; i < n; ++i) {
+      const int ph = i & 1;
+      const Gates& gt = sm.gates[ph];
+      const float w = REV ? a.scale * exp2_fast(gt.b[id]) : gt.w[id];
+      mbar_wait(&sm.full[ph], (i >> 1) & 1, a.status, &sm.abort);
+      if (i > 0) {
+        // The products of the chunk before have read W, and its X and Y.
+        mbar_wait(&sm.done[ph ^ 1], ((i - 1) >> 1) & 1, a.status, &sm.abort);
+        if (tid == 0 && i + 1 < n) load(i + 1);
+        __syncwarp();
       }
+      weigh_row(sm.X[ph], sm.W[0], sm.W[1], id, w);
+      fence_proxy_async_smem();
+      group_sync(1);
+      if (tid == 0) {
+        if (i > 1) {
+          mbar_wait(&sm.taken[ph], ((i - 2) >> 1) & 1, a.status, &sm.abort);
+          tc::fence_after();
+        }
+        outer_mma(sm.tmem + 64 * ph, dw, dy + ph * (kLTile >> 4));
+        tc::commit(&sm.done[ph]);
+      }
+      __syncwarp();
+      if (warp == 3 && i + 1 < n) {
+        // The other gates' last readers, the state's threads, have taken the chunk before.
+        if (i > 0) mbar_wait(&sm.taken[ph ^ 1], ((i - 1) >> 1) & 1, a.status, &sm.abort);
+        make_gates(sm.raw[ph ^ 1], sm.gates[ph ^ 1], lane);
+        if (i + 2 < n) fetch_gates(a, gp, (int64_t)chunk_of(i + 2) * kL, sm.raw[ph], lane);
+      }
+      group_sync(1);  // the next chunk's gates are there
     }
-    mbar_wait(&sm.done, ph, a.status, &sm.abort);
-    tc::fence_after();
-    if (tid == 0 && i + 2 < n) load(i + 2);  // X and Y of this chunk have been read
-    update_state(S, tmem, sm.W[1], tid, exp2_fast(gt.total), 1);
-    decay += gt.total;
-    tc::fence_before();
-    __syncthreads();
+  } else {
+    const uint32_t tmem = sm.tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    float decay = 0.f;
+    for (int i = 0; i < n; ++i) {
+      const int ph = i & 1;
+      if (CKPT) {
+        // Both parts of a row of the state, through shared memory, to its first part's thread.
+        if (id >= 64) put_state_row(sm.swap, S, id & 63);
+        group_sync(2);
+        if (id < 64) {
+          __nv_bfloat16* p = a.ckpt + ((size_t)pair * a.nchunk + chunk_of(i)) * 2 * kState + id * kD;
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const uint4 x = *reinterpret_cast<const uint4*>(sm.swap + id * 128 + ((c ^ (id & 7)) << 4));
+            const uint32_t second[4] = {x.x, x.y, x.z, x.w};
+            uint32_t h[4], l[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const F2 both = add(S[4 * c + e], from_bf16(second[e]));
+              h[e] = to_bf16(both);
+              l[e] = to_bf16(fma2(from_bf16(h[e]), f2(-1.f, -1.f), both));
+            }
+            reinterpret_cast<uint4*>(p)[c] = make_uint4(h[0], h[1], h[2], h[3]);
+            reinterpret_cast<uint4*>(p + kState)[c] = make_uint4(l[0], l[1], l[2], l[3]);
+          }
+        }
+        group_sync(2);
+      }
+      mbar_wait(&sm.done[ph], (i >> 1) & 1, a.status, &sm.abort);
+      tc::fence_after();
+      const float total = sm.gates[ph].total, keep = exp2_fast(total);
+      const F2 kk = f2(keep, keep);
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t d[32];
+        tc::ld32(tmem + 64 * ph + 32 * half, d);
+        tc::wait_ld();
+#pragma unroll
+        for (int c = 0; c < 16; ++c) S[16 * half + c] = fma2(kk, S[16 * half + c], f2u(d[2 * c], d[2 * c + 1]));
+      }
+      tc::fence_before();
+      mbar_arrive(&sm.taken[ph]);
+      decay += total;
+    }
+    if (a.local != nullptr) {
+      float4* at = reinterpret_cast<float4*>(sm.W[0]) + (id & 63) * 16;  // the products are done
+      if (id >= 64) {
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          const float2 x = split(S[2 * c]), y = split(S[2 * c + 1]);
+          at[c ^ (id & 7)] = make_float4(x.x, x.y, y.x, y.y);
+        }
+      }
+      group_sync(2);
+      if (id < 64) {
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          const float4 x = at[c ^ (id & 7)];
+          S[2 * c] = add(S[2 * c], f2(x.x, x.y));
+          S[2 * c + 1] = add(S[2 * c + 1], f2(x.z, x.w));
+        }
+        store_row(S, a.local + ((size_t)blockIdx.x * kD + id) * kD);
+      }
+      if (id == 0) a.seg_decay[blockIdx.x] = decay;
+    }
   }
-  if (a.local != nullptr) {
-    if (tid < 64) store_row(S, a.local + ((size_t)blockIdx.x * kD + tid) * kD);
-    if (tid == 0) a.seg_decay[blockIdx.x] = decay;
-  }
+  tc::fence_before();
+  __syncthreads();
   tc::fence_after();
-  if (warp == 0) {
+  if (warp == 4) {
     let_land(&sm.abort);
     __syncwarp();
-    tc::dealloc(sm.tmem, 64);
+    tc::dealloc(sm.tmem, 128);
   }
 }
 
@@ -580,6 +666,7 @@ struct __align__(1024) OutSmem {
   uint8_t W[2][kLTile];    // the weighted K, two terms
   uint8_t S[kTile];        // bf16 copy of the state before the chunk
   Gates gates[2];
+  __align__(16) float raw[2][kL];
   uint64_t qk, v[2];             // loads
   uint64_t scores, outs, added;  // Q·Kᵀ and Q·S; P·V; (w ⊙ K)ᵀ·V
   uint32_t tmem;
@@ -630,14 +717,30 @@ __global__ void __launch_bounds__(256, 2)
   }
   if (warp == 0) tc::alloc(&sm.tmem, kOutCols);
   F2 S[32];
-  GateRegs raw;
   if (!rows_side) {
     if (warp == 7) {
-      make_gates(fetch_gates(a, gp, (int64_t)c0 * kL, lane), sm.gates[0], lane);
-      if (n > 1) raw = fetch_gates(a, gp, (int64_t)(c0 + 1) * kL, lane);
+      fetch_gates(a, gp, (int64_t)c0 * kL, sm.raw[0], lane);
+      make_gates(sm.raw[0], sm.gates[0], lane);
+      if (n > 1) fetch_gates(a, gp, (int64_t)(c0 + 1) * kL, sm.raw[1], lane);
     }
     if (id < 64) {
-      load_row(S, a.start != nullptr ? a.start + ((size_t)blockIdx.x * kD + id) * kD : nullptr);
+      if (a.few) {
+        // Few segments: what those before this one add, in order, onto the initial state.
+        load_row(S, a.start != nullptr ? a.start + ((size_t)pair * kD + id) * kD : nullptr);
+        for (int before = 0; before < seg; ++before) {
+          const size_t at = (size_t)pair * a.nseg + before;
+          const float f = exp2_fast(a.seg_decay[at]);
+          const ulonglong2* x = reinterpret_cast<const ulonglong2*>(a.local + (at * kD + id) * kD);
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            const ulonglong2 y = x[c];
+            S[2 * c] = fma2(f2(f, f), S[2 * c], F2{y.x});
+            S[2 * c + 1] = fma2(f2(f, f), S[2 * c + 1], F2{y.y});
+          }
+        }
+      } else {
+        load_row(S, a.start != nullptr ? a.start + ((size_t)blockIdx.x * kD + id) * kD : nullptr);
+      }
       put_state_row(sm.S, S, id);
     }
   }
@@ -645,7 +748,9 @@ __global__ void __launch_bounds__(256, 2)
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
-  const uint32_t tmem = sm.tmem + ((uint32_t)((warp & 3) * 32) << 16);
+  const uint32_t tm = sm.tmem, tmem = tm + ((uint32_t)((warp & 3) * 32) << 16);
+  const uint32_t dq = desc_of(sm.Q), dk = desc_of(sm.K), dv = desc_of(sm.V[0]), ds = desc_of(sm.S),
+                 dw = desc_of(sm.W[0], kLTile);
 
   for (int i = 0; i < n; ++i) {
     const int ph = i & 1;
@@ -653,15 +758,12 @@ __global__ void __launch_bounds__(256, 2)
     if (rows_side) {
       if (tid == 0) {
         mbar_wait(&sm.qk, ph, a.status, &sm.abort);
-        const uint32_t q = smem_u32(sm.Q), k = smem_u32(sm.K), s = smem_u32(sm.S);
 #pragma unroll
         for (int kk = 0; kk < kD / 16; ++kk)
-          tc::mma(sm.tmem, tc::smem_desc(q + kk * 32, 16, 1024), tc::smem_desc(k + kk * 32, 16, 1024),
-                  tc::idesc_bf16(128, 128, 0, 0), kk != 0);
+          tc::mma(tm, desc_at(dq, kk * 32), desc_at(dk, kk * 32), tc::idesc_bf16(128, 128, 0, 0), kk != 0);
 #pragma unroll
         for (int kk = 0; kk < kD / 16; ++kk)
-          tc::mma(sm.tmem + kColQS, tc::smem_desc(q + kk * 32, 16, 1024), tc::smem_desc(s + kk * 2048, kTile, 1024),
-                  tc::idesc_bf16(128, 64, 0, 1), kk != 0);
+          tc::mma(tm + kColQS, desc_at(dq, kk * 32), desc_at(ds, kk * 2048), tc::idesc_bf16(128, 64, 0, 1), kk != 0);
         tc::commit(&sm.scores);
         if (i + 1 < n) {
           bulk_wait_read<0>();  // the outputs two chunks back have left the buffer
@@ -675,40 +777,36 @@ __global__ void __launch_bounds__(256, 2)
       tc::fence_after();
       // P over blocks of 32 keys: before this warp's own tokens the decay is a product of the key's to
       // its block's end and the query's from there; in its own block one exponential each; none after.
-#pragma unroll 1
-      for (int jb = 0; jb < 4; ++jb) {
-        uint32_t p[16];
-        if (jb < warp) {
-          uint32_t s[32];
-          tc::ld32(tmem + 32 * jb, s);
-          const float f = a.scale * exp2_fast(bi_ - gt.b[32 * jb + 31]);
-          const F2 ff = f2(f, f);
-          tc::wait_ld();
+      uint32_t sc[32], p[16];
+      tc::ld32(tmem, sc);
+      for (int jb = 0; jb < warp; ++jb) {
+        const float f = a.scale * exp2_fast(bi_ - gt.b[32 * jb + 31]);
+        const F2 ff = f2(f, f);
+        tc::wait_ld();
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            const ulonglong2 e = *reinterpret_cast<const ulonglong2*>(gt.end + 32 * jb + 4 * c);
-            p[2 * c] = to_bf16(mul(mul(ff, F2{e.x}), f2u(s[4 * c], s[4 * c + 1])));
-            p[2 * c + 1] = to_bf16(mul(mul(ff, F2{e.y}), f2u(s[4 * c + 2], s[4 * c + 3])));
-          }
-        } else if (jb == warp) {
-          uint32_t s[32];
-          tc::ld32(tmem + 32 * jb, s);
-          tc::wait_ld();
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            const float4 bj = *reinterpret_cast<const float4*>(gt.b + 32 * jb + 4 * c);
-            const float x0 = 4 * c <= lane ? a.scale * exp2_fast(bi_ - bj.x) * __uint_as_float(s[4 * c]) : 0.f;
-            const float x1 = 4 * c + 1 <= lane ? a.scale * exp2_fast(bi_ - bj.y) * __uint_as_float(s[4 * c + 1]) : 0.f;
-            const float x2 = 4 * c + 2 <= lane ? a.scale * exp2_fast(bi_ - bj.z) * __uint_as_float(s[4 * c + 2]) : 0.f;
-            const float x3 = 4 * c + 3 <= lane ? a.scale * exp2_fast(bi_ - bj.w) * __uint_as_float(s[4 * c + 3]) : 0.f;
-            p[2 * c] = pack_bf16(x0, x1);
-            p[2 * c + 1] = pack_bf16(x2, x3);
-          }
-        } else {
-#pragma unroll
-          for (int c = 0; c < 16; ++c) p[c] = 0;
+        for (int c = 0; c < 8; ++c) {
+          const ulonglong2 e = *reinterpret_cast<const ulonglong2*>(gt.end + 32 * jb + 4 * c);
+          p[2 * c] = to_bf16(mul(mul(ff, F2{e.x}), f2u(sc[4 * c], sc[4 * c + 1])));
+          p[2 * c + 1] = to_bf16(mul(mul(ff, F2{e.y}), f2u(sc[4 * c + 2], sc[4 * c + 3])));
         }
+        tc::ld32(tmem + 32 * (jb + 1), sc);
         tc::st16(tmem + kColP + 16 * jb, p);
+      }
+      {
+        const F2 bb = f2(bi_, bi_), one = f2(-1.f, -1.f), sl = f2(a.scale, a.scale);
+        tc::wait_ld();
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const ulonglong2 bj = *reinterpret_cast<const ulonglong2*>(gt.b + 32 * warp + 4 * c);
+          const float2 x = split(fma2(one, F2{bj.x}, bb)), y = split(fma2(one, F2{bj.y}, bb));
+          p[2 * c] = causal(to_bf16(mul(mul(sl, f2(exp2_fast(x.x), exp2_fast(x.y))), f2u(sc[4 * c], sc[4 * c + 1]))), lane - 4 * c);
+          p[2 * c + 1] =
+              causal(to_bf16(mul(mul(sl, f2(exp2_fast(y.x), exp2_fast(y.y))), f2u(sc[4 * c + 2], sc[4 * c + 3]))), lane - 4 * c - 2);
+        }
+        tc::st16(tmem + kColP + 16 * warp, p);
+#pragma unroll
+        for (int c = 0; c < 16; ++c) p[c] = 0;
+        for (int jb = warp + 1; jb < 4; ++jb) tc::st16(tmem + kColP + 16 * jb, p);
       }
       tc::wait_st();
       tc::fence_before();
@@ -716,11 +814,10 @@ __global__ void __launch_bounds__(256, 2)
       if (tid == 0) {
         tc::fence_after();
         mbar_wait(&sm.v[ph], (i >> 1) & 1, a.status, &sm.abort);
-        const uint32_t v = smem_u32(sm.V[ph]);
+        const uint32_t v = dv + ph * (kLTile >> 4);
 #pragma unroll
         for (int kk = 0; kk < kL / 16; ++kk)
-          tc::mma_a_tmem(sm.tmem + kColO, sm.tmem + kColP + 8 * kk, tc::smem_desc(v + kk * 2048, kLTile, 1024),
-                         tc::idesc_bf16(128, 64, 0, 1), kk != 0);
+          tc::mma_a_tmem(tm + kColO, tm + kColP + 8 * kk, desc_at(v, kk * 2048), tc::idesc_bf16(128, 64, 0, 1), kk != 0);
         tc::commit(&sm.outs);
       }
       __syncwarp();
@@ -756,13 +853,13 @@ __global__ void __launch_bounds__(256, 2)
       if (id == 0) {
         tc::fence_after();
         mbar_wait(&sm.v[ph], (i >> 1) & 1, a.status, &sm.abort);
-        outer_mma(sm.tmem + kColD, smem_u32(sm.W[0]), smem_u32(sm.V[ph]));
+        outer_mma(tm + kColD, dw, dv + ph * (kLTile >> 4));
         tc::commit(&sm.added);
       }
       __syncwarp();
       if (warp == 7 && i + 1 < n) {
-        make_gates(raw, sm.gates[ph ^ 1], lane);
-        if (i + 2 < n) raw = fetch_gates(a, gp, (int64_t)(c0 + i + 2) * kL, lane);
+        make_gates(sm.raw[ph ^ 1], sm.gates[ph ^ 1], lane);
+        if (i + 2 < n) fetch_gates(a, gp, (int64_t)(c0 + i + 2) * kL, sm.raw[ph], lane);
       }
       mbar_wait(&sm.scores, ph, a.status, &sm.abort);  // Q, K and the state's copy have been read
       if (id == 0 && i + 1 < n) load_qk(i + 1);
@@ -1213,6 +1310,10 @@ Plan plan_for(const ttt_gated_scan_desc* d, int chunk, int num_sms, int per_sm) 
 
 constexpr int kOutPerSm = 2, kBwdPerSm = 2;  // resident CTAs the kernels are built for
 
+// Up to so many segments the outputs' CTAs add up the states before theirs on their own (16 KB each from
+// L2), which saves a launch of some 8 us; beyond it one launch combines them in order.
+constexpr int kFewSegments = 8;
+
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
 template <class K>
@@ -1310,11 +1411,15 @@ ttt_status gated_scan(const ttt_gated_scan_desc* d, const void* q, const void* k
     a.seg_decay = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + round256((size_t)pairs * p.nseg * kState * 4));
     a.start = nullptr;
     TTT_TRY(raise_smem(k_gs_segment<false, false>, kSegSmem));
-    k_gs_segment<false, false><<<(unsigned)(pairs * a.nseg), 128, kSegSmem, s>>>(tk, tv, a);
+    k_gs_segment<false, false><<<(unsigned)(pairs * a.nseg), 256, kSegSmem, s>>>(tk, tv, a);
     TTT_CUDA(cudaGetLastError());
-    k_gs_combine<false><<<dim3((unsigned)pairs, kState / 128), 128, 0, s>>>(a.local, a.seg_decay, S0, a.nseg);
-    TTT_CUDA(cudaGetLastError());
-    a.start = a.local;
+    a.few = a.nseg <= kFewSegments && S_end != S0;  // with few, the last segment may write S_end before others read S0
+    a.start = S0;
+    if (!a.few) {
+      k_gs_combine<false><<<dim3((unsigned)pairs, kState / 128), 128, 0, s>>>(a.local, a.seg_decay, S0, a.nseg);
+      TTT_CUDA(cudaGetLastError());
+      a.start = a.local;
+    }
   }
   a.end = S_end;
   TTT_TRY(raise_smem(k_gs_out, kOutSmem));

@@ -196,6 +196,17 @@ def test_continued_calls_are_one_scan(cwl):
     _check_forward(torch.cat(parts, 2), state, x, 0.125)
 
 
+@pytest.mark.parametrize("T", [1024 + 5, 16 * 1024])
+def test_final_state_over_the_initial_one(cwl, T):
+    """``final`` may be ``initial`` with one, few and many segments."""
+    x = _cuda(_inputs(1, 3, T, 17))
+    o, S = cwl.gated_scan(x["q"], x["k"], x["v"], x["g"], initial=x["S0"])
+    for _ in range(3):
+        s = x["S0"].clone()
+        o2, s2 = cwl.gated_scan(x["q"], x["k"], x["v"], x["g"], initial=s, final=s)
+        assert s2 is s and torch.equal(o, o2) and torch.equal(S, s)
+
+
 @pytest.mark.parametrize("T", [1, 77])
 def test_layouts(cwl, T):
     """Token-major views, packed projections, gates [batch, tokens, heads], an output inside a larger
