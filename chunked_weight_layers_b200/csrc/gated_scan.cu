@@ -38,35 +38,30 @@ namespace ttt {
 
 namespace {
 
-constexpr int kC = 64;               // tokens per chunk
 constexpr int kD = 64;               // head width
-constexpr int kTile = kC * 128;      // bytes of a [64][64] bf16 tile
+constexpr int kTile = kD * 128;      // bytes of a [64][64] bf16 tile
 constexpr int kState = kD * kD;      // elements of a state
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kMinGate = -150.f;   // base-2 units: 2^-150 is 0 in fp32
 constexpr float kGoneGate = -104.f;  // a gate below kMinGate / kLog2e
 
-struct Rows {  // bf16 [batch, heads, tokens, 64] with strides in elements
+struct Rows {  // bf16 [batch, heads, 64], strides in elements
   const __nv_bfloat16* p;
-  int64_t sb, sh, st;
+  int64_t sb, sh;
 };
 
 struct GsArgs {
   int heads, nchunk, nseg, per_seg;  // per_seg: chunks of a segment
   int64_t T;
   float scale;
-  Rows q, k, v, dout;
   const float* g;
   int64_t gb, gh, gt;
-  __nv_bfloat16* o;                   // forward outputs
-  int64_t ob, oh, ot;
   const float* start;                 // [pairs][nseg or 1][64][64] states the segments start from, or null (zero)
   float* end;                         // final state [pairs][64][64] (the last segment's), or null
   float* local;                       // what each segment adds [pairs][nseg][64][64]
   int few;                            // the outputs' CTAs combine `local` themselves (start: one state a pair)
   float* seg_decay;                   // sums of the segments' gates, base-2 units [pairs][nseg]
   __nv_bfloat16* ckpt;                // state before every chunk, as two bf16 planes [pairs][nchunk][2][64][64]
-  __nv_bfloat16 *dq, *dk, *dv;        // dense [pairs][T][64]
   float* dg;                          // dense [pairs][T]
   DevStatus status;
 };
@@ -77,171 +72,7 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
-// Sums of a chunk's gates up to and with each token, base-2 units, into b[64] (one copy per warp;
-// the calling warp's lanes hold the raw gates of tokens lane and lane + 32).
-__device__ __forceinline__ void gate_sums(float g0, float g1, float* b, int lane) {
-  float x0 = g0 * kLog2e, x1 = g1 * kLog2e;
-  x0 = x0 < kMinGate ? kMinGate : x0;  // NaN stays
-  x1 = x1 < kMinGate ? kMinGate : x1;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const float y0 = __shfl_up_sync(0xffffffffu, x0, o), y1 = __shfl_up_sync(0xffffffffu, x1, o);
-    if (lane >= o) {
-      x0 += y0;
-      x1 += y1;
-    }
-  }
-  x1 += __shfl_sync(0xffffffffu, x0, 31);
-  __syncwarp();
-  b[lane] = x0;
-  b[lane + 32] = x1;
-  __syncwarp();
-}
-
-__device__ __forceinline__ void load_gates(const GsArgs& a, const float* gp, int64_t t0, int lane, float& g0, float& g1) {
-  g0 = t0 + lane < a.T ? gp[(t0 + lane) * a.gt] : 0.f;
-  g1 = t0 + lane + 32 < a.T ? gp[(t0 + lane + 32) * a.gt] : 0.f;
-}
-
-// Asynchronous copy of tokens t0 .. t0 + 63 of one (sequence, head) into a tile (rows past T zero).
-template <int THREADS>
-__device__ __forceinline__ void load_rows(uint32_t tile, const __nv_bfloat16* base, int64_t st, int64_t t0, int64_t T) {
-#pragma unroll
-  for (int i = threadIdx.x; i < kC * 8; i += THREADS) {
-    const int r = i >> 3, c = i & 7;
-    const bool ok = t0 + r < T;
-    wm::cp16(tile + r * 128 + ((c ^ (r & 7)) << 4), base + (ok ? (t0 + r) * st : 0) + 8 * c, ok);
-  }
-}
-
-// S += (w ⊙ X)ᵀ·Y for this warp's rows 16·warp .. +15 of S: X and Y tiles of 64 tokens, the
-// weighted X as two bf16 terms.
-__device__ __forceinline__ void add_outer(float (&S)[8][4], uint32_t X, uint32_t Y, const float (&w)[16], int row0, int lane) {
-#pragma unroll
-  for (int ks = 0; ks < 4; ++ks) {
-    uint32_t x[4], hi[4], lo[4];
-    wm::frag_a_t(X, 16 * ks, row0, lane, x);
-    // Registers 0, 1 hold tokens 16·ks + 2q, + 1 and registers 2, 3 those 8 later.
-    wm::scale_split(x[0], w[4 * ks], w[4 * ks + 1], hi[0], lo[0]);
-    wm::scale_split(x[1], w[4 * ks], w[4 * ks + 1], hi[1], lo[1]);
-    wm::scale_split(x[2], w[4 * ks + 2], w[4 * ks + 3], hi[2], lo[2]);
-    wm::scale_split(x[3], w[4 * ks + 2], w[4 * ks + 3], hi[3], lo[3]);
-#pragma unroll
-    for (int np = 0; np < 4; ++np) {
-      uint32_t y[4];
-      wm::frag_b_t(Y, 16 * ks, 16 * np, lane, y);
-      wm::mma(S[2 * np], hi, y[0], y[1]);
-      wm::mma(S[2 * np + 1], hi, y[2], y[3]);
-      wm::mma(S[2 * np], lo, y[0], y[1]);
-      wm::mma(S[2 * np + 1], lo, y[2], y[3]);
-    }
-  }
-}
-
-// A thread's part of a [64][64] fp32 state: rows row0 + g, + 8, columns 8·nt + 2q, + 1.
-__device__ __forceinline__ void load_state(float (&S)[8][4], const float* p, int row0, int lane) {
-  const int g = lane >> 2, q = lane & 3;
-#pragma unroll
-  for (int nt = 0; nt < 8; ++nt)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const float2 x = p == nullptr ? make_float2(0.f, 0.f)
-                                    : *reinterpret_cast<const float2*>(p + (row0 + g + 8 * h) * kD + 8 * nt + 2 * q);
-      S[nt][2 * h] = x.x;
-      S[nt][2 * h + 1] = x.y;
-    }
-}
-
-__device__ __forceinline__ void store_state(const float (&S)[8][4], float* p, int row0, int lane) {
-  const int g = lane >> 2, q = lane & 3;
-#pragma unroll
-  for (int nt = 0; nt < 8; ++nt)
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      *reinterpret_cast<float2*>(p + (row0 + g + 8 * h) * kD + 8 * nt + 2 * q) = make_float2(S[nt][2 * h], S[nt][2 * h + 1]);
-}
-
 // ---- states --------------------------------------------------------------------------------
-
-struct __align__(1024) StateSmem {
-  uint8_t X[2][kTile], Y[2][kTile];
-  float b[4][kC];
-};
-
-// Runs the state alone over a segment, 128 threads, warp w rows 16w .. 16w + 15 of the state.
-// Forward: X = K, Y = V, weights w; REV: from the last chunk to the first, X = Q, Y = dO, weights
-// u. CKPT: writes the state before every chunk (forward). grid: pairs · nseg.
-template <bool REV, bool CKPT>
-__global__ void __launch_bounds__(128, 4) k_gs_state(const GsArgs a) {
-  extern __shared__ uint8_t smem_raw[];
-  StateSmem& sm = *reinterpret_cast<StateSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-  const int pair = blockIdx.x / a.nseg, seg = blockIdx.x % a.nseg;
-  const int64_t bi = pair / a.heads, hi_ = pair % a.heads;
-  const Rows& rx = REV ? a.q : a.k;
-  const Rows& ry = REV ? a.dout : a.v;
-  const __nv_bfloat16* X = rx.p + bi * rx.sb + hi_ * rx.sh;
-  const __nv_bfloat16* Y = ry.p + bi * ry.sb + hi_ * ry.sh;
-  const float* gp = a.g + bi * a.gb + hi_ * a.gh;
-  const int c0 = seg * a.per_seg, c1 = min(a.nchunk, c0 + a.per_seg), n = c1 - c0;
-  auto chunk_at = [&](int i) { return REV ? c1 - 1 - i : c0 + i; };
-  auto load = [&](int i) {
-    const int64_t t0 = (int64_t)chunk_at(i) * kC;
-    load_rows<128>(smem_u32(sm.X[i & 1]), X, rx.st, t0, a.T);
-    load_rows<128>(smem_u32(sm.Y[i & 1]), Y, ry.st, t0, a.T);
-    wm::cp_commit();
-  };
-  float S[8][4];
-  load_state(S, a.start != nullptr ? a.start + (size_t)blockIdx.x * kState : nullptr, 16 * warp, lane);
-  float decay = 0.f, g0 = 0.f, g1 = 0.f;
-  if (n > 0) {
-    load(0);
-    load_gates(a, gp, (int64_t)chunk_at(0) * kC, lane, g0, g1);
-  }
-  for (int i = 0; i < n; ++i) {
-    gate_sums(g0, g1, sm.b[warp], lane);
-    if constexpr (CKPT) {
-      __nv_bfloat16* hp = a.ckpt + ((size_t)pair * a.nchunk + chunk_at(i)) * 2 * kState;
-#pragma unroll
-      for (int nt = 0; nt < 8; ++nt)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int at = (16 * warp + g + 8 * h) * kD + 8 * nt + 2 * q;
-          const uint32_t hi = pack_bf16(S[nt][2 * h], S[nt][2 * h + 1]);
-          const float2 f = wm::unpack(hi);
-          *reinterpret_cast<uint32_t*>(hp + at) = hi;
-          *reinterpret_cast<uint32_t*>(hp + kState + at) = pack_bf16(S[nt][2 * h] - f.x, S[nt][2 * h + 1] - f.y);
-        }
-    }
-    wm::cp_wait<0>();
-    __syncthreads();
-    if (i + 1 < n) {
-      load(i + 1);
-      load_gates(a, gp, (int64_t)chunk_at(i + 1) * kC, lane, g0, g1);
-    }
-    const float* b = sm.b[warp];
-    const float bC = b[kC - 1];
-    float w[16];
-#pragma unroll
-    for (int ks = 0; ks < 4; ++ks)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float x = b[16 * ks + 2 * q + (e & 1) + 8 * (e >> 1)];
-        w[4 * ks + e] = REV ? a.scale * exp2_fast(x) : exp2_fast(bC - x);
-      }
-    const float keep = exp2_fast(bC);
-#pragma unroll
-    for (int nt = 0; nt < 8; ++nt)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) S[nt][e] *= keep;
-    add_outer(S, smem_u32(sm.X[i & 1]), smem_u32(sm.Y[i & 1]), w, 16 * warp, lane);
-    decay += bC;
-  }
-  if (a.local != nullptr) {
-    store_state(S, a.local + (size_t)blockIdx.x * kState, 16 * warp, lane);
-    if (threadIdx.x == 0) a.seg_decay[blockIdx.x] = decay;
-  }
-}
 
 // The states the segments start from, in place of what they add: start[s + 1] =
 // 2^decay[s]·start[s] + local[s], from `first` (or zero); REV: start[s − 1] from start[s]. One element
@@ -357,7 +188,7 @@ __device__ __forceinline__ void weigh(uint32_t x, F2 w, uint32_t& hi, uint32_t& 
 // Token t's row of X (a [128][64] tile), weighted by w, as two bf16 terms into the rows of hi and lo.
 __device__ __forceinline__ void weigh_row(const uint8_t* X, uint8_t* hi, uint8_t* lo, int t, float w) {
   const F2 ww = f2(w, w);
-#pragma unroll
+#pragma unroll 2
   for (int c = 0; c < 8; ++c) {
     const uint32_t at = t * 128 + ((c ^ (t & 7)) << 4);
     const uint4 x = *reinterpret_cast<const uint4*>(X + at);
@@ -891,354 +722,464 @@ __global__ void __launch_bounds__(256, 2)
 // ---- backward ------------------------------------------------------------------------------
 
 struct __align__(1024) BwdSmem {
-  uint8_t Q[2][kTile], K[2][kTile], V[2][kTile], G[2][kTile];  // G: dO
-  uint8_t S[2][kTile];   // the state before the chunk: rounded, and what the rounding left
-  uint8_t dS[2][kTile];  // the gradient of the state after the chunk, the same way
-  float b[8][kC];
-  float rows[kC];        // Σ_j A_ij·(q_i·k_j) over j < i, plus q_i·(u_i·S·do_i)
-  float cols[kC];        // Σ_i A_ij·(q_i·k_j) over i > j
-  float past[kC];        // k_j·(w_j·dS'·v_j)
-  float dot[4];          // parts of e^{b_64}·<S, dS'>
+  uint8_t Q[kLTile], K[kLTile], V[kLTile], G[kLTile];  // G: dO
+  uint8_t S[2][kTile];    // the state before the chunk: rounded, and what the rounding left
+  uint8_t dS[2][kTile];   // the gradient of the state after the chunk, the same way
+  uint8_t W[2][kLTile];   // u ⊙ Q, two terms; then dV and dK on their way out
+  uint8_t P[2][kLTile];   // P and A, 128 queries x 128 keys, in halves of 64 keys
+  uint8_t A[2][kLTile];
+  uint8_t out[kLTile];    // dQ on its way out
+  uint8_t swap[kTile];    // the second terms' part of dS, 2^-9 of it, rounded to bf16
+  Gates gates[2];
+  __align__(16) float raw[3][kL];
+  __align__(16) float rows[2][kL];  // Σ_j A_ij·(q_i·k_j) over j < i, per half of the keys
+  __align__(16) float far[kL];      // q_i·(u_i·S·do_i)
+  __align__(16) float cols[4][kL];  // Σ_i A_ij·(q_i·k_j) over i > j, per 32 queries
+  __align__(16) float past[kL];     // k_j·(w_j·dS'·v_j)
+  float dot[4];                     // parts of e^{b_128}·<S, dS'>
+  uint64_t in, scores, inter, added, grads;
+  uint32_t tmem;
+  int abort;
 };
 
-// 256 threads, from the segment's last chunk to its first. Warps 0 .. 3 take rows of queries (dQ,
-// the rows' part of dg) and carry dS; warps 4 .. 7 take rows of keys (dK, dV, their part of dg).
-// grid: pairs · nseg.
-__global__ void __launch_bounds__(256, 2) k_gs_bwd(const GsArgs a) {
+// TMEM columns of k_gs_bwd: Q·Kᵀ and dO·Vᵀ, whose place dQ, dV and dK take once they have been read; the
+// products with the states; the state's sums.
+constexpr int kColSc = 0, kColDp = 128, kColDq = 64, kColDv = 128, kColDk = 192, kColDqi = 256, kColDki = 320, kColDvi = 384,
+              kColDs = 448;
+
+// Sums of 16 columns over the warp's lanes: the halves of the columns go to the halves of the lanes,
+// step by step, so 16 values take 16 exchanges. Lane l gets column (bits 4, 3, 2, 1 of l).
+__device__ __forceinline__ float sum_columns(const F2 (&m)[8], int lane) {
+  float v[16];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float2 f = split(m[i]);
+    v[2 * i] = f.x;
+    v[2 * i + 1] = f.y;
+  }
+#pragma unroll
+  for (int n = 8; n >= 1; n >>= 1) {
+    const bool upper = (lane & (2 * n)) != 0;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float send = upper ? v[i] : v[i + n], keep = upper ? v[i + n] : v[i];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, 2 * n);
+    }
+  }
+  return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 1);
+}
+
+// f · (64 columns of TMEM), and its product with row r of a tile.
+__device__ __forceinline__ float scaled_row(F2 (&x)[32], uint32_t tmem, float f, const uint8_t* tile, int r) {
+  const F2 ff = f2(f, f);
+  F2 d = f2(0.f, 0.f);
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    uint32_t y[32];
+    tc::ld32(tmem + 32 * half, y);
+    tc::wait_ld();
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const uint4 t = tile != nullptr ? *reinterpret_cast<const uint4*>(tile + r * 128 + (((4 * half + c) ^ (r & 7)) << 4))
+                                      : make_uint4(0, 0, 0, 0);
+      const uint32_t tw[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int j = 8 * c + 2 * e;
+        const F2 z = mul(ff, f2u(y[j], y[j + 1]));
+        x[16 * half + 4 * c + e] = z;
+        if (tile != nullptr) d = fma2(from_bf16(tw[e]), z, d);
+      }
+    }
+  }
+  const float2 s = split(d);
+  return s.x + s.y;
+}
+
+// x + (64 columns of TMEM), rounded, into row r of a tile.
+__device__ __forceinline__ void finish_row(const F2 (&x)[32], uint32_t tmem, uint8_t* tile, int r) {
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    uint32_t y[32];
+    tc::ld32(tmem + 32 * half, y);
+    tc::wait_ld();
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      uint32_t w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[e] = to_bf16(add(x[16 * half + 4 * c + e], f2u(y[8 * c + 2 * e], y[8 * c + 2 * e + 1])));
+      *reinterpret_cast<uint4*>(tile + r * 128 + (((4 * half + c) ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+}
+
+// A row of dS, its two parts in the threads id and id + 64, as two bf16 terms into the tiles' rows.
+__device__ __forceinline__ void put_ds(BwdSmem& sm, const F2 (&S)[32], int id) {
+  if (id >= 64) put_state_row(sm.swap, S, id & 63);
+  group_sync(3);
+  if (id < 64) {
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      const uint32_t at = id * 128 + ((c ^ (id & 7)) << 4);
+      const uint4 x = *reinterpret_cast<const uint4*>(sm.swap + at);
+      const uint32_t second[4] = {x.x, x.y, x.z, x.w};
+      uint32_t h[4], l[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const F2 both = add(S[4 * c + e], from_bf16(second[e]));
+        h[e] = to_bf16(both);
+        l[e] = to_bf16(fma2(from_bf16(h[e]), f2(-1.f, -1.f), both));
+      }
+      *reinterpret_cast<uint4*>(sm.dS[0] + at) = make_uint4(h[0], h[1], h[2], h[3]);
+      *reinterpret_cast<uint4*>(sm.dS[1] + at) = make_uint4(l[0], l[1], l[2], l[3]);
+    }
+  }
+}
+
+struct BwdTiles {
+  Tiles q, k, v, g, s, dq, dk, dv;
+};
+
+// From the segment's last chunk to its first: 512 threads in four groups of 128, one CTA an SM; thread
+// `id` of a group holds row `id` of what the group reads from TMEM.
+//   group 0  the scores of keys 0 .. 63: P, A and their sums; dQ
+//   group 1  the same for keys 64 .. 127; dV
+//   group 2  weighs Q (half of each row); carries dS, rows 0 .. 63 the first terms' part and 64 .. 127 the
+//            second's; dg
+//   group 3  weighs Q (the other half); dK
+// All products of a chunk read its tiles from shared memory, which bounds the kernel (some 650 KB a
+// chunk through 128 bytes a cycle). The next chunk's tiles are asked for when the last product has
+// read these, and come while the gradients are rounded and sent out. grid: pairs · nseg.
+__global__ void __launch_bounds__(512, 1) k_gs_bwd(const __grid_constant__ BwdTiles tm_, const GsArgs a) {
   extern __shared__ uint8_t smem_raw[];
   BwdSmem& sm = *reinterpret_cast<BwdSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, id = tid & 127, group = tid >> 7;
   const int pair = blockIdx.x / a.nseg, seg = blockIdx.x % a.nseg;
-  const int64_t bi = pair / a.heads, hi_ = pair % a.heads;
-  const __nv_bfloat16* Q = a.q.p + bi * a.q.sb + hi_ * a.q.sh;
-  const __nv_bfloat16* K = a.k.p + bi * a.k.sb + hi_ * a.k.sh;
-  const __nv_bfloat16* V = a.v.p + bi * a.v.sb + hi_ * a.v.sh;
-  const __nv_bfloat16* G = a.dout.p + bi * a.dout.sb + hi_ * a.dout.sh;
+  const int bi = pair / a.heads, hi_ = pair % a.heads;
   const float* gp = a.g + bi * a.gb + hi_ * a.gh;
-  const __nv_bfloat16* ckpt = a.ckpt + (size_t)pair * a.nchunk * 2 * kState;
-  const size_t out0 = (size_t)pair * a.T * kD;
-  const int c0 = seg * a.per_seg, c1 = min(a.nchunk, c0 + a.per_seg);
-  const bool query_side = warp < 4;
-  const int row0 = 16 * (warp & 3);
-
-  auto load = [&](int c) {
-    const int64_t t0 = (int64_t)c * kC;
-    load_rows<256>(smem_u32(sm.Q[c & 1]), Q, a.q.st, t0, a.T);
-    load_rows<256>(smem_u32(sm.K[c & 1]), K, a.k.st, t0, a.T);
-    load_rows<256>(smem_u32(sm.V[c & 1]), V, a.v.st, t0, a.T);
-    load_rows<256>(smem_u32(sm.G[c & 1]), G, a.dout.st, t0, a.T);
+  const int c0 = seg * a.per_seg, c1 = min(a.nchunk, c0 + a.per_seg), n = c1 - c0;
+  auto load = [&](int i) {
+    const int t = (c1 - 1 - i) * kL;
+    mbar_arrive_expect_tx(&sm.in, 5 * kLTile);
+    tma_load_tile(sm.Q, &tm_.q.map, &sm.in, t, hi_ * tm_.q.head, bi * tm_.q.batch);
+    tma_load_tile(sm.K, &tm_.k.map, &sm.in, t, hi_ * tm_.k.head, bi * tm_.k.batch);
+    tma_load_tile(sm.G, &tm_.g.map, &sm.in, t, hi_ * tm_.g.head, bi * tm_.g.batch);
+    tma_load_tile(sm.V, &tm_.v.map, &sm.in, t, hi_ * tm_.v.head, bi * tm_.v.batch);
+    tma_load_tile(sm.S[0], &tm_.s.map, &sm.in, t, hi_, bi);  // both planes: 128 rows a chunk
   };
-  auto load_ckpt = [&](int c) {
-    load_rows<256>(smem_u32(sm.S[0]), ckpt + (size_t)c * 2 * kState, kD, 0, kD);
-    load_rows<256>(smem_u32(sm.S[1]), ckpt + (size_t)c * 2 * kState + kState, kD, 0, kD);
-  };
-  float dS[8][4];
-  load_state(dS, a.start != nullptr && query_side ? a.start + (size_t)blockIdx.x * kState : nullptr, row0, lane);
-  float g0 = 0.f, g1 = 0.f;
-  if (c0 < c1) {
-    load(c1 - 1);
-    load_ckpt(c1 - 1);
-    wm::cp_commit();
-    load_gates(a, gp, (int64_t)(c1 - 1) * kC, lane, g0, g1);
+  if (tid == 0) {
+    mbar_init(&sm.in, 1);
+    mbar_init(&sm.scores, 1);
+    mbar_init(&sm.inter, 1);
+    mbar_init(&sm.added, 1);
+    mbar_init(&sm.grads, 1);
+    sm.abort = 0;
+    fence_barrier_init();
+    load(0);
   }
-  for (int c = c1 - 1; c >= c0; --c) {
-    const int64_t t0 = (int64_t)c * kC;
-    const float raw0 = g0, raw1 = g1;
-    gate_sums(g0, g1, sm.b[warp], lane);
-    if (query_side) {
+  if (warp == 4) tc::alloc(&sm.tmem, 512);
+  // Keys after a query's block of 32 never get a score: zero once.
+  for (int i = tid; i < 2 * kLTile / 16; i += 512) {
+    reinterpret_cast<uint4*>(sm.P[0])[i] = make_uint4(0, 0, 0, 0);
+    reinterpret_cast<uint4*>(sm.A[0])[i] = make_uint4(0, 0, 0, 0);
+  }
+  for (int i = tid; i < 4 * kL; i += 512) (&sm.cols[0][0])[i] = 0.f;
+  for (int i = tid; i < 2 * kL; i += 512) (&sm.rows[0][0])[i] = 0.f;
+  F2 S[32];  // group 2: the row of dS; groups 0, 1, 3: the gradient's part from beyond the chunk
+  if (group == 2) {
+    const bool first = id < 64;
+    load_row(S, a.start != nullptr && first ? a.start + ((size_t)(a.few ? pair : blockIdx.x) * kD + id) * kD : nullptr);
+    if (a.few && first) {
+      for (int later = a.nseg - 1; later > seg; --later) {
+        const size_t at = (size_t)pair * a.nseg + later;
+        const float f = exp2_fast(a.seg_decay[at]);
+        const ulonglong2* x = reinterpret_cast<const ulonglong2*>(a.local + (at * kD + id) * kD);
 #pragma unroll
-      for (int nt = 0; nt < 8; ++nt)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t at = swz128_bf16(row0 + g + 8 * h, 8 * nt + 2 * q);
-          const uint32_t hi = pack_bf16(dS[nt][2 * h], dS[nt][2 * h + 1]);
-          const float2 f = wm::unpack(hi);
-          *reinterpret_cast<uint32_t*>(sm.dS[0] + at) = hi;
-          *reinterpret_cast<uint32_t*>(sm.dS[1] + at) = pack_bf16(dS[nt][2 * h] - f.x, dS[nt][2 * h + 1] - f.y);
+        for (int c = 0; c < 16; ++c) {
+          const ulonglong2 y = x[c];
+          S[2 * c] = fma2(f2(f, f), S[2 * c], F2{y.x});
+          S[2 * c + 1] = fma2(f2(f, f), S[2 * c + 1], F2{y.y});
         }
+      }
     }
-    wm::cp_wait<0>();
-    __syncthreads();
-    if (c > c0) {
-      load(c - 1);
-      load_gates(a, gp, t0 - kC, lane, g0, g1);
+    put_ds(sm, S, id);
+    if (warp == 11) {
+      fetch_gates(a, gp, (int64_t)(c1 - 1) * kL, sm.raw[0], lane);
+      make_gates(sm.raw[0], sm.gates[0], lane);
+      if (n > 1) fetch_gates(a, gp, (int64_t)(c1 - 2) * kL, sm.raw[1], lane);
     }
-    const int buf = c & 1;
-    const uint32_t Qs = smem_u32(sm.Q[buf]), Ks = smem_u32(sm.K[buf]), Vs = smem_u32(sm.V[buf]), Gs = smem_u32(sm.G[buf]);
-    const float* b = sm.b[warp];
-    const float bC = b[kC - 1];
-    const float br0 = b[row0 + g], br1 = b[row0 + g + 8];
-    float x1[8][4];  // dQ, or dK
-    float x2[8][4];  // dV (key side)
-#pragma unroll
-    for (int nt = 0; nt < 8; ++nt)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) x1[nt][e] = x2[nt][e] = 0.f;
+  }
+  fence_proxy_async_smem();
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tm = sm.tmem, tmem = tm + ((uint32_t)((warp & 3) * 32) << 16);
 
-    if (query_side) {
-      uint32_t ga[4][4];
+  for (int i = 0; i < n; ++i) {
+    const int ph = i & 1, chunk = c1 - 1 - i;
+    const Gates& gt = sm.gates[ph];
+    const float mine = gt.b[id];
+    if (group < 2) {
+      if (tid == 0) {
+        const uint32_t dq = desc_of(sm.Q), dk = desc_of(sm.K), dv = desc_of(sm.V), dg = desc_of(sm.G), ds = desc_of(sm.S[0]),
+                       dd = desc_of(sm.dS[0]);
+        mbar_wait(&sm.in, ph, a.status, &sm.abort);
 #pragma unroll
-      for (int ks = 0; ks < 4; ++ks) wm::frag_a(Gs, row0, 16 * ks, lane, ga[ks]);
-      // u ⊙ (dO·Sᵀ), with S as two terms.
+        for (int kk = 0; kk < 4; ++kk) tc::mma(tm + kColSc, desc_at(dq, kk * 32), desc_at(dk, kk * 32), tc::idesc_bf16(128, 128, 0, 0), kk != 0);
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const uint32_t Sa = smem_u32(sm.S[half]);
+        for (int kk = 0; kk < 4; ++kk) tc::mma(tm + kColDp, desc_at(dg, kk * 32), desc_at(dv, kk * 32), tc::idesc_bf16(128, 128, 0, 0), kk != 0);
+        tc::commit(&sm.scores);
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks)
+        for (int kk = 0; kk < 8; ++kk)
+          tc::mma(tm + kColDqi, desc_at(dg, (kk & 3) * 32), desc_at(ds, (kk >> 2) * kTile + (kk & 3) * 32), tc::idesc_bf16(128, 64, 0, 0), kk != 0);
 #pragma unroll
-          for (int np = 0; np < 4; ++np) {
-            uint32_t y[4];
-            wm::frag_b(Sa, 16 * np, 16 * ks, lane, y);
-            wm::mma(x1[2 * np], ga[ks], y[0], y[1]);
-            wm::mma(x1[2 * np + 1], ga[ks], y[2], y[3]);
-          }
+        for (int kk = 0; kk < 8; ++kk)
+          tc::mma(tm + kColDki, desc_at(dv, (kk & 3) * 32), desc_at(dd, (kk >> 2) * kTile + (kk & 3) * 32), tc::idesc_bf16(128, 64, 0, 0), kk != 0);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) tc::mma(tm + kColDvi, desc_at(dk, kk * 32), desc_at(dd, kk * 2048), tc::idesc_bf16(128, 64, 0, 1), kk != 0);
+        tc::commit(&sm.inter);
       }
-      const float u0 = a.scale * exp2_fast(br0), u1 = a.scale * exp2_fast(br1);
-      float r0 = 0.f, r1 = 0.f, dot = 0.f;
-#pragma unroll
-      for (int nt = 0; nt < 8; ++nt) {
-        x1[nt][0] *= u0;
-        x1[nt][1] *= u0;
-        x1[nt][2] *= u1;
-        x1[nt][3] *= u1;
-        const uint32_t at0 = swz128_bf16(row0 + g, 8 * nt + 2 * q), at1 = swz128_bf16(row0 + g + 8, 8 * nt + 2 * q);
-        const float2 q0 = wm::unpack(*reinterpret_cast<const uint32_t*>(sm.Q[buf] + at0));
-        const float2 q1 = wm::unpack(*reinterpret_cast<const uint32_t*>(sm.Q[buf] + at1));
-        r0 = fmaf(q0.x, x1[nt][0], fmaf(q0.y, x1[nt][1], r0));
-        r1 = fmaf(q1.x, x1[nt][2], fmaf(q1.y, x1[nt][3], r1));
-        const float2 h0 = wm::unpack(*reinterpret_cast<const uint32_t*>(sm.S[0] + at0));
-        const float2 h1 = wm::unpack(*reinterpret_cast<const uint32_t*>(sm.S[0] + at1));
-        const float2 l0 = wm::unpack(*reinterpret_cast<const uint32_t*>(sm.S[1] + at0));
-        const float2 l1 = wm::unpack(*reinterpret_cast<const uint32_t*>(sm.S[1] + at1));
-        dot = fmaf(h0.x + l0.x, dS[nt][0], fmaf(h0.y + l0.y, dS[nt][1], dot));
-        dot = fmaf(h1.x + l1.x, dS[nt][2], fmaf(h1.y + l1.y, dS[nt][3], dot));
-      }
-      uint32_t qa[4][4];
-#pragma unroll
-      for (int ks = 0; ks < 4; ++ks) wm::frag_a(Qs, row0, 16 * ks, lane, qa[ks]);
-#pragma unroll
-      for (int kb = 0; kb < 4; ++kb) {
-        if (kb > (warp & 3)) break;
-        float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}}, d[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {
-          uint32_t y[4];
-          wm::frag_b(Ks, 16 * kb, 16 * ks, lane, y);
-          wm::mma(s[0], qa[ks], y[0], y[1]);
-          wm::mma(s[1], qa[ks], y[2], y[3]);
-          wm::frag_b(Vs, 16 * kb, 16 * ks, lane, y);
-          wm::mma(d[0], ga[ks], y[0], y[1]);
-          wm::mma(d[1], ga[ks], y[2], y[3]);
-        }
-        uint32_t pa[4];
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-          const int j = 16 * kb + 8 * nt + 2 * q, i0 = row0 + g;
-          const float2 bj = *reinterpret_cast<const float2*>(b + j);
-          const float a0 = j <= i0 ? a.scale * d[nt][0] * exp2_fast(br0 - bj.x) : 0.f;
-          const float a1 = j + 1 <= i0 ? a.scale * d[nt][1] * exp2_fast(br0 - bj.y) : 0.f;
-          const float a2 = j <= i0 + 8 ? a.scale * d[nt][2] * exp2_fast(br1 - bj.x) : 0.f;
-          const float a3 = j + 1 <= i0 + 8 ? a.scale * d[nt][3] * exp2_fast(br1 - bj.y) : 0.f;
-          r0 += (j < i0 ? a0 * s[nt][0] : 0.f) + (j + 1 < i0 ? a1 * s[nt][1] : 0.f);
-          r1 += (j < i0 + 8 ? a2 * s[nt][2] : 0.f) + (j + 1 < i0 + 8 ? a3 * s[nt][3] : 0.f);
-          pa[2 * nt] = pack_bf16(a0, a1);
-          pa[2 * nt + 1] = pack_bf16(a2, a3);
-        }
-#pragma unroll
-        for (int np = 0; np < 4; ++np) {
-          uint32_t y[4];
-          wm::frag_b_t(Ks, 16 * kb, 16 * np, lane, y);
-          wm::mma(x1[2 * np], pa, y[0], y[1]);
-          wm::mma(x1[2 * np + 1], pa, y[2], y[3]);
-        }
-      }
-#pragma unroll
-      for (int o = 1; o < 4; o <<= 1) {
-        r0 += __shfl_xor_sync(0xffffffffu, r0, o);
-        r1 += __shfl_xor_sync(0xffffffffu, r1, o);
-      }
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-      if (q == 0) {
-        sm.rows[row0 + g] = r0;
-        sm.rows[row0 + g + 8] = r1;
-      }
-      const float keep = exp2_fast(bC);
-      if (lane == 0) sm.dot[warp] = keep * dot;
-      // dS ← e^{b_64}·dS' + (u ⊙ Q)ᵀ·dO.
-      float w[16];
-#pragma unroll
-      for (int ks = 0; ks < 4; ++ks)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) w[4 * ks + e] = a.scale * exp2_fast(b[16 * ks + 2 * q + (e & 1) + 8 * (e >> 1)]);
-#pragma unroll
-      for (int nt = 0; nt < 8; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) dS[nt][e] *= keep;
-      add_outer(dS, Qs, Gs, w, row0, lane);
-    } else {
-      uint32_t ka[4][4], va[4][4];
-#pragma unroll
-      for (int ks = 0; ks < 4; ++ks) {
-        wm::frag_a(Ks, row0, 16 * ks, lane, ka[ks]);
-        wm::frag_a(Vs, row0, 16 * ks, lane, va[ks]);
-      }
-      // w ⊙ (V·dS'ᵀ), with dS' as two terms, and w ⊙ (K·dS').
-      const uint32_t dSa = smem_u32(sm.dS[0]), dSb = smem_u32(sm.dS[1]);
-#pragma unroll
-      for (int ks = 0; ks < 4; ++ks)
-#pragma unroll
-        for (int np = 0; np < 4; ++np) {
-          uint32_t y[4];
-          wm::frag_b(dSa, 16 * np, 16 * ks, lane, y);
-          wm::mma(x1[2 * np], va[ks], y[0], y[1]);
-          wm::mma(x1[2 * np + 1], va[ks], y[2], y[3]);
-          wm::frag_b(dSb, 16 * np, 16 * ks, lane, y);
-          wm::mma(x1[2 * np], va[ks], y[0], y[1]);
-          wm::mma(x1[2 * np + 1], va[ks], y[2], y[3]);
-          wm::frag_b_t(dSa, 16 * ks, 16 * np, lane, y);
-          wm::mma(x2[2 * np], ka[ks], y[0], y[1]);
-          wm::mma(x2[2 * np + 1], ka[ks], y[2], y[3]);
-        }
-      const float w0 = exp2_fast(bC - br0), w1 = exp2_fast(bC - br1);
-      float p0 = 0.f, p1 = 0.f, m0 = 0.f, m1 = 0.f;
-#pragma unroll
-      for (int nt = 0; nt < 8; ++nt) {
-        x1[nt][0] *= w0;
-        x1[nt][1] *= w0;
-        x1[nt][2] *= w1;
-        x1[nt][3] *= w1;
-        x2[nt][0] *= w0;
-        x2[nt][1] *= w0;
-        x2[nt][2] *= w1;
-        x2[nt][3] *= w1;
-        const float2 k0 = wm::unpack(*reinterpret_cast<const uint32_t*>(sm.K[buf] + swz128_bf16(row0 + g, 8 * nt + 2 * q)));
-        const float2 k1 = wm::unpack(*reinterpret_cast<const uint32_t*>(sm.K[buf] + swz128_bf16(row0 + g + 8, 8 * nt + 2 * q)));
-        p0 = fmaf(k0.x, x1[nt][0], fmaf(k0.y, x1[nt][1], p0));
-        p1 = fmaf(k1.x, x1[nt][2], fmaf(k1.y, x1[nt][3], p1));
-      }
-      // Blocks of 16 queries from this warp's own tokens on: rows j (keys), columns i (queries).
-#pragma unroll
-      for (int ib = 0; ib < 4; ++ib) {
-        if (ib < (warp & 3)) continue;
-        float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}}, d[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {
-          uint32_t y[4];
-          wm::frag_b(Qs, 16 * ib, 16 * ks, lane, y);
-          wm::mma(s[0], ka[ks], y[0], y[1]);
-          wm::mma(s[1], ka[ks], y[2], y[3]);
-          wm::frag_b(Gs, 16 * ib, 16 * ks, lane, y);
-          wm::mma(d[0], va[ks], y[0], y[1]);
-          wm::mma(d[1], va[ks], y[2], y[3]);
-        }
-        uint32_t pa[4], aa[4];
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-          const int i = 16 * ib + 8 * nt + 2 * q, j0 = row0 + g;
-          const float2 bq = *reinterpret_cast<const float2*>(b + i);
-          const float e0 = i >= j0 ? a.scale * exp2_fast(bq.x - br0) : 0.f;
-          const float e1 = i + 1 >= j0 ? a.scale * exp2_fast(bq.y - br0) : 0.f;
-          const float e2 = i >= j0 + 8 ? a.scale * exp2_fast(bq.x - br1) : 0.f;
-          const float e3 = i + 1 >= j0 + 8 ? a.scale * exp2_fast(bq.y - br1) : 0.f;
-          const float a0 = e0 * d[nt][0], a1 = e1 * d[nt][1], a2 = e2 * d[nt][2], a3 = e3 * d[nt][3];
-          m0 += (i > j0 ? a0 * s[nt][0] : 0.f) + (i + 1 > j0 ? a1 * s[nt][1] : 0.f);
-          m1 += (i > j0 + 8 ? a2 * s[nt][2] : 0.f) + (i + 1 > j0 + 8 ? a3 * s[nt][3] : 0.f);
-          aa[2 * nt] = pack_bf16(a0, a1);
-          aa[2 * nt + 1] = pack_bf16(a2, a3);
-          pa[2 * nt] = pack_bf16(e0 * s[nt][0], e1 * s[nt][1]);
-          pa[2 * nt + 1] = pack_bf16(e2 * s[nt][2], e3 * s[nt][3]);
-        }
-#pragma unroll
-        for (int np = 0; np < 4; ++np) {
-          uint32_t y[4];
-          wm::frag_b_t(Qs, 16 * ib, 16 * np, lane, y);
-          wm::mma(x1[2 * np], aa, y[0], y[1]);
-          wm::mma(x1[2 * np + 1], aa, y[2], y[3]);
-          wm::frag_b_t(Gs, 16 * ib, 16 * np, lane, y);
-          wm::mma(x2[2 * np], pa, y[0], y[1]);
-          wm::mma(x2[2 * np + 1], pa, y[2], y[3]);
-        }
-      }
-#pragma unroll
-      for (int o = 1; o < 4; o <<= 1) {
-        p0 += __shfl_xor_sync(0xffffffffu, p0, o);
-        p1 += __shfl_xor_sync(0xffffffffu, p1, o);
-        m0 += __shfl_xor_sync(0xffffffffu, m0, o);
-        m1 += __shfl_xor_sync(0xffffffffu, m1, o);
-      }
-      if (q == 0) {
-        sm.past[row0 + g] = p0;
-        sm.past[row0 + g + 8] = p1;
-        sm.cols[row0 + g] = m0;
-        sm.cols[row0 + g + 8] = m1;
-      }
-    }
-    __syncthreads();  // every tile of this chunk has been read; rows, cols, past and dot are visible
-    if (c > c0) {
-      load_ckpt(c - 1);
-      wm::cp_commit();
-    }
-    // Gradients out through the tiles just read (this warp's own rows of Q, or of K and V).
-    auto put = [&](uint8_t* tile, const float (&x)[8][4], __nv_bfloat16* out) {
-#pragma unroll
-      for (int nt = 0; nt < 8; ++nt)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          *reinterpret_cast<uint32_t*>(tile + swz128_bf16(row0 + g + 8 * h, 8 * nt + 2 * q)) =
-              pack_bf16(x[nt][2 * h], x[nt][2 * h + 1]);
       __syncwarp();
+      mbar_wait(&sm.scores, ph, a.status, &sm.abort);
+      tc::fence_after();
+      // 16 keys at a time, up to this warp's own tokens (in blocks of 32: before them the decay is a
+      // product of the key's to its block's end and the query's from there).
+      const int w = warp & 3;
+      F2 sum = f2(0.f, 0.f);
+      for (int sb = 0; sb < 4; ++sb) {
+        const int j0 = 64 * group + 16 * sb, jb = j0 >> 5;
+        if (jb > w) break;
+        uint32_t s[16], d[16], p[8], x[8];
+        F2 m[8];
+        tc::ld16(tmem + kColSc + j0, s);
+        tc::ld16(tmem + kColDp + j0, d);
+        if (jb < w) {
+          const float f = a.scale * exp2_fast(mine - gt.b[32 * jb + 31]);
+          const F2 ff = f2(f, f);
+          tc::wait_ld();
 #pragma unroll
-      for (int i = lane; i < 128; i += 32) {
-        const int r = row0 + (i >> 3), y = i & 7;
-        if (t0 + r < a.T)
-          *reinterpret_cast<uint4*>(out + out0 + (t0 + r) * kD + 8 * y) =
-              *reinterpret_cast<const uint4*>(tile + r * 128 + ((y ^ (r & 7)) << 4));
+          for (int c = 0; c < 8; ++c) {
+            const F2 dec = mul(ff, *reinterpret_cast<const F2*>(gt.end + j0 + 2 * c));
+            const F2 sc = f2u(s[2 * c], s[2 * c + 1]), at = mul(dec, f2u(d[2 * c], d[2 * c + 1]));
+            p[c] = to_bf16(mul(dec, sc));
+            x[c] = to_bf16(at);
+            m[c] = mul(at, sc);
+            sum = add(sum, m[c]);
+          }
+        } else {
+          const int own = lane - (j0 & 31);  // this row's token among the 16
+          tc::wait_ld();
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const float2 b = *reinterpret_cast<const float2*>(gt.b + j0 + 2 * c);
+            const F2 dec = f2(own >= 2 * c ? a.scale * exp2_fast(mine - b.x) : 0.f, own > 2 * c ? a.scale * exp2_fast(mine - b.y) : 0.f);
+            const F2 sc = f2u(s[2 * c], s[2 * c + 1]), at = mul(dec, f2u(d[2 * c], d[2 * c + 1]));
+            p[c] = to_bf16(mul(dec, sc));
+            x[c] = to_bf16(at);
+            const float2 y = split(mul(at, sc));
+            m[c] = f2(own > 2 * c ? y.x : 0.f, own > 2 * c + 1 ? y.y : 0.f);
+            sum = add(sum, m[c]);
+          }
+        }
+        const int r = id & 7;
+        uint4* P = reinterpret_cast<uint4*>(sm.P[group] + id * 128);
+        uint4* A = reinterpret_cast<uint4*>(sm.A[group] + id * 128);
+        P[(2 * sb) ^ r] = make_uint4(p[0], p[1], p[2], p[3]);
+        P[(2 * sb + 1) ^ r] = make_uint4(p[4], p[5], p[6], p[7]);
+        A[(2 * sb) ^ r] = make_uint4(x[0], x[1], x[2], x[3]);
+        A[(2 * sb + 1) ^ r] = make_uint4(x[4], x[5], x[6], x[7]);
+        const float total = sum_columns(m, lane);
+        if ((lane & 1) == 0) sm.cols[w][j0 + (((lane >> 4) & 1) * 8 + ((lane >> 3) & 1) * 4 + ((lane >> 2) & 1) * 2 + ((lane >> 1) & 1))] = total;
       }
-    };
-    if (query_side) {
-      put(sm.Q[buf], x1, a.dq);
+      const float2 sums = split(sum);
+      sm.rows[group][id] = sums.x + sums.y;
+      fence_proxy_async_smem();
+      tc::fence_before();
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      if (tid == 0) {
+        tc::fence_after();
+        const uint32_t dp = desc_of(sm.P[0], kLTile), da = desc_of(sm.A[0], kLTile), dak = desc_of(sm.A[0]), dq = desc_of(sm.Q),
+                       dk = desc_of(sm.K), dg = desc_of(sm.G);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          tc::mma(tm + kColDq, desc_at(dak, (kk >> 2) * kLTile + (kk & 3) * 32), desc_at(dk, kk * 2048), tc::idesc_bf16(128, 64, 0, 1), kk != 0);
+        outer_mma(tm + kColDv, dp, dg);
+        outer_mma(tm + kColDk, da, dq);
+        tc::commit(&sm.grads);
+      }
+      __syncwarp();
+      mbar_wait(&sm.in, ph, a.status, &sm.abort);  // this thread reads Q itself
+      mbar_wait(&sm.inter, ph, a.status, &sm.abort);
+      tc::fence_after();
+      if (group == 0) {
+        sm.far[id] = scaled_row(S, tmem + kColDqi, a.scale * exp2_fast(mine), sm.Q, id);
+      } else {
+        scaled_row(S, tmem + kColDvi, gt.w[id], nullptr, id);
+      }
     } else {
-      put(sm.K[buf], x1, a.dk);
-      put(sm.V[buf], x2, a.dv);
+      mbar_wait(&sm.in, ph, a.status, &sm.abort);
+      {
+        // Half a row of u ⊙ Q each.
+        const float u = a.scale * exp2_fast(mine);
+        const F2 uu = f2(u, u);
+#pragma unroll 2
+        for (int c = 4 * (group - 2); c < 4 * (group - 2) + 4; ++c) {
+          const uint32_t at = id * 128 + ((c ^ (id & 7)) << 4);
+          const uint4 x = *reinterpret_cast<const uint4*>(sm.Q + at);
+          uint4 h, l;
+          weigh(x.x, uu, h.x, l.x);
+          weigh(x.y, uu, h.y, l.y);
+          weigh(x.z, uu, h.z, l.z);
+          weigh(x.w, uu, h.w, l.w);
+          *reinterpret_cast<uint4*>(sm.W[0] + at) = h;
+          *reinterpret_cast<uint4*>(sm.W[1] + at) = l;
+        }
+      }
+      fence_proxy_async_smem();
+      asm volatile("bar.sync 2, 256;" ::: "memory");
+      if (tid == 256) {
+        outer_mma(tm + kColDs, desc_of(sm.W[0], kLTile), desc_of(sm.G));
+        tc::commit(&sm.added);
+      }
+      __syncwarp();
+      if (group == 2) {
+        const float keep = exp2_fast(gt.total);
+        F2 d = f2(0.f, 0.f);
+        const int r = id & 63;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const uint32_t at = r * 128 + ((c ^ (r & 7)) << 4);
+          const uint4 x = *reinterpret_cast<const uint4*>(sm.S[0] + at), y = *reinterpret_cast<const uint4*>(sm.S[1] + at);
+          d = fma2(S[4 * c], add(from_bf16(x.x), from_bf16(y.x)), d);
+          d = fma2(S[4 * c + 1], add(from_bf16(x.y), from_bf16(y.y)), d);
+          d = fma2(S[4 * c + 2], add(from_bf16(x.z), from_bf16(y.z)), d);
+          d = fma2(S[4 * c + 3], add(from_bf16(x.w), from_bf16(y.w)), d);
+        }
+        const float2 dd = split(d);
+        float dot = dd.x + dd.y;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+        if (lane == 0) sm.dot[warp & 3] = keep * dot;
+        mbar_wait(&sm.added, ph, a.status, &sm.abort);
+        tc::fence_after();
+        const F2 kk = f2(keep, keep);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t y[32];
+          tc::ld32(tmem + kColDs + 32 * half, y);
+          tc::wait_ld();
+#pragma unroll
+          for (int c = 0; c < 16; ++c) S[16 * half + c] = fma2(kk, S[16 * half + c], f2u(y[2 * c], y[2 * c + 1]));
+        }
+        mbar_wait(&sm.inter, ph, a.status, &sm.abort);  // dS' has been read
+        put_ds(sm, S, id);
+        fence_proxy_async_smem();
+        if (warp == 11 && i + 1 < n) {
+          make_gates(sm.raw[(i + 1) % 3], sm.gates[ph ^ 1], lane);
+          if (i + 2 < n) fetch_gates(a, gp, (int64_t)(chunk - 2) * kL, sm.raw[(i + 2) % 3], lane);
+        }
+      } else {
+        mbar_wait(&sm.inter, ph, a.status, &sm.abort);
+        tc::fence_after();
+        sm.past[id] = scaled_row(S, tmem + kColDki, gt.w[id], sm.K, id);
+      }
     }
-    if (warp == 7) {
-      // dg over the chunk: sums over the tokens from t on of (rows − cols), sums over those before
-      // t of past.
-      float s0 = sm.rows[lane] - sm.cols[lane], s1 = sm.rows[lane + 32] - sm.cols[lane + 32];
-      const float f0 = sm.past[lane], f1 = sm.past[lane + 32];
-      float c0_ = f0, c1_ = f1;
+    tc::fence_before();
+    __syncthreads();  // the chunk's tiles have been read but by the products still running
+    tc::fence_after();
+    if (group != 2) {
+      mbar_wait(&sm.grads, ph, a.status, &sm.abort);
+      tc::fence_after();
+      if (tid == 0 && i + 1 < n) load(i + 1);
+      __syncwarp();
+      uint8_t* stage = group == 0 ? sm.out : group == 1 ? sm.W[0] : sm.W[1];
+      finish_row(S, tmem + (group == 0 ? kColDq : group == 1 ? kColDv : kColDk), stage, id);
+      fence_proxy_async_smem();
+      group_sync(4 + group);
+      if (id == 0) {
+        tma_store_tile(group == 0 ? &tm_.dq.map : group == 1 ? &tm_.dv.map : &tm_.dk.map, stage, chunk * kL, hi_, bi);
+        bulk_commit();
+        bulk_wait_read<0>();
+      }
+    } else if (warp == 8) {
+      // dg over the chunk, four tokens a lane: sums over the tokens from t on of (rows − cols), sums over
+      // those before t of past.
+      float4 s = *reinterpret_cast<const float4*>(sm.rows[0] + 4 * lane);
+      const float4 s1 = *reinterpret_cast<const float4*>(sm.rows[1] + 4 * lane), f = *reinterpret_cast<const float4*>(sm.far + 4 * lane),
+                   p = *reinterpret_cast<const float4*>(sm.past + 4 * lane), raw = *reinterpret_cast<const float4*>(sm.raw[i % 3] + 4 * lane);
+      s.x += s1.x + f.x, s.y += s1.y + f.y, s.z += s1.z + f.z, s.w += s1.w + f.w;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float4 c = *reinterpret_cast<const float4*>(sm.cols[q] + 4 * lane);
+        s.x -= c.x, s.y -= c.y, s.z -= c.z, s.w -= c.w;
+      }
+      s.z += s.w, s.y += s.z, s.x += s.y;
+      float after = s.x, before = (p.x + p.y) + (p.z + p.w);
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const float y0 = __shfl_down_sync(0xffffffffu, s0, o), y1 = __shfl_down_sync(0xffffffffu, s1, o);
-        const float z0 = __shfl_up_sync(0xffffffffu, c0_, o), z1 = __shfl_up_sync(0xffffffffu, c1_, o);
-        if (lane + o < 32) {
-          s0 += y0;
-          s1 += y1;
-        }
-        if (lane >= o) {
-          c0_ += z0;
-          c1_ += z1;
-        }
+        const float y = __shfl_down_sync(0xffffffffu, after, o), z = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane + o < 32) after += y;
+        if (lane >= o) before += z;
       }
-      s0 += __shfl_sync(0xffffffffu, s1, 0);
-      const float first = __shfl_sync(0xffffffffu, c0_, 31);
+      after = __shfl_down_sync(0xffffffffu, after, 1);
+      before = __shfl_up_sync(0xffffffffu, before, 1);
       const float all = (sm.dot[0] + sm.dot[1]) + (sm.dot[2] + sm.dot[3]);
-      const float d0 = all + s0 + (c0_ - f0), d1 = all + s1 + (first + (c1_ - f1));
-      float* dg = a.dg + (size_t)pair * a.T;
-      // Where the gate's factor is 0 in fp32 so is its derivative.
-      if (t0 + lane < a.T) dg[t0 + lane] = raw0 < kGoneGate ? 0.f : d0;
-      if (t0 + lane + 32 < a.T) dg[t0 + lane + 32] = raw1 < kGoneGate ? 0.f : d1;
+      const float base = all + (lane == 31 ? 0.f : after) + (lane == 0 ? 0.f : before);
+      const float v[4] = {base + s.x, base + s.y + p.x, base + s.z + (p.x + p.y), base + s.w + (p.x + p.y + p.z)};
+      const float g[4] = {raw.x, raw.y, raw.z, raw.w};
+      const int64_t t0 = (int64_t)chunk * kL + 4 * lane;
+      float* dg = a.dg + (size_t)pair * a.T + t0;
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (t0 + q < a.T) dg[q] = g[q] < kGoneGate ? 0.f : v[q];  // where the gate's factor is 0 in fp32 so is its derivative
+    }
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+  }
+  if (a.end != nullptr && seg == 0 && group == 2) {
+    float4* at = reinterpret_cast<float4*>(sm.P[0]) + (id & 63) * 16;  // the products are done
+    if (id >= 64) {
+#pragma unroll
+      for (int c = 0; c < 16; ++c) {
+        const float2 x = split(S[2 * c]), y = split(S[2 * c + 1]);
+        at[c ^ (id & 7)] = make_float4(x.x, x.y, y.x, y.y);
+      }
+    }
+    group_sync(3);
+    if (id < 64) {
+#pragma unroll
+      for (int c = 0; c < 16; ++c) {
+        const float4 x = at[c ^ (id & 7)];
+        S[2 * c] = add(S[2 * c], f2(x.x, x.y));
+        S[2 * c + 1] = add(S[2 * c + 1], f2(x.z, x.w));
+      }
+      store_row(S, a.end + ((size_t)pair * kD + id) * kD);
     }
   }
-  if (a.end != nullptr && seg == 0 && query_side) store_state(dS, a.end + (size_t)pair * kState, row0, lane);
+  __syncthreads();
+  if (warp == 4) {
+    let_land(&sm.abort);
+    __syncwarp();
+    tc::dealloc(tm, 512);
+  }
 }
 
 // ---- one token -----------------------------------------------------------------------------
 
 // S ← e^g·S + kᵀ·v in place, o = scale · q·S: one CTA of 128 threads per (sequence, head), each
 // thread four columns of eight rows, all its loads in flight at once.
-__global__ void __launch_bounds__(128) k_gs_step(const GsArgs a, float* __restrict__ state) {
+struct StepArgs {
+  Rows q, k, v;
+  const float* g;
+  int64_t gb, gh;
+  __nv_bfloat16* o;
+  int64_t ob, oh;
+  int heads;
+  float scale;
+};
+
+__global__ void __launch_bounds__(128) k_gs_step(const StepArgs a, float* __restrict__ state) {
   __shared__ float4 part[8][16];
   const int pair = blockIdx.x, cg = threadIdx.x & 15, rg = threadIdx.x >> 4;
   const int64_t bi = pair / a.heads, hi = pair % a.heads;
@@ -1295,20 +1236,21 @@ int segments(int64_t pairs, int nchunk, int slots) {
   return (int)std::max<int64_t>(1, std::min<int64_t>(most, slots / pairs));
 }
 
+constexpr int kPerSm = 2;  // resident CTAs of k_gs_segment and k_gs_out, which the plan fills
+
 struct Plan {
   int nchunk, nseg, per_seg;
 };
 
-Plan plan_for(const ttt_gated_scan_desc* d, int chunk, int num_sms, int per_sm) {
+Plan plan_for(const ttt_gated_scan_desc* d, int num_sms) {
   Plan p;
-  p.nchunk = (int)((d->tokens + chunk - 1) / chunk);
-  p.nseg = segments((int64_t)d->batch * d->heads, p.nchunk, num_sms * per_sm);
+  p.nchunk = (int)((d->tokens + kL - 1) / kL);
+  p.nseg = segments((int64_t)d->batch * d->heads, p.nchunk, num_sms * kPerSm);
   p.per_seg = (p.nchunk + p.nseg - 1) / p.nseg;
   p.nseg = (p.nchunk + p.per_seg - 1) / p.per_seg;  // none empty
   return p;
 }
 
-constexpr int kOutPerSm = 2, kBwdPerSm = 2;  // resident CTAs the kernels are built for
 
 // Up to so many segments the outputs' CTAs add up the states before theirs on their own (16 KB each from
 // L2), which saves a launch of some 8 us; beyond it one launch combines them in order.
@@ -1322,24 +1264,20 @@ ttt_status raise_smem(K* fn, size_t bytes) {
   return TTT_OK;
 }
 
-constexpr size_t kSegSmem = sizeof(SegSmem) + 1024;
-constexpr size_t kStateSmem = sizeof(StateSmem) + 1024, kOutSmem = sizeof(OutSmem) + 1024, kBwdSmem = sizeof(BwdSmem) + 1024;
-static_assert(2 * (kBwdSmem + 1024) <= 233472, "two CTAs of k_gs_bwd do not fit an SM");
+constexpr size_t kSegSmem = sizeof(SegSmem) + 1024, kOutSmem = sizeof(OutSmem) + 1024, kBwdSmem = sizeof(BwdSmem) + 1024;
+static_assert(kBwdSmem <= 232448, "k_gs_bwd exceeds the 227 KB of shared memory per block");
 static_assert(2 * (kOutSmem + 1024) <= 233472, "two CTAs of k_gs_out do not fit an SM");
 static_assert(2 * (kSegSmem + 1024) <= 233472, "two CTAs of k_gs_segment do not fit an SM");
 
 Rows rows_of(const void* p, const ttt_strides& s) {
-  return Rows{static_cast<const __nv_bfloat16*>(p), s.batch, s.head, s.token};
+  return Rows{static_cast<const __nv_bfloat16*>(p), s.batch, s.head};
 }
 
-GsArgs base_args(const ttt_gated_scan_desc* d, const void* q, const void* k, const void* v, const float* g) {
+GsArgs base_args(const ttt_gated_scan_desc* d, const float* g) {
   GsArgs a = {};
   a.heads = d->heads;
   a.T = d->tokens;
   a.scale = d->scale;
-  a.q = rows_of(q, d->q);
-  a.k = rows_of(k, d->k);
-  a.v = rows_of(v, d->v);
   a.g = g;
   a.gb = d->g.batch;
   a.gh = d->g.head;
@@ -1348,25 +1286,13 @@ GsArgs base_args(const ttt_gated_scan_desc* d, const void* q, const void* k, con
   return a;
 }
 
-// The states that the segments start from, into a.local (which every later launch reads as start).
-template <bool REV>
-ttt_status segment_starts(GsArgs a, const float* first, int64_t pairs, cudaStream_t s) {
-  a.start = nullptr;
-  TTT_TRY(raise_smem(k_gs_state<REV, false>, kStateSmem));
-  k_gs_state<REV, false><<<(unsigned)(pairs * a.nseg), 128, kStateSmem, s>>>(a);
-  TTT_CUDA(cudaGetLastError());
-  k_gs_combine<REV><<<dim3((unsigned)pairs, kState / 128), 128, 0, s>>>(a.local, a.seg_decay, first, a.nseg);
-  TTT_CUDA(cudaGetLastError());
-  return TTT_OK;
-}
-
 }  // namespace
 
 size_t gated_scan_workspace(const ttt_gated_scan_desc* d, bool backward, int num_sms) {
   const size_t pairs = (size_t)d->batch * d->heads;
-  const Plan p = plan_for(d, backward ? kC : kL, num_sms, backward ? kBwdPerSm : kOutPerSm);
-  const size_t seg = p.nseg > 1 ? round256(pairs * p.nseg * kState * 4) + round256(pairs * p.nseg * 4) : 0;
-  return seg + (backward ? round256(pairs * p.nchunk * 2 * kState * 2) : 0);
+  const Plan p = plan_for(d, num_sms);
+  const size_t seg = p.nseg > 1 ? 2 * (round256(pairs * p.nseg * kState * 4) + round256(pairs * p.nseg * 4)) : 0;
+  return (backward ? seg : seg / 2) + (backward ? round256(pairs * p.nchunk * 2 * kState * 2) : 0);
 }
 
 // The tensor map of [batch, heads, tokens, 64] rows in tiles of 128 tokens.
@@ -1390,15 +1316,11 @@ static ttt_status tiles_of(Tiles* t, const void* p, const ttt_strides& s, const 
 ttt_status gated_scan(const ttt_gated_scan_desc* d, const void* q, const void* k, const void* v, const float* g,
                       const float* S0, void* o, float* S_end, void* ws, int32_t* status, int num_sms, cudaStream_t s) {
   const int64_t pairs = (int64_t)d->batch * d->heads;
-  const Plan p = plan_for(d, kL, num_sms, kOutPerSm);
-  GsArgs a = base_args(d, q, k, v, g);
+  const Plan p = plan_for(d, num_sms);
+  GsArgs a = base_args(d, g);
   a.nchunk = p.nchunk;
   a.nseg = p.nseg;
   a.per_seg = p.per_seg;
-  a.o = static_cast<__nv_bfloat16*>(o);
-  a.ob = d->o.batch;
-  a.oh = d->o.head;
-  a.ot = d->o.token;
   a.status = DevStatus{status, kWaitLimitNs};
   a.start = S0;
   Tiles tq, tk, tv, to;
@@ -1432,52 +1354,72 @@ ttt_status gated_scan_backward(const ttt_gated_scan_desc* d, const void* dout, c
                                const void* v, const float* g, const float* S0, const float* dS_end, void* dq, void* dk,
                                void* dv, float* dg, float* dS0, void* ws, int32_t* status, int num_sms, cudaStream_t s) {
   const int64_t pairs = (int64_t)d->batch * d->heads;
-  const Plan p = plan_for(d, kC, num_sms, kBwdPerSm);
-  GsArgs a = base_args(d, q, k, v, g);
+  const Plan p = plan_for(d, num_sms);
+  GsArgs a = base_args(d, g);
   a.nchunk = p.nchunk;
   a.nseg = p.nseg;
   a.per_seg = p.per_seg;
-  a.dout = rows_of(dout, d->o);
   a.status = DevStatus{status, kWaitLimitNs};
   uint8_t* w = static_cast<uint8_t*>(ws);
   a.ckpt = reinterpret_cast<__nv_bfloat16*>(w);
   w += round256((size_t)pairs * p.nchunk * 2 * kState * 2);
-  float* local = reinterpret_cast<float*>(w);
-  float* decay = reinterpret_cast<float*>(w + round256((size_t)pairs * p.nseg * kState * 4));
+  const size_t local_bytes = round256((size_t)pairs * p.nseg * kState * 4), decay_bytes = round256((size_t)pairs * p.nseg * 4);
+  float* local[2];
+  float* decay[2];
+  for (int i = 0; i < 2; ++i) {
+    local[i] = reinterpret_cast<float*>(w + i * (local_bytes + decay_bytes));
+    decay[i] = reinterpret_cast<float*>(w + i * (local_bytes + decay_bytes) + local_bytes);
+  }
+  BwdTiles t;
+  TTT_TRY(tiles_of(&t.q, q, d->q, d));
+  TTT_TRY(tiles_of(&t.k, k, d->k, d));
+  TTT_TRY(tiles_of(&t.v, v, d->v, d));
+  TTT_TRY(tiles_of(&t.g, dout, d->o, d));
+  // The gradients are dense; the states' two planes lie as 128 rows of 64 a chunk.
+  ttt_gated_scan_desc rows = *d;
+  ttt_strides dense = {(int64_t)d->heads * d->tokens * kD, d->tokens * kD, kD};
+  TTT_TRY(tiles_of(&t.dq, dq, dense, &rows));
+  TTT_TRY(tiles_of(&t.dk, dk, dense, &rows));
+  TTT_TRY(tiles_of(&t.dv, dv, dense, &rows));
+  rows.tokens = (int64_t)p.nchunk * kL;
+  dense = {(int64_t)d->heads * rows.tokens * kD, rows.tokens * kD, kD};
+  TTT_TRY(tiles_of(&t.s, a.ckpt, dense, &rows));
+  const unsigned grid = (unsigned)(pairs * p.nseg);
+  TTT_TRY(raise_smem(k_gs_segment<false, true>, kSegSmem));
   if (p.nseg > 1) {
-    a.local = local;
-    a.seg_decay = decay;
-    TTT_TRY(segment_starts<false>(a, S0, pairs, s));
+    TTT_TRY(raise_smem(k_gs_segment<false, false>, kSegSmem));
+    TTT_TRY(raise_smem(k_gs_segment<true, false>, kSegSmem));
+    a.local = local[0];
+    a.seg_decay = decay[0];
+    k_gs_segment<false, false><<<grid, 256, kSegSmem, s>>>(t.k, t.v, a);
+    TTT_CUDA(cudaGetLastError());
+    k_gs_combine<false><<<dim3((unsigned)pairs, kState / 128), 128, 0, s>>>(a.local, a.seg_decay, S0, a.nseg);
+    TTT_CUDA(cudaGetLastError());
+    a.local = local[1];
+    a.seg_decay = decay[1];
+    k_gs_segment<true, false><<<grid, 256, kSegSmem, s>>>(t.q, t.g, a);
+    TTT_CUDA(cudaGetLastError());
+    k_gs_combine<true><<<dim3((unsigned)pairs, kState / 128), 128, 0, s>>>(a.local, a.seg_decay, dS_end, a.nseg);
+    TTT_CUDA(cudaGetLastError());
   }
   // The state before every chunk.
-  a.start = p.nseg > 1 ? local : S0;
   a.local = nullptr;
-  TTT_TRY(raise_smem(k_gs_state<false, true>, kStateSmem));
-  k_gs_state<false, true><<<(unsigned)(pairs * p.nseg), 128, kStateSmem, s>>>(a);
+  a.start = p.nseg > 1 ? local[0] : S0;
+  k_gs_segment<false, true><<<grid, 256, kSegSmem, s>>>(t.k, t.v, a);
   TTT_CUDA(cudaGetLastError());
-  if (p.nseg > 1) {
-    a.local = local;
-    TTT_TRY(segment_starts<true>(a, dS_end, pairs, s));
-    a.local = nullptr;
-  }
-  a.start = p.nseg > 1 ? local : dS_end;
+  a.start = p.nseg > 1 ? local[1] : dS_end;
   a.end = dS0;
-  a.dq = static_cast<__nv_bfloat16*>(dq);
-  a.dk = static_cast<__nv_bfloat16*>(dk);
-  a.dv = static_cast<__nv_bfloat16*>(dv);
   a.dg = dg;
   TTT_TRY(raise_smem(k_gs_bwd, kBwdSmem));
-  k_gs_bwd<<<(unsigned)(pairs * p.nseg), 256, kBwdSmem, s>>>(a);
+  k_gs_bwd<<<grid, 512, kBwdSmem, s>>>(t, a);
   TTT_CUDA(cudaGetLastError());
   return TTT_OK;
 }
 
 ttt_status gated_scan_step(const ttt_gated_scan_desc* d, const void* q, const void* k, const void* v, const float* g,
                            float* state, void* o, cudaStream_t s) {
-  GsArgs a = base_args(d, q, k, v, g);
-  a.o = static_cast<__nv_bfloat16*>(o);
-  a.ob = d->o.batch;
-  a.oh = d->o.head;
+  const StepArgs a = {rows_of(q, d->q), rows_of(k, d->k), rows_of(v, d->v), g, d->g.batch, d->g.head, static_cast<__nv_bfloat16*>(o),
+                      d->o.batch, d->o.head, d->heads, d->scale};
   k_gs_step<<<(unsigned)((int64_t)d->batch * d->heads), 128, 0, s>>>(a, state);
   TTT_CUDA(cudaGetLastError());
   return TTT_OK;
