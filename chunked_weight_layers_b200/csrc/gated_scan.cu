@@ -737,7 +737,7 @@ struct __align__(1024) BwdSmem {
   __align__(16) float cols[4][kL];  // Σ_i A_ij·(q_i·k_j) over i > j, per 32 queries
   __align__(16) float past[kL];     // k_j·(w_j·dS'·v_j)
   float dot[4];                     // parts of e^{b_128}·<S, dS'>
-  uint64_t in, scores, inter, added, grads;
+  uint64_t in, scores, inter, added, grads, sent;
   uint32_t tmem;
   int abort;
 };
@@ -746,28 +746,6 @@ struct __align__(1024) BwdSmem {
 // products with the states; the state's sums.
 constexpr int kColSc = 0, kColDp = 128, kColDq = 64, kColDv = 128, kColDk = 192, kColDqi = 256, kColDki = 320, kColDvi = 384,
               kColDs = 448;
-
-// Sums of 16 columns over the warp's lanes: the halves of the columns go to the halves of the lanes,
-// step by step, so 16 values take 16 exchanges. Lane l gets column (bits 4, 3, 2, 1 of l).
-__device__ __forceinline__ float sum_columns(const F2 (&m)[8], int lane) {
-  float v[16];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float2 f = split(m[i]);
-    v[2 * i] = f.x;
-    v[2 * i + 1] = f.y;
-  }
-#pragma unroll
-  for (int n = 8; n >= 1; n >>= 1) {
-    const bool upper = (lane & (2 * n)) != 0;
-#pragma unroll
-    for (int i = 0; i < n; ++i) {
-      const float send = upper ? v[i] : v[i + n], keep = upper ? v[i + n] : v[i];
-      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, 2 * n);
-    }
-  }
-  return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 1);
-}
 
 // f · (64 columns of TMEM), and its product with row r of a tile.
 __device__ __forceinline__ float scaled_row(F2 (&x)[32], uint32_t tmem, float f, const uint8_t* tile, int r) {
@@ -873,6 +851,7 @@ __global__ void __launch_bounds__(512, 1) k_gs_bwd(const __grid_constant__ BwdTi
     mbar_init(&sm.inter, 1);
     mbar_init(&sm.added, 1);
     mbar_init(&sm.grads, 1);
+    mbar_init(&sm.sent, 2);
     sm.abort = 0;
     fence_barrier_init();
     load(0);
@@ -919,6 +898,10 @@ __global__ void __launch_bounds__(512, 1) k_gs_bwd(const __grid_constant__ BwdTi
     const int ph = i & 1, chunk = c1 - 1 - i;
     const Gates& gt = sm.gates[ph];
     const float mine = gt.b[id];
+    if (i > 0 && id == 0 && group != 2) {
+      bulk_wait_read<0>();  // the last chunk's gradient has left its buffer (group 0's: used again past the next barrier)
+      if (group != 0) mbar_arrive(&sm.sent);
+    }
     if (group < 2) {
       if (tid == 0) {
         const uint32_t dq = desc_of(sm.Q), dk = desc_of(sm.K), dv = desc_of(sm.V), dg = desc_of(sm.G), ds = desc_of(sm.S[0]),
@@ -942,57 +925,95 @@ __global__ void __launch_bounds__(512, 1) k_gs_bwd(const __grid_constant__ BwdTi
       __syncwarp();
       mbar_wait(&sm.scores, ph, a.status, &sm.abort);
       tc::fence_after();
-      // 16 keys at a time, up to this warp's own tokens (in blocks of 32: before them the decay is a
-      // product of the key's to its block's end and the query's from there).
-      const int w = warp & 3;
-      F2 sum = f2(0.f, 0.f);
-      for (int sb = 0; sb < 4; ++sb) {
-        const int j0 = 64 * group + 16 * sb, jb = j0 >> 5;
-        if (jb > w) break;
-        uint32_t s[16], d[16], p[8], x[8];
-        F2 m[8];
-        tc::ld16(tmem + kColSc + j0, s);
-        tc::ld16(tmem + kColDp + j0, d);
-        if (jb < w) {
-          const float f = a.scale * exp2_fast(mine - gt.b[32 * jb + 31]);
-          const F2 ff = f2(f, f);
-          tc::wait_ld();
+      // Blocks of 32 keys up to this warp's own 32 queries (before them the decay is a product of the
+      // key's to its block's end and the query's from there), 16 keys at a time as matrix fragments: a
+      // lane holds four queries and four keys, so a key's sum over the warp's queries takes four
+      // exchanges for 16 keys, where whole rows in a lane would take 16.
+      const int w = warp & 3, fg = lane >> 2, fq = lane & 3;
+      float br[4];
+      F2 sum[4];
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            const F2 dec = mul(ff, *reinterpret_cast<const F2*>(gt.end + j0 + 2 * c));
-            const F2 sc = f2u(s[2 * c], s[2 * c + 1]), at = mul(dec, f2u(d[2 * c], d[2 * c + 1]));
-            p[c] = to_bf16(mul(dec, sc));
-            x[c] = to_bf16(at);
-            m[c] = mul(at, sc);
-            sum = add(sum, m[c]);
-          }
-        } else {
-          const int own = lane - (j0 & 31);  // this row's token among the 16
-          tc::wait_ld();
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            const float2 b = *reinterpret_cast<const float2*>(gt.b + j0 + 2 * c);
-            const F2 dec = f2(own >= 2 * c ? a.scale * exp2_fast(mine - b.x) : 0.f, own > 2 * c ? a.scale * exp2_fast(mine - b.y) : 0.f);
-            const F2 sc = f2u(s[2 * c], s[2 * c + 1]), at = mul(dec, f2u(d[2 * c], d[2 * c + 1]));
-            p[c] = to_bf16(mul(dec, sc));
-            x[c] = to_bf16(at);
-            const float2 y = split(mul(at, sc));
-            m[c] = f2(own > 2 * c ? y.x : 0.f, own > 2 * c + 1 ? y.y : 0.f);
-            sum = add(sum, m[c]);
-          }
-        }
-        const int r = id & 7;
-        uint4* P = reinterpret_cast<uint4*>(sm.P[group] + id * 128);
-        uint4* A = reinterpret_cast<uint4*>(sm.A[group] + id * 128);
-        P[(2 * sb) ^ r] = make_uint4(p[0], p[1], p[2], p[3]);
-        P[(2 * sb + 1) ^ r] = make_uint4(p[4], p[5], p[6], p[7]);
-        A[(2 * sb) ^ r] = make_uint4(x[0], x[1], x[2], x[3]);
-        A[(2 * sb + 1) ^ r] = make_uint4(x[4], x[5], x[6], x[7]);
-        const float total = sum_columns(m, lane);
-        if ((lane & 1) == 0) sm.cols[w][j0 + (((lane >> 4) & 1) * 8 + ((lane >> 3) & 1) * 4 + ((lane >> 2) & 1) * 2 + ((lane >> 1) & 1))] = total;
+      for (int r = 0; r < 4; ++r) {
+        br[r] = gt.b[32 * w + 8 * r + fg];
+        sum[r] = f2(0.f, 0.f);
       }
-      const float2 sums = split(sum);
-      sm.rows[group][id] = sums.x + sums.y;
+      const uint32_t row = 32 * w + (lane & 15), Pt = smem_u32(sm.P[group]), At = smem_u32(sm.A[group]);
+#pragma unroll 1
+      for (int blk = 0; blk < 2; ++blk) {
+        const int jb = 2 * group + blk;
+        if (jb > w) break;
+        uint32_t s[2][2][8], d[2][2][8];  // [16 keys][16 queries]
+#pragma unroll
+        for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            tc::ld_frag16(tmem + ((uint32_t)(16 * h) << 16) + kColSc + 32 * jb + 16 * sub, s[sub][h]);
+            tc::ld_frag16(tmem + ((uint32_t)(16 * h) << 16) + kColDp + 32 * jb + 16 * sub, d[sub][h]);
+          }
+        F2 ff[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float f = jb < w ? a.scale * exp2_fast(br[r] - gt.b[32 * jb + 31]) : a.scale;
+          ff[r] = f2(f, f);
+        }
+        tc::wait_ld();
+#pragma unroll
+        for (int sub = 0; sub < 2; ++sub) {
+          F2 col[2];
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            const int j = 32 * jb + 16 * sub + 8 * n + 2 * fq;
+            const F2 end = *reinterpret_cast<const F2*>(gt.end + j);
+            const float2 b = *reinterpret_cast<const float2*>(gt.b + j);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              uint32_t& sr = s[sub][r >> 1][4 * n + 2 * (r & 1)];
+              uint32_t& dr = d[sub][r >> 1][4 * n + 2 * (r & 1)];
+              const F2 sc = f2u(sr, s[sub][r >> 1][4 * n + 2 * (r & 1) + 1]), dp = f2u(dr, d[sub][r >> 1][4 * n + 2 * (r & 1) + 1]);
+              F2 dec, m;
+              if (jb < w) {
+                dec = mul(ff[r], end);
+              } else {
+                const int own = 8 * r + fg - (16 * sub + 8 * n + 2 * fq);  // the query's place after the pair's first key
+                dec = mul(ff[r], f2(own >= 0 ? exp2_fast(br[r] - b.x) : 0.f, own > 0 ? exp2_fast(br[r] - b.y) : 0.f));
+              }
+              const F2 at = mul(dec, dp);
+              sr = to_bf16(mul(dec, sc));
+              dr = to_bf16(at);
+              m = mul(at, sc);
+              if (jb == w) {
+                const int own = 8 * r + fg - (16 * sub + 8 * n + 2 * fq);
+                const float2 y = split(m);
+                m = f2(own > 0 ? y.x : 0.f, own > 1 ? y.y : 0.f);
+              }
+              sum[r] = add(sum[r], m);
+              col[n] = r == 0 ? m : add(col[n], m);
+            }
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t at = (row + 16 * h) * 128 + (((4 * blk + 2 * sub + (lane >> 4)) ^ (row & 7)) << 4);
+            wm::stsm(Pt + at, s[sub][h][0], s[sub][h][2], s[sub][h][4], s[sub][h][6]);
+            wm::stsm(At + at, d[sub][h][0], d[sub][h][2], d[sub][h][4], d[sub][h][6]);
+          }
+          // Halves of the four keys to halves of the lanes, twice, and the last two added up.
+          const float2 c0 = split(col[0]), c1 = split(col[1]);
+          const bool up = (lane & 16) != 0, odd = (lane & 8) != 0;
+          const float x = (up ? c1.x : c0.x) + __shfl_xor_sync(0xffffffffu, up ? c0.x : c1.x, 16);
+          const float y = (up ? c1.y : c0.y) + __shfl_xor_sync(0xffffffffu, up ? c0.y : c1.y, 16);
+          float z = (odd ? y : x) + __shfl_xor_sync(0xffffffffu, odd ? x : y, 8);
+          z += __shfl_xor_sync(0xffffffffu, z, 4);
+          if ((lane & 4) == 0) sm.cols[w][32 * jb + 16 * sub + (up ? 8 : 0) + 2 * fq + (odd ? 1 : 0)] = z;
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float2 f = split(sum[r]);
+        float x = f.x + f.y;
+        x += __shfl_xor_sync(0xffffffffu, x, 1);
+        x += __shfl_xor_sync(0xffffffffu, x, 2);
+        if (fq == 0) sm.rows[group][32 * w + 8 * r + fg] = x;
+      }
       fence_proxy_async_smem();
       tc::fence_before();
       asm volatile("bar.sync 1, 256;" ::: "memory");
@@ -1018,6 +1039,7 @@ __global__ void __launch_bounds__(512, 1) k_gs_bwd(const __grid_constant__ BwdTi
       }
     } else {
       mbar_wait(&sm.in, ph, a.status, &sm.abort);
+      if (i > 0) mbar_wait(&sm.sent, ph ^ 1, a.status, &sm.abort);  // dV and dK have left the buffers
       {
         // Half a row of u ⊙ Q each.
         const float u = a.scale * exp2_fast(mine);
@@ -1099,7 +1121,6 @@ __global__ void __launch_bounds__(512, 1) k_gs_bwd(const __grid_constant__ BwdTi
       if (id == 0) {
         tma_store_tile(group == 0 ? &tm_.dq.map : group == 1 ? &tm_.dv.map : &tm_.dk.map, stage, chunk * kL, hi_, bi);
         bulk_commit();
-        bulk_wait_read<0>();
       }
     } else if (warp == 8) {
       // dg over the chunk, four tokens a lane: sums over the tokens from t on of (rows − cols), sums over
@@ -1157,6 +1178,7 @@ __global__ void __launch_bounds__(512, 1) k_gs_bwd(const __grid_constant__ BwdTi
       store_row(S, a.end + ((size_t)pair * kD + id) * kD);
     }
   }
+  if (id == 0) bulk_wait_read<0>();
   __syncthreads();
   if (warp == 4) {
     let_land(&sm.abort);
