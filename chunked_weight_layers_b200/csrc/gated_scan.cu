@@ -188,7 +188,7 @@ __device__ __forceinline__ void weigh(uint32_t x, F2 w, uint32_t& hi, uint32_t& 
 // Token t's row of X (a [128][64] tile), weighted by w, as two bf16 terms into the rows of hi and lo.
 __device__ __forceinline__ void weigh_row(const uint8_t* X, uint8_t* hi, uint8_t* lo, int t, float w) {
   const F2 ww = f2(w, w);
-#pragma unroll 2
+#pragma unroll
   for (int c = 0; c < 8; ++c) {
     const uint32_t at = t * 128 + ((c ^ (t & 7)) << 4);
     const uint4 x = *reinterpret_cast<const uint4*>(X + at);
@@ -227,6 +227,12 @@ __device__ __forceinline__ uint32_t causal(uint32_t pair, int row) {
   uint32_t keep;
   asm("bmsk.clamp.b32 %0, 0, %1;" : "=r"(keep) : "r"(max(row + 1, 0) * 16));
   return pair & keep;
+}
+
+// All N threads of the CTA, from wherever their halves or groups are.
+template <int N>
+__device__ __forceinline__ void cta_sync() {
+  asm volatile("bar.sync 0, %0;" ::"n"(N) : "memory");
 }
 
 __device__ __forceinline__ void group_sync(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
@@ -547,46 +553,17 @@ __global__ void __launch_bounds__(256, 2)
     load_v(0);
   }
   if (warp == 0) tc::alloc(&sm.tmem, kOutCols);
-  F2 S[32];
-  if (!rows_side) {
-    if (warp == 7) {
-      fetch_gates(a, gp, (int64_t)c0 * kL, sm.raw[0], lane);
-      make_gates(sm.raw[0], sm.gates[0], lane);
-      if (n > 1) fetch_gates(a, gp, (int64_t)(c0 + 1) * kL, sm.raw[1], lane);
-    }
-    if (id < 64) {
-      if (a.few) {
-        // Few segments: what those before this one add, in order, onto the initial state.
-        load_row(S, a.start != nullptr ? a.start + ((size_t)pair * kD + id) * kD : nullptr);
-        for (int before = 0; before < seg; ++before) {
-          const size_t at = (size_t)pair * a.nseg + before;
-          const float f = exp2_fast(a.seg_decay[at]);
-          const ulonglong2* x = reinterpret_cast<const ulonglong2*>(a.local + (at * kD + id) * kD);
-#pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            const ulonglong2 y = x[c];
-            S[2 * c] = fma2(f2(f, f), S[2 * c], F2{y.x});
-            S[2 * c + 1] = fma2(f2(f, f), S[2 * c + 1], F2{y.y});
-          }
-        }
-      } else {
-        load_row(S, a.start != nullptr ? a.start + ((size_t)blockIdx.x * kD + id) * kD : nullptr);
-      }
-      put_state_row(sm.S, S, id);
-    }
-  }
-  fence_proxy_async_smem();
-  tc::fence_before();
-  __syncthreads();
-  tc::fence_after();
-  const uint32_t tm = sm.tmem, tmem = tm + ((uint32_t)((warp & 3) * 32) << 16);
-  const uint32_t dq = desc_of(sm.Q), dk = desc_of(sm.K), dv = desc_of(sm.V[0]), ds = desc_of(sm.S),
-                 dw = desc_of(sm.W[0], kLTile);
-
-  for (int i = 0; i < n; ++i) {
-    const int ph = i & 1;
-    const Gates& gt = sm.gates[ph];
-    if (rows_side) {
+  // The two halves run loops of their own, so that the state's registers are not held through the other
+  // half's work; barrier 0 ends each chunk for both.
+  if (rows_side) {
+    tc::fence_before();
+    cta_sync<256>();
+    tc::fence_after();
+    const uint32_t tm = sm.tmem, tmem = tm + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t dq = desc_of(sm.Q), dk = desc_of(sm.K), dv = desc_of(sm.V[0]), ds = desc_of(sm.S);
+    for (int i = 0; i < n; ++i) {
+      const int ph = i & 1;
+      const Gates& gt = sm.gates[ph];
       if (tid == 0) {
         mbar_wait(&sm.qk, ph, a.status, &sm.abort);
 #pragma unroll
@@ -675,7 +652,51 @@ __global__ void __launch_bounds__(256, 2)
         }
       }
       fence_proxy_async_smem();
-    } else {
+      tc::fence_before();
+      cta_sync<256>();
+      tc::fence_after();
+      if (tid == 0) {
+        tma_store_tile(&to.map, sm.V[ph], (c0 + i) * kL, hi_, bi);
+        bulk_commit();
+      }
+    }
+    if (tid == 0) bulk_wait_read<0>();
+  } else {
+    F2 S[32];
+    if (warp == 7) {
+      fetch_gates(a, gp, (int64_t)c0 * kL, sm.raw[0], lane);
+      make_gates(sm.raw[0], sm.gates[0], lane);
+      if (n > 1) fetch_gates(a, gp, (int64_t)(c0 + 1) * kL, sm.raw[1], lane);
+    }
+    if (id < 64) {
+      if (a.few) {
+        // Few segments: what those before this one add, in order, onto the initial state.
+        load_row(S, a.start != nullptr ? a.start + ((size_t)pair * kD + id) * kD : nullptr);
+        for (int before = 0; before < seg; ++before) {
+          const size_t at = (size_t)pair * a.nseg + before;
+          const float f = exp2_fast(a.seg_decay[at]);
+          const ulonglong2* x = reinterpret_cast<const ulonglong2*>(a.local + (at * kD + id) * kD);
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            const ulonglong2 y = x[c];
+            S[2 * c] = fma2(f2(f, f), S[2 * c], F2{y.x});
+            S[2 * c + 1] = fma2(f2(f, f), S[2 * c + 1], F2{y.y});
+          }
+        }
+      } else {
+        load_row(S, a.start != nullptr ? a.start + ((size_t)blockIdx.x * kD + id) * kD : nullptr);
+      }
+      put_state_row(sm.S, S, id);
+    }
+    fence_proxy_async_smem();
+    tc::fence_before();
+    cta_sync<256>();
+    tc::fence_after();
+    const uint32_t tm = sm.tmem, tmem = tm + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t dv = desc_of(sm.V[0]), dw = desc_of(sm.W[0], kLTile);
+    for (int i = 0; i < n; ++i) {
+      const int ph = i & 1;
+      const Gates& gt = sm.gates[ph];
       mbar_wait(&sm.qk, ph, a.status, &sm.abort);
       weigh_row(sm.K, sm.W[0], sm.W[1], id, gt.w[id]);
       fence_proxy_async_smem();
@@ -688,10 +709,6 @@ __global__ void __launch_bounds__(256, 2)
         tc::commit(&sm.added);
       }
       __syncwarp();
-      if (warp == 7 && i + 1 < n) {
-        make_gates(sm.raw[ph ^ 1], sm.gates[ph ^ 1], lane);
-        if (i + 2 < n) fetch_gates(a, gp, (int64_t)(c0 + i + 2) * kL, sm.raw[ph], lane);
-      }
       mbar_wait(&sm.scores, ph, a.status, &sm.abort);  // Q, K and the state's copy have been read
       if (id == 0 && i + 1 < n) load_qk(i + 1);
       __syncwarp();
@@ -699,18 +716,17 @@ __global__ void __launch_bounds__(256, 2)
       tc::fence_after();
       update_state(S, tmem + kColD, sm.W[1], id, exp2_fast(gt.total), 2);
       if (id < 64) put_state_row(sm.S, S, id);
+      if (warp == 7 && i + 1 < n) {
+        make_gates(sm.raw[ph ^ 1], sm.gates[ph ^ 1], lane);
+        if (i + 2 < n) fetch_gates(a, gp, (int64_t)(c0 + i + 2) * kL, sm.raw[ph], lane);
+      }
       fence_proxy_async_smem();
+      tc::fence_before();
+      cta_sync<256>();
+      tc::fence_after();
     }
-    tc::fence_before();
-    __syncthreads();
-    tc::fence_after();
-    if (tid == 0) {
-      tma_store_tile(&to.map, sm.V[ph], (c0 + i) * kL, hi_, bi);
-      bulk_commit();
-    }
+    if (a.end != nullptr && seg == a.nseg - 1 && id < 64) store_row(S, a.end + ((size_t)pair * kD + id) * kD);
   }
-  if (a.end != nullptr && seg == a.nseg - 1 && !rows_side && id < 64) store_row(S, a.end + ((size_t)pair * kD + id) * kD);
-  if (tid == 0) bulk_wait_read<0>();
   __syncthreads();
   if (warp == 0) {
     let_land(&sm.abort);
@@ -758,15 +774,14 @@ __device__ __forceinline__ float scaled_row(F2 (&x)[32], uint32_t tmem, float f,
     tc::wait_ld();
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      const uint4 t = tile != nullptr ? *reinterpret_cast<const uint4*>(tile + r * 128 + (((4 * half + c) ^ (r & 7)) << 4))
-                                      : make_uint4(0, 0, 0, 0);
+      const uint4 t = *reinterpret_cast<const uint4*>(tile + r * 128 + (((4 * half + c) ^ (r & 7)) << 4));
       const uint32_t tw[4] = {t.x, t.y, t.z, t.w};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int j = 8 * c + 2 * e;
         const F2 z = mul(ff, f2u(y[j], y[j + 1]));
         x[16 * half + 4 * c + e] = z;
-        if (tile != nullptr) d = fma2(from_bf16(tw[e]), z, d);
+        d = fma2(from_bf16(tw[e]), z, d);
       }
     }
   }
@@ -812,6 +827,27 @@ __device__ __forceinline__ void put_ds(BwdSmem& sm, const F2 (&S)[32], int id) {
       *reinterpret_cast<uint4*>(sm.dS[1] + at) = make_uint4(l[0], l[1], l[2], l[3]);
     }
   }
+}
+
+// Half a row (16-byte pieces c0 .. c0 + 3) of u ⊙ Q, as two bf16 terms, by groups 2 and 3 together.
+__device__ __forceinline__ void weigh_half(BwdSmem& sm, const GsArgs& a, int id, int c0, float u, int ph, bool later) {
+  mbar_wait(&sm.in, ph, a.status, &sm.abort);
+  if (later) mbar_wait(&sm.sent, ph ^ 1, a.status, &sm.abort);  // dV and dK have left the buffers
+  const F2 uu = f2(u, u);
+#pragma unroll
+  for (int c = c0; c < c0 + 4; ++c) {
+    const uint32_t at = id * 128 + ((c ^ (id & 7)) << 4);
+    const uint4 x = *reinterpret_cast<const uint4*>(sm.Q + at);
+    uint4 h, l;
+    weigh(x.x, uu, h.x, l.x);
+    weigh(x.y, uu, h.y, l.y);
+    weigh(x.z, uu, h.z, l.z);
+    weigh(x.w, uu, h.w, l.w);
+    *reinterpret_cast<uint4*>(sm.W[0] + at) = h;
+    *reinterpret_cast<uint4*>(sm.W[1] + at) = l;
+  }
+  fence_proxy_async_smem();
+  asm volatile("bar.sync 2, 256;" ::: "memory");
 }
 
 struct BwdTiles {
@@ -864,8 +900,10 @@ __global__ void __launch_bounds__(512, 1) k_gs_bwd(const __grid_constant__ BwdTi
   }
   for (int i = tid; i < 4 * kL; i += 512) (&sm.cols[0][0])[i] = 0.f;
   for (int i = tid; i < 2 * kL; i += 512) (&sm.rows[0][0])[i] = 0.f;
-  F2 S[32];  // group 2: the row of dS; groups 0, 1, 3: the gradient's part from beyond the chunk
+  // Group 2 runs a loop of its own, so that dS's registers are not held through the others' work; barrier
+  // 0 joins all groups twice a chunk.
   if (group == 2) {
+    F2 S[32];  // a row of one part of dS
     const bool first = id < 64;
     load_row(S, a.start != nullptr && first ? a.start + ((size_t)(a.few ? pair : blockIdx.x) * kD + id) * kD : nullptr);
     if (a.few && first) {
@@ -887,303 +925,291 @@ __global__ void __launch_bounds__(512, 1) k_gs_bwd(const __grid_constant__ BwdTi
       make_gates(sm.raw[0], sm.gates[0], lane);
       if (n > 1) fetch_gates(a, gp, (int64_t)(c1 - 2) * kL, sm.raw[1], lane);
     }
-  }
-  fence_proxy_async_smem();
-  tc::fence_before();
-  __syncthreads();
-  tc::fence_after();
-  const uint32_t tm = sm.tmem, tmem = tm + ((uint32_t)((warp & 3) * 32) << 16);
-
-  for (int i = 0; i < n; ++i) {
-    const int ph = i & 1, chunk = c1 - 1 - i;
-    const Gates& gt = sm.gates[ph];
-    const float mine = gt.b[id];
-    if (i > 0 && id == 0 && group != 2) {
-      bulk_wait_read<0>();  // the last chunk's gradient has left its buffer (group 0's: used again past the next barrier)
-      if (group != 0) mbar_arrive(&sm.sent);
-    }
-    if (group < 2) {
-      if (tid == 0) {
-        const uint32_t dq = desc_of(sm.Q), dk = desc_of(sm.K), dv = desc_of(sm.V), dg = desc_of(sm.G), ds = desc_of(sm.S[0]),
-                       dd = desc_of(sm.dS[0]);
-        mbar_wait(&sm.in, ph, a.status, &sm.abort);
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk) tc::mma(tm + kColSc, desc_at(dq, kk * 32), desc_at(dk, kk * 32), tc::idesc_bf16(128, 128, 0, 0), kk != 0);
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk) tc::mma(tm + kColDp, desc_at(dg, kk * 32), desc_at(dv, kk * 32), tc::idesc_bf16(128, 128, 0, 0), kk != 0);
-        tc::commit(&sm.scores);
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          tc::mma(tm + kColDqi, desc_at(dg, (kk & 3) * 32), desc_at(ds, (kk >> 2) * kTile + (kk & 3) * 32), tc::idesc_bf16(128, 64, 0, 0), kk != 0);
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          tc::mma(tm + kColDki, desc_at(dv, (kk & 3) * 32), desc_at(dd, (kk >> 2) * kTile + (kk & 3) * 32), tc::idesc_bf16(128, 64, 0, 0), kk != 0);
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk) tc::mma(tm + kColDvi, desc_at(dk, kk * 32), desc_at(dd, kk * 2048), tc::idesc_bf16(128, 64, 0, 1), kk != 0);
-        tc::commit(&sm.inter);
-      }
-      __syncwarp();
-      mbar_wait(&sm.scores, ph, a.status, &sm.abort);
-      tc::fence_after();
-      // Blocks of 32 keys up to this warp's own 32 queries (before them the decay is a product of the
-      // key's to its block's end and the query's from there), 16 keys at a time as matrix fragments: a
-      // lane holds four queries and four keys, so a key's sum over the warp's queries takes four
-      // exchanges for 16 keys, where whole rows in a lane would take 16.
-      const int w = warp & 3, fg = lane >> 2, fq = lane & 3;
-      float br[4];
-      F2 sum[4];
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        br[r] = gt.b[32 * w + 8 * r + fg];
-        sum[r] = f2(0.f, 0.f);
-      }
-      const uint32_t row = 32 * w + (lane & 15), Pt = smem_u32(sm.P[group]), At = smem_u32(sm.A[group]);
-#pragma unroll 1
-      for (int blk = 0; blk < 2; ++blk) {
-        const int jb = 2 * group + blk;
-        if (jb > w) break;
-        uint32_t s[2][2][8], d[2][2][8];  // [16 keys][16 queries]
-#pragma unroll
-        for (int sub = 0; sub < 2; ++sub)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            tc::ld_frag16(tmem + ((uint32_t)(16 * h) << 16) + kColSc + 32 * jb + 16 * sub, s[sub][h]);
-            tc::ld_frag16(tmem + ((uint32_t)(16 * h) << 16) + kColDp + 32 * jb + 16 * sub, d[sub][h]);
-          }
-        F2 ff[4];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const float f = jb < w ? a.scale * exp2_fast(br[r] - gt.b[32 * jb + 31]) : a.scale;
-          ff[r] = f2(f, f);
-        }
-        tc::wait_ld();
-#pragma unroll
-        for (int sub = 0; sub < 2; ++sub) {
-          F2 col[2];
-#pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            const int j = 32 * jb + 16 * sub + 8 * n + 2 * fq;
-            const F2 end = *reinterpret_cast<const F2*>(gt.end + j);
-            const float2 b = *reinterpret_cast<const float2*>(gt.b + j);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              uint32_t& sr = s[sub][r >> 1][4 * n + 2 * (r & 1)];
-              uint32_t& dr = d[sub][r >> 1][4 * n + 2 * (r & 1)];
-              const F2 sc = f2u(sr, s[sub][r >> 1][4 * n + 2 * (r & 1) + 1]), dp = f2u(dr, d[sub][r >> 1][4 * n + 2 * (r & 1) + 1]);
-              F2 dec, m;
-              if (jb < w) {
-                dec = mul(ff[r], end);
-              } else {
-                const int own = 8 * r + fg - (16 * sub + 8 * n + 2 * fq);  // the query's place after the pair's first key
-                dec = mul(ff[r], f2(own >= 0 ? exp2_fast(br[r] - b.x) : 0.f, own > 0 ? exp2_fast(br[r] - b.y) : 0.f));
-              }
-              const F2 at = mul(dec, dp);
-              sr = to_bf16(mul(dec, sc));
-              dr = to_bf16(at);
-              m = mul(at, sc);
-              if (jb == w) {
-                const int own = 8 * r + fg - (16 * sub + 8 * n + 2 * fq);
-                const float2 y = split(m);
-                m = f2(own > 0 ? y.x : 0.f, own > 1 ? y.y : 0.f);
-              }
-              sum[r] = add(sum[r], m);
-              col[n] = r == 0 ? m : add(col[n], m);
-            }
-          }
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t at = (row + 16 * h) * 128 + (((4 * blk + 2 * sub + (lane >> 4)) ^ (row & 7)) << 4);
-            wm::stsm(Pt + at, s[sub][h][0], s[sub][h][2], s[sub][h][4], s[sub][h][6]);
-            wm::stsm(At + at, d[sub][h][0], d[sub][h][2], d[sub][h][4], d[sub][h][6]);
-          }
-          // Halves of the four keys to halves of the lanes, twice, and the last two added up.
-          const float2 c0 = split(col[0]), c1 = split(col[1]);
-          const bool up = (lane & 16) != 0, odd = (lane & 8) != 0;
-          const float x = (up ? c1.x : c0.x) + __shfl_xor_sync(0xffffffffu, up ? c0.x : c1.x, 16);
-          const float y = (up ? c1.y : c0.y) + __shfl_xor_sync(0xffffffffu, up ? c0.y : c1.y, 16);
-          float z = (odd ? y : x) + __shfl_xor_sync(0xffffffffu, odd ? x : y, 8);
-          z += __shfl_xor_sync(0xffffffffu, z, 4);
-          if ((lane & 4) == 0) sm.cols[w][32 * jb + 16 * sub + (up ? 8 : 0) + 2 * fq + (odd ? 1 : 0)] = z;
-        }
-      }
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const float2 f = split(sum[r]);
-        float x = f.x + f.y;
-        x += __shfl_xor_sync(0xffffffffu, x, 1);
-        x += __shfl_xor_sync(0xffffffffu, x, 2);
-        if (fq == 0) sm.rows[group][32 * w + 8 * r + fg] = x;
-      }
-      fence_proxy_async_smem();
-      tc::fence_before();
-      asm volatile("bar.sync 1, 256;" ::: "memory");
-      if (tid == 0) {
-        tc::fence_after();
-        const uint32_t dp = desc_of(sm.P[0], kLTile), da = desc_of(sm.A[0], kLTile), dak = desc_of(sm.A[0]), dq = desc_of(sm.Q),
-                       dk = desc_of(sm.K), dg = desc_of(sm.G);
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          tc::mma(tm + kColDq, desc_at(dak, (kk >> 2) * kLTile + (kk & 3) * 32), desc_at(dk, kk * 2048), tc::idesc_bf16(128, 64, 0, 1), kk != 0);
-        outer_mma(tm + kColDv, dp, dg);
-        outer_mma(tm + kColDk, da, dq);
-        tc::commit(&sm.grads);
-      }
-      __syncwarp();
-      mbar_wait(&sm.in, ph, a.status, &sm.abort);  // this thread reads Q itself
-      mbar_wait(&sm.inter, ph, a.status, &sm.abort);
-      tc::fence_after();
-      if (group == 0) {
-        sm.far[id] = scaled_row(S, tmem + kColDqi, a.scale * exp2_fast(mine), sm.Q, id);
-      } else {
-        scaled_row(S, tmem + kColDvi, gt.w[id], nullptr, id);
-      }
-    } else {
-      mbar_wait(&sm.in, ph, a.status, &sm.abort);
-      if (i > 0) mbar_wait(&sm.sent, ph ^ 1, a.status, &sm.abort);  // dV and dK have left the buffers
-      {
-        // Half a row of u ⊙ Q each.
-        const float u = a.scale * exp2_fast(mine);
-        const F2 uu = f2(u, u);
-#pragma unroll 2
-        for (int c = 4 * (group - 2); c < 4 * (group - 2) + 4; ++c) {
-          const uint32_t at = id * 128 + ((c ^ (id & 7)) << 4);
-          const uint4 x = *reinterpret_cast<const uint4*>(sm.Q + at);
-          uint4 h, l;
-          weigh(x.x, uu, h.x, l.x);
-          weigh(x.y, uu, h.y, l.y);
-          weigh(x.z, uu, h.z, l.z);
-          weigh(x.w, uu, h.w, l.w);
-          *reinterpret_cast<uint4*>(sm.W[0] + at) = h;
-          *reinterpret_cast<uint4*>(sm.W[1] + at) = l;
-        }
-      }
-      fence_proxy_async_smem();
-      asm volatile("bar.sync 2, 256;" ::: "memory");
-      if (tid == 256) {
+    fence_proxy_async_smem();
+    tc::fence_before();
+    cta_sync<512>();
+    tc::fence_after();
+    const uint32_t tm = sm.tmem, tmem = tm + ((uint32_t)((warp & 3) * 32) << 16);
+    for (int i = 0; i < n; ++i) {
+      const int ph = i & 1, chunk = c1 - 1 - i;
+      const Gates& gt = sm.gates[ph];
+      weigh_half(sm, a, id, 0, a.scale * exp2_fast(gt.b[id]), ph, i > 0);
+      if (id == 0) {
         outer_mma(tm + kColDs, desc_of(sm.W[0], kLTile), desc_of(sm.G));
         tc::commit(&sm.added);
       }
       __syncwarp();
-      if (group == 2) {
-        const float keep = exp2_fast(gt.total);
-        F2 d = f2(0.f, 0.f);
-        const int r = id & 63;
+      const float keep = exp2_fast(gt.total);
+      F2 d = f2(0.f, 0.f);
+      const int r = id & 63;
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          const uint32_t at = r * 128 + ((c ^ (r & 7)) << 4);
-          const uint4 x = *reinterpret_cast<const uint4*>(sm.S[0] + at), y = *reinterpret_cast<const uint4*>(sm.S[1] + at);
-          d = fma2(S[4 * c], add(from_bf16(x.x), from_bf16(y.x)), d);
-          d = fma2(S[4 * c + 1], add(from_bf16(x.y), from_bf16(y.y)), d);
-          d = fma2(S[4 * c + 2], add(from_bf16(x.z), from_bf16(y.z)), d);
-          d = fma2(S[4 * c + 3], add(from_bf16(x.w), from_bf16(y.w)), d);
+      for (int c = 0; c < 8; ++c) {
+        const uint32_t at = r * 128 + ((c ^ (r & 7)) << 4);
+        const uint4 x = *reinterpret_cast<const uint4*>(sm.S[0] + at), y = *reinterpret_cast<const uint4*>(sm.S[1] + at);
+        d = fma2(S[4 * c], add(from_bf16(x.x), from_bf16(y.x)), d);
+        d = fma2(S[4 * c + 1], add(from_bf16(x.y), from_bf16(y.y)), d);
+        d = fma2(S[4 * c + 2], add(from_bf16(x.z), from_bf16(y.z)), d);
+        d = fma2(S[4 * c + 3], add(from_bf16(x.w), from_bf16(y.w)), d);
+      }
+      const float2 dd = split(d);
+      float dot = dd.x + dd.y;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+      if (lane == 0) sm.dot[warp & 3] = keep * dot;
+      mbar_wait(&sm.added, ph, a.status, &sm.abort);
+      tc::fence_after();
+      const F2 kk = f2(keep, keep);
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t y[32];
+        tc::ld32(tmem + kColDs + 32 * half, y);
+        tc::wait_ld();
+#pragma unroll
+        for (int c = 0; c < 16; ++c) S[16 * half + c] = fma2(kk, S[16 * half + c], f2u(y[2 * c], y[2 * c + 1]));
+      }
+      mbar_wait(&sm.inter, ph, a.status, &sm.abort);  // dS' has been read
+      put_ds(sm, S, id);
+      fence_proxy_async_smem();
+      if (warp == 11 && i + 1 < n) {
+        make_gates(sm.raw[(i + 1) % 3], sm.gates[ph ^ 1], lane);
+        if (i + 2 < n) fetch_gates(a, gp, (int64_t)(chunk - 2) * kL, sm.raw[(i + 2) % 3], lane);
+      }
+      tc::fence_before();
+      cta_sync<512>();
+      tc::fence_after();
+      if (warp == 8) {
+        // dg over the chunk, four tokens a lane: sums over the tokens from t on of (rows − cols), sums over
+        // those before t of past.
+        float4 s = *reinterpret_cast<const float4*>(sm.rows[0] + 4 * lane);
+        const float4 s1 = *reinterpret_cast<const float4*>(sm.rows[1] + 4 * lane), f = *reinterpret_cast<const float4*>(sm.far + 4 * lane),
+                     p = *reinterpret_cast<const float4*>(sm.past + 4 * lane), raw = *reinterpret_cast<const float4*>(sm.raw[i % 3] + 4 * lane);
+        s.x += s1.x + f.x, s.y += s1.y + f.y, s.z += s1.z + f.z, s.w += s1.w + f.w;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float4 c = *reinterpret_cast<const float4*>(sm.cols[q] + 4 * lane);
+          s.x -= c.x, s.y -= c.y, s.z -= c.z, s.w -= c.w;
         }
-        const float2 dd = split(d);
-        float dot = dd.x + dd.y;
+        s.z += s.w, s.y += s.z, s.x += s.y;
+        float after = s.x, before = (p.x + p.y) + (p.z + p.w);
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-        if (lane == 0) sm.dot[warp & 3] = keep * dot;
-        mbar_wait(&sm.added, ph, a.status, &sm.abort);
-        tc::fence_after();
-        const F2 kk = f2(keep, keep);
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t y[32];
-          tc::ld32(tmem + kColDs + 32 * half, y);
-          tc::wait_ld();
-#pragma unroll
-          for (int c = 0; c < 16; ++c) S[16 * half + c] = fma2(kk, S[16 * half + c], f2u(y[2 * c], y[2 * c + 1]));
+        for (int o = 1; o < 32; o <<= 1) {
+          const float y = __shfl_down_sync(0xffffffffu, after, o), z = __shfl_up_sync(0xffffffffu, before, o);
+          if (lane + o < 32) after += y;
+          if (lane >= o) before += z;
         }
-        mbar_wait(&sm.inter, ph, a.status, &sm.abort);  // dS' has been read
-        put_ds(sm, S, id);
-        fence_proxy_async_smem();
-        if (warp == 11 && i + 1 < n) {
-          make_gates(sm.raw[(i + 1) % 3], sm.gates[ph ^ 1], lane);
-          if (i + 2 < n) fetch_gates(a, gp, (int64_t)(chunk - 2) * kL, sm.raw[(i + 2) % 3], lane);
+        after = __shfl_down_sync(0xffffffffu, after, 1);
+        before = __shfl_up_sync(0xffffffffu, before, 1);
+        const float all = (sm.dot[0] + sm.dot[1]) + (sm.dot[2] + sm.dot[3]);
+        const float base = all + (lane == 31 ? 0.f : after) + (lane == 0 ? 0.f : before);
+        const float v[4] = {base + s.x, base + s.y + p.x, base + s.z + (p.x + p.y), base + s.w + (p.x + p.y + p.z)};
+        const float g[4] = {raw.x, raw.y, raw.z, raw.w};
+        const int64_t t0 = (int64_t)chunk * kL + 4 * lane;
+        float* dg = a.dg + (size_t)pair * a.T + t0;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (t0 + q < a.T) dg[q] = g[q] < kGoneGate ? 0.f : v[q];  // where the gate's factor is 0 in fp32 so is its derivative
+      }
+      tc::fence_before();
+      cta_sync<512>();
+      tc::fence_after();
+    }
+    if (a.end != nullptr && seg == 0) {
+      float4* at = reinterpret_cast<float4*>(sm.P[0]) + (id & 63) * 16;  // the products are done
+      if (id >= 64) {
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          const float2 x = split(S[2 * c]), y = split(S[2 * c + 1]);
+          at[c ^ (id & 7)] = make_float4(x.x, x.y, y.x, y.y);
         }
-      } else {
-        mbar_wait(&sm.inter, ph, a.status, &sm.abort);
-        tc::fence_after();
-        sm.past[id] = scaled_row(S, tmem + kColDki, gt.w[id], sm.K, id);
+      }
+      group_sync(3);
+      if (id < 64) {
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          const float4 x = at[c ^ (id & 7)];
+          S[2 * c] = add(S[2 * c], f2(x.x, x.y));
+          S[2 * c + 1] = add(S[2 * c + 1], f2(x.z, x.w));
+        }
+        store_row(S, a.end + ((size_t)pair * kD + id) * kD);
       }
     }
+  } else {
+    fence_proxy_async_smem();
     tc::fence_before();
-    __syncthreads();  // the chunk's tiles have been read but by the products still running
+    cta_sync<512>();
     tc::fence_after();
-    if (group != 2) {
+    const uint32_t tm = sm.tmem, tmem = tm + ((uint32_t)((warp & 3) * 32) << 16);
+    for (int i = 0; i < n; ++i) {
+      const int ph = i & 1, chunk = c1 - 1 - i;
+      const Gates& gt = sm.gates[ph];
+      const float mine = gt.b[id];
+      if (i > 0 && id == 0) {
+        bulk_wait_read<0>();  // the last chunk's gradient has left its buffer (group 0's: used again past the next barrier)
+        if (group != 0) mbar_arrive(&sm.sent);
+      }
+      if (group < 2) {
+        if (tid == 0) {
+          const uint32_t dq = desc_of(sm.Q), dk = desc_of(sm.K), dv = desc_of(sm.V), dg = desc_of(sm.G), ds = desc_of(sm.S[0]),
+                         dd = desc_of(sm.dS[0]);
+          mbar_wait(&sm.in, ph, a.status, &sm.abort);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) tc::mma(tm + kColSc, desc_at(dq, kk * 32), desc_at(dk, kk * 32), tc::idesc_bf16(128, 128, 0, 0), kk != 0);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) tc::mma(tm + kColDp, desc_at(dg, kk * 32), desc_at(dv, kk * 32), tc::idesc_bf16(128, 128, 0, 0), kk != 0);
+          tc::commit(&sm.scores);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            tc::mma(tm + kColDqi, desc_at(dg, (kk & 3) * 32), desc_at(ds, (kk >> 2) * kTile + (kk & 3) * 32), tc::idesc_bf16(128, 64, 0, 0), kk != 0);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            tc::mma(tm + kColDki, desc_at(dv, (kk & 3) * 32), desc_at(dd, (kk >> 2) * kTile + (kk & 3) * 32), tc::idesc_bf16(128, 64, 0, 0), kk != 0);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) tc::mma(tm + kColDvi, desc_at(dk, kk * 32), desc_at(dd, kk * 2048), tc::idesc_bf16(128, 64, 0, 1), kk != 0);
+          tc::commit(&sm.inter);
+        }
+        __syncwarp();
+        // Blocks of 32 keys up to this warp's own 32 queries (before them the decay is a product of the
+        // key's to its block's end and the query's from there), 16 keys at a time as matrix fragments: a
+        // lane holds four queries and four keys, so a key's sum over the warp's queries takes four
+        // exchanges for 16 keys, where whole rows in a lane would take 16.
+        const int w = warp & 3, fg = lane >> 2, fq = lane & 3;
+        float br[4];
+        F2 sum[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          br[r] = gt.b[32 * w + 8 * r + fg];
+          sum[r] = f2(0.f, 0.f);
+        }
+        mbar_wait(&sm.scores, ph, a.status, &sm.abort);
+        tc::fence_after();
+        const uint32_t row = 32 * w + (lane & 15), Pt = smem_u32(sm.P[group]), At = smem_u32(sm.A[group]);
+#pragma unroll 1
+        for (int blk = 0; blk < 2; ++blk) {
+          const int jb = 2 * group + blk;
+          if (jb > w) break;
+          uint32_t s[2][2][8], d[2][2][8];  // [16 keys][16 queries]
+#pragma unroll
+          for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              tc::ld_frag16(tmem + ((uint32_t)(16 * h) << 16) + kColSc + 32 * jb + 16 * sub, s[sub][h]);
+              tc::ld_frag16(tmem + ((uint32_t)(16 * h) << 16) + kColDp + 32 * jb + 16 * sub, d[sub][h]);
+            }
+          F2 dec[2][2][4];  // the decays, scaled: [16 keys][8 keys][queries]
+          if (jb < w) {
+            const float end = gt.b[32 * jb + 31];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const float f = a.scale * exp2_fast(br[r] - end);
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+                dec[c >> 1][c & 1][r] = mul(f2(f, f), *reinterpret_cast<const F2*>(gt.end + 32 * jb + 8 * c + 2 * fq));
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const float2 b = *reinterpret_cast<const float2*>(gt.b + 32 * jb + 8 * c + 2 * fq);
+#pragma unroll
+              for (int r = 0; r < 4; ++r) {
+                const int own = 8 * (r - c) + fg - 2 * fq;  // the query's place after the pair's first key
+                dec[c >> 1][c & 1][r] = f2(own >= 0 ? a.scale * exp2_fast(br[r] - b.x) : 0.f, own > 0 ? a.scale * exp2_fast(br[r] - b.y) : 0.f);
+              }
+            }
+          }
+          tc::wait_ld();
+#pragma unroll
+          for (int sub = 0; sub < 2; ++sub) {
+            F2 col[2];
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+              for (int r = 0; r < 4; ++r) {
+                uint32_t* sp = &s[sub][r >> 1][4 * n + 2 * (r & 1)];
+                uint32_t* dp = &d[sub][r >> 1][4 * n + 2 * (r & 1)];
+                const F2 sc = f2u(sp[0], sp[1]), at = mul(dec[sub][n][r], f2u(dp[0], dp[1]));
+                sp[0] = to_bf16(mul(dec[sub][n][r], sc));
+                dp[0] = to_bf16(at);
+                // A token's own pair is in its row's and its column's sum alike, and drops out of dg.
+                const F2 m = mul(at, sc);
+                sum[r] = add(sum[r], m);
+                col[n] = r == 0 ? m : add(col[n], m);
+              }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t at = (row + 16 * h) * 128 + (((4 * blk + 2 * sub + (lane >> 4)) ^ (row & 7)) << 4);
+              wm::stsm(Pt + at, s[sub][h][0], s[sub][h][2], s[sub][h][4], s[sub][h][6]);
+              wm::stsm(At + at, d[sub][h][0], d[sub][h][2], d[sub][h][4], d[sub][h][6]);
+            }
+            // Halves of the four keys to halves of the lanes, twice, and the last two added up.
+            const float2 c0 = split(col[0]), c1 = split(col[1]);
+            const bool up = (lane & 16) != 0, odd = (lane & 8) != 0;
+            const float x = (up ? c1.x : c0.x) + __shfl_xor_sync(0xffffffffu, up ? c0.x : c1.x, 16);
+            const float y = (up ? c1.y : c0.y) + __shfl_xor_sync(0xffffffffu, up ? c0.y : c1.y, 16);
+            float z = (odd ? y : x) + __shfl_xor_sync(0xffffffffu, odd ? x : y, 8);
+            z += __shfl_xor_sync(0xffffffffu, z, 4);
+            if ((lane & 4) == 0) sm.cols[w][32 * jb + 16 * sub + (up ? 8 : 0) + 2 * fq + (odd ? 1 : 0)] = z;
+          }
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float2 f = split(sum[r]);
+          float x = f.x + f.y;
+          x += __shfl_xor_sync(0xffffffffu, x, 1);
+          x += __shfl_xor_sync(0xffffffffu, x, 2);
+          if (fq == 0) sm.rows[group][32 * w + 8 * r + fg] = x;
+        }
+        fence_proxy_async_smem();
+        tc::fence_before();
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        if (tid == 0) {
+          tc::fence_after();
+          const uint32_t dp = desc_of(sm.P[0], kLTile), da = desc_of(sm.A[0], kLTile), dak = desc_of(sm.A[0]), dq = desc_of(sm.Q),
+                         dk = desc_of(sm.K), dg = desc_of(sm.G);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            tc::mma(tm + kColDq, desc_at(dak, (kk >> 2) * kLTile + (kk & 3) * 32), desc_at(dk, kk * 2048), tc::idesc_bf16(128, 64, 0, 1), kk != 0);
+          outer_mma(tm + kColDv, dp, dg);
+          outer_mma(tm + kColDk, da, dq);
+          tc::commit(&sm.grads);
+        }
+        __syncwarp();
+      } else {
+        weigh_half(sm, a, id, 4, a.scale * exp2_fast(mine), ph, i > 0);
+      }
+      mbar_wait(&sm.in, ph, a.status, &sm.abort);  // this thread reads Q or K itself
+      mbar_wait(&sm.inter, ph, a.status, &sm.abort);
+      tc::fence_after();
+      F2 x[32];  // the gradient's part from beyond the chunk
+      const float dot = scaled_row(x, tmem + (group == 0 ? kColDqi : group == 1 ? kColDvi : kColDki),
+                                   group == 0 ? a.scale * exp2_fast(mine) : gt.w[id], group == 0 ? sm.Q : sm.K, id);
+      if (group == 0) sm.far[id] = dot;
+      if (group == 3) sm.past[id] = dot;
+      tc::fence_before();
+      cta_sync<512>();  // the chunk's tiles have been read but by the products still running
+      tc::fence_after();
       mbar_wait(&sm.grads, ph, a.status, &sm.abort);
       tc::fence_after();
       if (tid == 0 && i + 1 < n) load(i + 1);
       __syncwarp();
       uint8_t* stage = group == 0 ? sm.out : group == 1 ? sm.W[0] : sm.W[1];
-      finish_row(S, tmem + (group == 0 ? kColDq : group == 1 ? kColDv : kColDk), stage, id);
+      finish_row(x, tmem + (group == 0 ? kColDq : group == 1 ? kColDv : kColDk), stage, id);
       fence_proxy_async_smem();
       group_sync(4 + group);
       if (id == 0) {
         tma_store_tile(group == 0 ? &tm_.dq.map : group == 1 ? &tm_.dv.map : &tm_.dk.map, stage, chunk * kL, hi_, bi);
         bulk_commit();
       }
-    } else if (warp == 8) {
-      // dg over the chunk, four tokens a lane: sums over the tokens from t on of (rows − cols), sums over
-      // those before t of past.
-      float4 s = *reinterpret_cast<const float4*>(sm.rows[0] + 4 * lane);
-      const float4 s1 = *reinterpret_cast<const float4*>(sm.rows[1] + 4 * lane), f = *reinterpret_cast<const float4*>(sm.far + 4 * lane),
-                   p = *reinterpret_cast<const float4*>(sm.past + 4 * lane), raw = *reinterpret_cast<const float4*>(sm.raw[i % 3] + 4 * lane);
-      s.x += s1.x + f.x, s.y += s1.y + f.y, s.z += s1.z + f.z, s.w += s1.w + f.w;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const float4 c = *reinterpret_cast<const float4*>(sm.cols[q] + 4 * lane);
-        s.x -= c.x, s.y -= c.y, s.z -= c.z, s.w -= c.w;
-      }
-      s.z += s.w, s.y += s.z, s.x += s.y;
-      float after = s.x, before = (p.x + p.y) + (p.z + p.w);
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const float y = __shfl_down_sync(0xffffffffu, after, o), z = __shfl_up_sync(0xffffffffu, before, o);
-        if (lane + o < 32) after += y;
-        if (lane >= o) before += z;
-      }
-      after = __shfl_down_sync(0xffffffffu, after, 1);
-      before = __shfl_up_sync(0xffffffffu, before, 1);
-      const float all = (sm.dot[0] + sm.dot[1]) + (sm.dot[2] + sm.dot[3]);
-      const float base = all + (lane == 31 ? 0.f : after) + (lane == 0 ? 0.f : before);
-      const float v[4] = {base + s.x, base + s.y + p.x, base + s.z + (p.x + p.y), base + s.w + (p.x + p.y + p.z)};
-      const float g[4] = {raw.x, raw.y, raw.z, raw.w};
-      const int64_t t0 = (int64_t)chunk * kL + 4 * lane;
-      float* dg = a.dg + (size_t)pair * a.T + t0;
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (t0 + q < a.T) dg[q] = g[q] < kGoneGate ? 0.f : v[q];  // where the gate's factor is 0 in fp32 so is its derivative
+      tc::fence_before();
+      cta_sync<512>();
+      tc::fence_after();
     }
-    tc::fence_before();
-    __syncthreads();
-    tc::fence_after();
+    if (id == 0) bulk_wait_read<0>();
   }
-  if (a.end != nullptr && seg == 0 && group == 2) {
-    float4* at = reinterpret_cast<float4*>(sm.P[0]) + (id & 63) * 16;  // the products are done
-    if (id >= 64) {
-#pragma unroll
-      for (int c = 0; c < 16; ++c) {
-        const float2 x = split(S[2 * c]), y = split(S[2 * c + 1]);
-        at[c ^ (id & 7)] = make_float4(x.x, x.y, y.x, y.y);
-      }
-    }
-    group_sync(3);
-    if (id < 64) {
-#pragma unroll
-      for (int c = 0; c < 16; ++c) {
-        const float4 x = at[c ^ (id & 7)];
-        S[2 * c] = add(S[2 * c], f2(x.x, x.y));
-        S[2 * c + 1] = add(S[2 * c + 1], f2(x.z, x.w));
-      }
-      store_row(S, a.end + ((size_t)pair * kD + id) * kD);
-    }
-  }
-  if (id == 0) bulk_wait_read<0>();
   __syncthreads();
   if (warp == 4) {
     let_land(&sm.abort);
     __syncwarp();
-    tc::dealloc(tm, 512);
+    tc::dealloc(sm.tmem, 512);
   }
 }
 
