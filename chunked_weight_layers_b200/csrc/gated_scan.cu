@@ -308,6 +308,13 @@ __device__ __forceinline__ void tma_load_tile(void* dst, const CUtensorMap* map,
       : "memory");
 }
 
+// Brings the tile into L2.
+__device__ __forceinline__ void tma_prefetch_tile(const CUtensorMap* map, int t, int h, int b) {
+  asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global [%0, {%1, %2, %3, %4}];" ::"l"(reinterpret_cast<uint64_t>(map)), "r"(0),
+               "r"(t), "r"(h), "r"(b)
+               : "memory");
+}
+
 __device__ __forceinline__ void tma_store_tile(const CUtensorMap* map, const void* src, int t, int h, int b) {
   asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%2, %3, %4, %5}], [%1];" ::"l"(
                    reinterpret_cast<uint64_t>(map)),
@@ -881,6 +888,14 @@ __global__ void __launch_bounds__(512, 1) k_gs_bwd(const __grid_constant__ BwdTi
     tma_load_tile(sm.V, &tm_.v.map, &sm.in, t, hi_ * tm_.v.head, bi * tm_.v.batch);
     tma_load_tile(sm.S[0], &tm_.s.map, &sm.in, t, hi_, bi);  // both planes: 128 rows a chunk
   };
+  auto prefetch = [&](int i) {
+    const int t = (c1 - 1 - i) * kL;
+    tma_prefetch_tile(&tm_.q.map, t, hi_ * tm_.q.head, bi * tm_.q.batch);
+    tma_prefetch_tile(&tm_.k.map, t, hi_ * tm_.k.head, bi * tm_.k.batch);
+    tma_prefetch_tile(&tm_.g.map, t, hi_ * tm_.g.head, bi * tm_.g.batch);
+    tma_prefetch_tile(&tm_.v.map, t, hi_ * tm_.v.head, bi * tm_.v.batch);
+    tma_prefetch_tile(&tm_.s.map, t, hi_, bi);
+  };
   if (tid == 0) {
     mbar_init(&sm.in, 1);
     mbar_init(&sm.scores, 1);
@@ -933,6 +948,10 @@ __global__ void __launch_bounds__(512, 1) k_gs_bwd(const __grid_constant__ BwdTi
     for (int i = 0; i < n; ++i) {
       const int ph = i & 1, chunk = c1 - 1 - i;
       const Gates& gt = sm.gates[ph];
+      // The next chunk's tiles have no room here yet: they come to L2 meanwhile (loaded from HBM when this
+      // chunk is done they took 6500 cycles of the chunk's 12000, all SMs asking at once).
+      if (id == 32 && i + 1 < n) prefetch(i + 1);
+      __syncwarp();
       weigh_half(sm, a, id, 0, a.scale * exp2_fast(gt.b[id]), ph, i > 0);
       if (id == 0) {
         outer_mma(tm + kColDs, desc_of(sm.W[0], kLTile), desc_of(sm.G));
@@ -1043,12 +1062,14 @@ __global__ void __launch_bounds__(512, 1) k_gs_bwd(const __grid_constant__ BwdTi
       const int ph = i & 1, chunk = c1 - 1 - i;
       const Gates& gt = sm.gates[ph];
       const float mine = gt.b[id];
-      if (i > 0 && id == 0) {
-        bulk_wait_read<0>();  // the last chunk's gradient has left its buffer (group 0's: used again past the next barrier)
-        if (group != 0) mbar_arrive(&sm.sent);
+      if (i > 0 && group != 0 && id == 32) {
+        bulk_wait_read<0>();  // the last chunk's gradient has left the buffer
+        mbar_arrive(&sm.sent);
       }
       if (group < 2) {
-        if (tid == 0) {
+        // Warp 4 has no scores to weigh (its queries come before group 1's keys): it issues the products,
+        // which holds it for as long as they run.
+        if (tid == 128) {
           const uint32_t dq = desc_of(sm.Q), dk = desc_of(sm.K), dv = desc_of(sm.V), dg = desc_of(sm.G), ds = desc_of(sm.S[0]),
                          dd = desc_of(sm.dS[0]);
           mbar_wait(&sm.in, ph, a.status, &sm.abort);
@@ -1161,7 +1182,7 @@ __global__ void __launch_bounds__(512, 1) k_gs_bwd(const __grid_constant__ BwdTi
         fence_proxy_async_smem();
         tc::fence_before();
         asm volatile("bar.sync 1, 256;" ::: "memory");
-        if (tid == 0) {
+        if (tid == 128) {
           tc::fence_after();
           const uint32_t dp = desc_of(sm.P[0], kLTile), da = desc_of(sm.A[0], kLTile), dak = desc_of(sm.A[0]), dq = desc_of(sm.Q),
                          dk = desc_of(sm.K), dg = desc_of(sm.G);
@@ -1182,20 +1203,23 @@ __global__ void __launch_bounds__(512, 1) k_gs_bwd(const __grid_constant__ BwdTi
       F2 x[32];  // the gradient's part from beyond the chunk
       const float dot = scaled_row(x, tmem + (group == 0 ? kColDqi : group == 1 ? kColDvi : kColDki),
                                    group == 0 ? a.scale * exp2_fast(mine) : gt.w[id], group == 0 ? sm.Q : sm.K, id);
-      if (group == 0) sm.far[id] = dot;
+      if (group == 0) {
+        sm.far[id] = dot;
+        if (id == 32) bulk_wait_read<0>();  // the last chunk's dQ has left its buffer
+      }
       if (group == 3) sm.past[id] = dot;
       tc::fence_before();
       cta_sync<512>();  // the chunk's tiles have been read but by the products still running
       tc::fence_after();
       mbar_wait(&sm.grads, ph, a.status, &sm.abort);
       tc::fence_after();
-      if (tid == 0 && i + 1 < n) load(i + 1);
+      if (tid == 128 && i + 1 < n) load(i + 1);
       __syncwarp();
       uint8_t* stage = group == 0 ? sm.out : group == 1 ? sm.W[0] : sm.W[1];
       finish_row(x, tmem + (group == 0 ? kColDq : group == 1 ? kColDv : kColDk), stage, id);
       fence_proxy_async_smem();
       group_sync(4 + group);
-      if (id == 0) {
+      if (id == 32) {
         tma_store_tile(group == 0 ? &tm_.dq.map : group == 1 ? &tm_.dv.map : &tm_.dk.map, stage, chunk * kL, hi_, bi);
         bulk_commit();
       }
@@ -1203,7 +1227,7 @@ __global__ void __launch_bounds__(512, 1) k_gs_bwd(const __grid_constant__ BwdTi
       cta_sync<512>();
       tc::fence_after();
     }
-    if (id == 0) bulk_wait_read<0>();
+    if (id == 32) bulk_wait_read<0>();
   }
   __syncthreads();
   if (warp == 4) {
