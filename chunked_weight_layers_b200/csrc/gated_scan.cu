@@ -339,21 +339,82 @@ __device__ __forceinline__ void let_land(const volatile int* abort) {
 }
 
 struct __align__(1024) SegSmem {
-  uint8_t X[2][kLTile], Y[2][kLTile];
-  uint8_t W[2][kLTile];  // the weighted X, two terms
+  uint8_t X[2][kLTile];  // X; once weighed, the first term of w ⊙ X
+  uint8_t L[2][kLTile];  // the second term
+  uint8_t Y[2][kLTile];
   uint8_t swap[kTile];   // CKPT: the second terms' part of the state, 2^-9 of it, rounded to bf16
-  Gates gates[2];
+  Gates gates[3];
   __align__(16) float raw[2][kL];
-  uint64_t full[2], done[2], taken[2];
+  uint64_t full[2], done[2];
   uint32_t tmem;
   int abort;
 };
 
+// Adds what outer_mma left in TMEM onto a row of one part of the state: S ← keep·S + sums.
+__device__ __forceinline__ void take_sums(F2 (&S)[32], uint32_t tmem, float keep) {
+  const F2 k = f2(keep, keep);
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    uint32_t d[32];
+    tc::ld32(tmem + 32 * half, d);
+    tc::wait_ld();
+#pragma unroll
+    for (int c = 0; c < 16; ++c) S[16 * half + c] = fma2(k, S[16 * half + c], f2u(d[2 * c], d[2 * c + 1]));
+  }
+}
+
+// The two parts of a state, rows of the first in threads 0 .. 63 of a group and of the second in 64 .. 127,
+// added up in the first through `swap` (16 KB), in fp32.
+__device__ __forceinline__ void join_parts(F2 (&S)[32], uint8_t* swap, int id, int bar) {
+  float4* at = reinterpret_cast<float4*>(swap) + (id & 63) * 16;
+  if (id >= 64) {
+#pragma unroll
+    for (int c = 0; c < 16; ++c) {
+      const float2 x = split(S[2 * c]), y = split(S[2 * c + 1]);
+      at[c ^ (id & 7)] = make_float4(x.x, x.y, y.x, y.y);
+    }
+  }
+  group_sync(bar);
+  if (id < 64) {
+#pragma unroll
+    for (int c = 0; c < 16; ++c) {
+      const float4 x = at[c ^ (id & 7)];
+      S[2 * c] = add(S[2 * c], f2(x.x, x.y));
+      S[2 * c + 1] = add(S[2 * c + 1], f2(x.z, x.w));
+    }
+  }
+}
+
+// The two parts added up and rounded to bf16 twice, the value and what that rounding left, eight pairs of
+// pieces at a time to put(16-byte piece, value, rest); the second part comes through `swap` in bf16 (it is
+// 2^-9 of the state).
+template <class Put>
+__device__ __forceinline__ void split_parts(const F2 (&S)[32], uint8_t* swap, int id, int bar, Put put) {
+  if (id >= 64) put_state_row(swap, S, id & 63);
+  group_sync(bar);
+  if (id < 64) {
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      const uint4 x = *reinterpret_cast<const uint4*>(swap + id * 128 + ((c ^ (id & 7)) << 4));
+      const uint32_t second[4] = {x.x, x.y, x.z, x.w};
+      uint32_t h[4], l[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const F2 both = add(S[4 * c + e], from_bf16(second[e]));
+        h[e] = to_bf16(both);
+        l[e] = to_bf16(fma2(from_bf16(h[e]), f2(-1.f, -1.f), both));
+      }
+      put(c, make_uint4(h[0], h[1], h[2], h[3]), make_uint4(l[0], l[1], l[2], l[3]));
+    }
+  }
+}
+
 // Runs the state alone over a segment. Forward: X = K, Y = V, weights w; REV: from the last chunk to
-// the first, X = Q, Y = dO, weights scale·2^b. Threads 0 .. 127 weigh a row of X each and hand the tile to
-// the tensor cores, threads 128 .. 255 add the results (two sets of TMEM columns) to a row of the state
-// each, rows 0 .. 63 the first terms' part of it and 64 .. 127 the second's, which are added at the end.
-// CKPT: writes the state before every chunk, as two bf16 planes (forward). grid: pairs · nseg.
+// the first, X = Q, Y = dO, weights scale·2^b. All 256 threads weigh half a row of X each, and the tensor
+// cores take the tile while the next is weighed; threads 128 .. 255 add the sums of the chunk before (two
+// sets of TMEM columns) to a row of the state each, rows 0 .. 63 the first terms' part of it and 64 .. 127
+// the second's, which are added at the end. CKPT: writes the state before every chunk, as two bf16 planes
+// (forward). grid: pairs · nseg.
 template <bool REV, bool CKPT>
 __global__ void __launch_bounds__(256, 2)
     k_gs_segment(const __grid_constant__ Tiles tx, const __grid_constant__ Tiles ty, const GsArgs a) {
@@ -372,130 +433,112 @@ __global__ void __launch_bounds__(256, 2)
     tma_load_tile(sm.X[i & 1], &tx.map, bar, chunk_of(i) * kL, hi_ * tx.head, bi * tx.batch);
     tma_load_tile(sm.Y[i & 1], &ty.map, bar, chunk_of(i) * kL, hi_ * ty.head, bi * ty.batch);
   };
+  auto prefetch = [&](int i) {
+    tma_prefetch_tile(&tx.map, chunk_of(i) * kL, hi_ * tx.head, bi * tx.batch);
+    tma_prefetch_tile(&ty.map, chunk_of(i) * kL, hi_ * ty.head, bi * ty.batch);
+  };
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.full[i], 1);
       mbar_init(&sm.done[i], 1);
-      mbar_init(&sm.taken[i], 128);
     }
     sm.abort = 0;
     fence_barrier_init();
     load(0);
     if (n > 1) load(1);
+    if (n > 2) prefetch(2);
   }
   if (warp == 4) tc::alloc(&sm.tmem, 128);
-  F2 S[32];
   if (warp == 3) {
     fetch_gates(a, gp, (int64_t)chunk_of(0) * kL, sm.raw[0], lane);
     make_gates(sm.raw[0], sm.gates[0], lane);
     if (n > 1) fetch_gates(a, gp, (int64_t)chunk_of(1) * kL, sm.raw[1], lane);
-  } else if (warp >= 4) {
-    load_row(S, a.start != nullptr && id < 64 ? a.start + ((size_t)blockIdx.x * kD + id) * kD : nullptr);
   }
+  // Half a row of chunk i's X: its first term in place, its second beside.
+  auto weigh_chunk = [&](int i) {
+    const int ph = i & 1, c0_ = 4 * (tid >> 7);
+    const Gates& gt = sm.gates[i % 3];
+    const float w = REV ? a.scale * exp2_fast(gt.b[id]) : gt.w[id];
+    const F2 ww = f2(w, w);
+    mbar_wait(&sm.full[ph], (i >> 1) & 1, a.status, &sm.abort);
+#pragma unroll
+    for (int c = c0_; c < c0_ + 4; ++c) {
+      const uint32_t at = id * 128 + ((c ^ (id & 7)) << 4);
+      const uint4 x = *reinterpret_cast<const uint4*>(sm.X[ph] + at);
+      uint4 h, l;
+      weigh(x.x, ww, h.x, l.x);
+      weigh(x.y, ww, h.y, l.y);
+      weigh(x.z, ww, h.z, l.z);
+      weigh(x.w, ww, h.w, l.w);
+      *reinterpret_cast<uint4*>(sm.X[ph] + at) = h;
+      *reinterpret_cast<uint4*>(sm.L[ph] + at) = l;
+    }
+    fence_proxy_async_smem();
+  };
   tc::fence_before();
-  __syncthreads();
+  cta_sync<256>();
   tc::fence_after();
   if (warp < 4) {
-    const uint32_t dw = desc_of(sm.W[0], kLTile), dy = desc_of(sm.Y[0]);
+    const uint32_t tm = sm.tmem, dx = desc_of(sm.X[0], 2 * kLTile), dy = desc_of(sm.Y[0]);
     for (int i = 0; i < n; ++i) {
       const int ph = i & 1;
-      const Gates& gt = sm.gates[ph];
-      const float w = REV ? a.scale * exp2_fast(gt.b[id]) : gt.w[id];
-      mbar_wait(&sm.full[ph], (i >> 1) & 1, a.status, &sm.abort);
-      if (i > 0) {
-        // The products of the chunk before have read W, and its X and Y.
-        mbar_wait(&sm.done[ph ^ 1], ((i - 1) >> 1) & 1, a.status, &sm.abort);
-        if (tid == 0 && i + 1 < n) load(i + 1);
-        __syncwarp();
-      }
-      weigh_row(sm.X[ph], sm.W[0], sm.W[1], id, w);
-      fence_proxy_async_smem();
-      group_sync(1);
+      weigh_chunk(i);
+      cta_sync<256>();  // also: the sums two chunks back have been taken
       if (tid == 0) {
-        if (i > 1) {
-          mbar_wait(&sm.taken[ph], ((i - 2) >> 1) & 1, a.status, &sm.abort);
-          tc::fence_after();
-        }
-        outer_mma(sm.tmem + 64 * ph, dw, dy + ph * (kLTile >> 4));
+        tc::fence_after();
+        outer_mma(tm + 64 * ph, dx + ph * (kLTile >> 4), dy + ph * (kLTile >> 4));
         tc::commit(&sm.done[ph]);
       }
-      __syncwarp();
       if (warp == 3 && i + 1 < n) {
-        // The other gates' last readers, the state's threads, have taken the chunk before.
-        if (i > 0) mbar_wait(&sm.taken[ph ^ 1], ((i - 1) >> 1) & 1, a.status, &sm.abort);
-        make_gates(sm.raw[ph ^ 1], sm.gates[ph ^ 1], lane);
+        make_gates(sm.raw[ph ^ 1], sm.gates[(i + 1) % 3], lane);
         if (i + 2 < n) fetch_gates(a, gp, (int64_t)chunk_of(i + 2) * kL, sm.raw[ph], lane);
       }
       group_sync(1);  // the next chunk's gates are there
+      if (warp == 3) asm volatile("bar.arrive 3, 160;" ::: "memory");
     }
   } else {
     const uint32_t tmem = sm.tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    F2 S[32];
+    load_row(S, a.start != nullptr && id < 64 ? a.start + ((size_t)blockIdx.x * kD + id) * kD : nullptr);
     float decay = 0.f;
-    for (int i = 0; i < n; ++i) {
-      const int ph = i & 1;
-      if (CKPT) {
-        // Both parts of a row of the state, through shared memory, to its first part's thread.
-        if (id >= 64) put_state_row(sm.swap, S, id & 63);
-        group_sync(2);
-        if (id < 64) {
-          __nv_bfloat16* p = a.ckpt + ((size_t)pair * a.nchunk + chunk_of(i)) * 2 * kState + id * kD;
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            const uint4 x = *reinterpret_cast<const uint4*>(sm.swap + id * 128 + ((c ^ (id & 7)) << 4));
-            const uint32_t second[4] = {x.x, x.y, x.z, x.w};
-            uint32_t h[4], l[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const F2 both = add(S[4 * c + e], from_bf16(second[e]));
-              h[e] = to_bf16(both);
-              l[e] = to_bf16(fma2(from_bf16(h[e]), f2(-1.f, -1.f), both));
-            }
-            reinterpret_cast<uint4*>(p)[c] = make_uint4(h[0], h[1], h[2], h[3]);
-            reinterpret_cast<uint4*>(p + kState)[c] = make_uint4(l[0], l[1], l[2], l[3]);
-          }
+    for (int i = 0; i <= n; ++i) {
+      if (i < n) {
+        if (i > 0) asm volatile("bar.sync 3, 160;" ::: "memory");  // this chunk's gates are there
+        weigh_chunk(i);
+        tc::fence_before();
+        cta_sync<256>();
+      }
+      if (i > 0) {
+        const int last = (i - 1) & 1;
+        mbar_wait(&sm.done[last], ((i - 1) >> 1) & 1, a.status, &sm.abort);
+        tc::fence_after();
+        if (id == 0 && i + 1 < n) {
+          load(i + 1);  // the tiles of the chunk before have been read
+          if (i + 2 < n) prefetch(i + 2);
         }
+        __syncwarp();
+        const float total = sm.gates[(i - 1) % 3].total;
+        take_sums(S, tmem + 64 * last, exp2_fast(total));
+        decay += total;
+      }
+      if (CKPT && i < n) {
+        __nv_bfloat16* p = a.ckpt + ((size_t)pair * a.nchunk + chunk_of(i)) * 2 * kState + (id & 63) * kD;
+        split_parts(S, sm.swap, id, 2, [&](int c, uint4 h, uint4 l) {
+          reinterpret_cast<uint4*>(p)[c] = h;
+          reinterpret_cast<uint4*>(p + kState)[c] = l;
+        });
         group_sync(2);
       }
-      mbar_wait(&sm.done[ph], (i >> 1) & 1, a.status, &sm.abort);
-      tc::fence_after();
-      const float total = sm.gates[ph].total, keep = exp2_fast(total);
-      const F2 kk = f2(keep, keep);
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        uint32_t d[32];
-        tc::ld32(tmem + 64 * ph + 32 * half, d);
-        tc::wait_ld();
-#pragma unroll
-        for (int c = 0; c < 16; ++c) S[16 * half + c] = fma2(kk, S[16 * half + c], f2u(d[2 * c], d[2 * c + 1]));
-      }
-      tc::fence_before();
-      mbar_arrive(&sm.taken[ph]);
-      decay += total;
     }
+    asm volatile("bar.sync 3, 160;" ::: "memory");
     if (a.local != nullptr) {
-      float4* at = reinterpret_cast<float4*>(sm.W[0]) + (id & 63) * 16;  // the products are done
-      if (id >= 64) {
-#pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          const float2 x = split(S[2 * c]), y = split(S[2 * c + 1]);
-          at[c ^ (id & 7)] = make_float4(x.x, x.y, y.x, y.y);
-        }
-      }
-      group_sync(2);
-      if (id < 64) {
-#pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          const float4 x = at[c ^ (id & 7)];
-          S[2 * c] = add(S[2 * c], f2(x.x, x.y));
-          S[2 * c + 1] = add(S[2 * c + 1], f2(x.z, x.w));
-        }
-        store_row(S, a.local + ((size_t)blockIdx.x * kD + id) * kD);
-      }
+      join_parts(S, sm.X[0], id, 2);  // the products are done
+      if (id < 64) store_row(S, a.local + ((size_t)blockIdx.x * kD + id) * kD);
       if (id == 0) a.seg_decay[blockIdx.x] = decay;
     }
   }
   tc::fence_before();
-  __syncthreads();
+  cta_sync<256>();
   tc::fence_after();
   if (warp == 4) {
     let_land(&sm.abort);
@@ -813,27 +856,13 @@ __device__ __forceinline__ void finish_row(const F2 (&x)[32], uint32_t tmem, uin
   }
 }
 
-// A row of dS, its two parts in the threads id and id + 64, as two bf16 terms into the tiles' rows.
+// dS as two bf16 terms into the tiles.
 __device__ __forceinline__ void put_ds(BwdSmem& sm, const F2 (&S)[32], int id) {
-  if (id >= 64) put_state_row(sm.swap, S, id & 63);
-  group_sync(3);
-  if (id < 64) {
-#pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      const uint32_t at = id * 128 + ((c ^ (id & 7)) << 4);
-      const uint4 x = *reinterpret_cast<const uint4*>(sm.swap + at);
-      const uint32_t second[4] = {x.x, x.y, x.z, x.w};
-      uint32_t h[4], l[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const F2 both = add(S[4 * c + e], from_bf16(second[e]));
-        h[e] = to_bf16(both);
-        l[e] = to_bf16(fma2(from_bf16(h[e]), f2(-1.f, -1.f), both));
-      }
-      *reinterpret_cast<uint4*>(sm.dS[0] + at) = make_uint4(h[0], h[1], h[2], h[3]);
-      *reinterpret_cast<uint4*>(sm.dS[1] + at) = make_uint4(l[0], l[1], l[2], l[3]);
-    }
-  }
+  split_parts(S, sm.swap, id, 3, [&](int c, uint4 h, uint4 l) {
+    const uint32_t at = id * 128 + ((c ^ (id & 7)) << 4);
+    *reinterpret_cast<uint4*>(sm.dS[0] + at) = h;
+    *reinterpret_cast<uint4*>(sm.dS[1] + at) = l;
+  });
 }
 
 // Half a row (16-byte pieces c0 .. c0 + 3) of u ⊙ Q, as two bf16 terms, by groups 2 and 3 together.
@@ -977,15 +1006,7 @@ __global__ void __launch_bounds__(512, 1) k_gs_bwd(const __grid_constant__ BwdTi
       if (lane == 0) sm.dot[warp & 3] = keep * dot;
       mbar_wait(&sm.added, ph, a.status, &sm.abort);
       tc::fence_after();
-      const F2 kk = f2(keep, keep);
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        uint32_t y[32];
-        tc::ld32(tmem + kColDs + 32 * half, y);
-        tc::wait_ld();
-#pragma unroll
-        for (int c = 0; c < 16; ++c) S[16 * half + c] = fma2(kk, S[16 * half + c], f2u(y[2 * c], y[2 * c + 1]));
-      }
+      take_sums(S, tmem + kColDs, keep);
       mbar_wait(&sm.inter, ph, a.status, &sm.abort);  // dS' has been read
       put_ds(sm, S, id);
       fence_proxy_async_smem();
@@ -1033,24 +1054,8 @@ __global__ void __launch_bounds__(512, 1) k_gs_bwd(const __grid_constant__ BwdTi
       tc::fence_after();
     }
     if (a.end != nullptr && seg == 0) {
-      float4* at = reinterpret_cast<float4*>(sm.P[0]) + (id & 63) * 16;  // the products are done
-      if (id >= 64) {
-#pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          const float2 x = split(S[2 * c]), y = split(S[2 * c + 1]);
-          at[c ^ (id & 7)] = make_float4(x.x, x.y, y.x, y.y);
-        }
-      }
-      group_sync(3);
-      if (id < 64) {
-#pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          const float4 x = at[c ^ (id & 7)];
-          S[2 * c] = add(S[2 * c], f2(x.x, x.y));
-          S[2 * c + 1] = add(S[2 * c + 1], f2(x.z, x.w));
-        }
-        store_row(S, a.end + ((size_t)pair * kD + id) * kD);
-      }
+      join_parts(S, sm.P[0], id, 3);  // the products are done
+      if (id < 64) store_row(S, a.end + ((size_t)pair * kD + id) * kD);
     }
   } else {
     fence_proxy_async_smem();
