@@ -23,7 +23,7 @@
 // round into as many parts as there are pairs, whose fp32 results a small launch adds in order.
 // Sizes need not be multiples of the tiles: TMA reads zeros past the ends, stores are clipped.
 //
-// k_ffn_few takes up to 32 tokens, where the weights' bytes are all that counts: see there.
+// k_ffn_few takes up to 16 tokens, where the weights' bytes are all that counts: see there.
 #include <algorithm>
 
 #include "internal.h"
@@ -59,6 +59,7 @@ struct FfnArgs {
   int kblocks;        // k-blocks of one product (DX: of each of the two)
   int tiles_m, tiles_n;
   int cols;           // FWD: columns of f in a tile, a multiple of 8 up to 128
+  int rows;           // FWD, DX: tokens of a tile that each CTA takes, a multiple of 8 up to 128 (DW: 128)
   int whole;          // tiles whose sum one pair makes alone: the first of the order
   int splits, per_split;  // parts of the sums of the tiles after them, and k-blocks of a part
   int act;
@@ -184,15 +185,15 @@ __global__ void __launch_bounds__(kFThreads, 1)
           }
           uint8_t *sa = sm.ring[s], *sb = sa + kHalf;
           // Both CTAs' loads complete on the first CTA's barrier, which expects the bytes of both.
-          if (rank == 0) mbar_arrive_expect_tx(&sm.full[s], 2 * kHalf + 2 * bcols * FK * 2);
+          if (rank == 0) mbar_arrive_expect_tx(&sm.full[s], 2 * (a.rows + bcols) * FK * 2);
           const uint32_t bar = pair::in_first(&sm.full[s]);
           if constexpr (MODE == FWD) {
-            pair::load_2d(sa, &tmA0, bar, kb * FK, m * kTileM + rank * FM);
+            pair::load_2d(sa, &tmA0, bar, kb * FK, (2 * m + rank) * a.rows);
             pair::load_2d(sb, rank ? &tmB1 : &tmB0, bar, kb * FK, n * a.cols);
           } else if constexpr (MODE == DX) {
             const bool up = kb >= a.kblocks;
             const int k = (up ? kb - a.kblocks : kb) * FK;
-            pair::load_2d(sa, up ? &tmA1 : &tmA0, bar, k, m * kTileM + rank * FM);
+            pair::load_2d(sa, up ? &tmA1 : &tmA0, bar, k, (2 * m + rank) * a.rows);
             for (int j = 0; j < 2; ++j)
               pair::load_2d(sb + j * (kHalf / 2), up ? &tmB1 : &tmB0, bar, n * kTileN + rank * FM + 64 * j, k);
           } else {
@@ -220,6 +221,8 @@ __global__ void __launch_bounds__(kFThreads, 1)
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
       const uint32_t idesc = tc::idesc_bf16(kTileM, 2 * bcols, MODE == DW, MODE != FWD);
+      // K-major operands step along their rows, MN-major ones (64 columns a box, 8192 bytes) down them.
+      const uint32_t da = tc::desc_of(sm.ring[0], MODE == DW ? 8192 : 16), db = tc::desc_of(sm.ring[0] + kHalf, MODE == FWD ? 16 : 8192);
       uint32_t it = 0, tcount = 0;
       bool ok = true;
       for (int t = me; t < units && ok; t += npairs) {
@@ -237,13 +240,11 @@ __global__ void __launch_bounds__(kFThreads, 1)
             break;
           }
           tc::fence_after();
-          const uint32_t a0 = smem_u32(sm.ring[s]), b0 = a0 + kHalf;
+          const uint32_t ad = da + s * (2 * kHalf >> 4), bd = db + s * (2 * kHalf >> 4);
 #pragma unroll
-          for (int kk = 0; kk < FK / 16; ++kk) {
-            const uint64_t ad = MODE == DW ? tc::smem_desc(a0 + kk * 2048, 8192, 1024) : tc::smem_desc(a0 + kk * 32, 16, 1024);
-            const uint64_t bd = MODE == FWD ? tc::smem_desc(b0 + kk * 32, 16, 1024) : tc::smem_desc(b0 + kk * 2048, 8192, 1024);
-            pair::mma(tmem + acc * kTileN, ad, bd, idesc, (kb != un.k0 || kk != 0));
-          }
+          for (int kk = 0; kk < FK / 16; ++kk)
+            pair::mma(tmem + acc * kTileN, tc::desc_at(ad, kk * (MODE == DW ? 2048 : 32)), tc::desc_at(bd, kk * (MODE == FWD ? 32 : 2048)),
+                      idesc, (kb != un.k0 || kk != 0));
           pair::commit(&sm.empty[s]);
         }
         if (!ok) break;
@@ -267,7 +268,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
       if (!__all_sync(0xffffffffu, ok)) break;
       tc::fence_after();
       const uint32_t tb = tmem + ((uint32_t)(lq * 32) << 16) + (uint32_t)(acc * kTileN);
-      int row0 = un.m * kTileM + rank * FM + lq * 32;
+      int row0 = (2 * un.m + rank) * a.rows + lq * 32, row_end = min(a.M, (2 * un.m + rank + 1) * a.rows);
       if constexpr (MODE == FWD) {
         const int col_end = min(a.N, (un.n + 1) * a.cols);
 #pragma unroll 1
@@ -284,8 +285,8 @@ __global__ void __launch_bounds__(kFThreads, 1)
             u[i] = __uint_as_float(ru[i]);
           }
           if (a.g != nullptr) {
-            store_tile(stage, lane, g, a.g, a.N, row0, a.M, col, col_end);
-            store_tile(stage, lane, u, a.u, a.N, row0, a.M, col, col_end);
+            store_tile(stage, lane, g, a.g, a.N, row0, row_end, col, col_end);
+            store_tile(stage, lane, u, a.u, a.N, row0, row_end, col, col_end);
           }
           if (a.act == TTT_ACT_SILU) {
 #pragma unroll
@@ -294,7 +295,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
 #pragma unroll
             for (int i = 0; i < 32; ++i) g[i] = g[i] * normal_cdf(g[i]) * u[i];
           }
-          store_tile(stage, lane, g, a.z, a.N, row0, a.M, col, col_end);
+          store_tile(stage, lane, g, a.z, a.N, row0, row_end, col, col_end);
         }
       } else {
         __nv_bfloat16* out = a.z;
@@ -302,6 +303,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
           const int half_m = a.tiles_m / 2;
           out = un.m >= half_m ? a.u : a.g;
           row0 -= un.m >= half_m ? half_m * kTileM : 0;
+          row_end = a.M;
         }
 #pragma unroll 1
         for (int c = half * 32; c < kTileN; c += 64) {
@@ -316,7 +318,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
             float v[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-            store_tile(stage, lane, v, out, a.N, row0, a.M, un.n * kTileN + c, a.N);
+            store_tile(stage, lane, v, out, a.N, row0, row_end, un.n * kTileN + c, a.N);
           }
         }
       }
@@ -342,7 +344,8 @@ __global__ void __launch_bounds__(256) k_ffn_join(const FfnArgs a) {
   const Unit un = unit_at(a, a.whole + blockIdx.y * a.splits, 0);
   const int r = blockIdx.x * 8 + (threadIdx.x >> 5), c = (threadIdx.x & 31) * 8;
   __nv_bfloat16* out = a.z;
-  int row = un.m * kTileM + r;
+  int row = (2 * un.m + r / FM) * a.rows + r % FM;
+  if (r % FM >= a.rows) return;
   if (MODE == DW) {
     const int half_m = a.tiles_m / 2;
     out = un.m >= half_m ? a.u : a.g;
@@ -400,10 +403,10 @@ __global__ void __launch_bounds__(256) k_ffn_act_bwd(const __nv_bfloat16* __rest
   *reinterpret_cast<uint4*>(du + i) = make_uint4(b4[0], b4[1], b4[2], b4[3]);
 }
 
-// ---- up to 32 tokens -------------------------------------------------------------------------
+// ---- up to 16 tokens -------------------------------------------------------------------------
 
 // The weights' bytes bound it, so they go from HBM straight into the registers that the tensor
-// cores read (mma.sync: with at most 32 columns its rate is far from counting), with no stage in
+// cores read (mma.sync: with at most 16 columns its rate is far from counting), with no stage in
 // shared memory and no barrier on the way. A CTA of four warps takes eight rows of Wg and the same
 // eight of Wu as the 16 rows of one product, so a thread ends with g and u of the same outputs; warp
 // w takes every fourth 32-wide slice of the sum, the next slices' loads in flight while it works on
@@ -427,7 +430,7 @@ __global__ void __launch_bounds__(32 * kFewWarps) k_ffn_few(const __nv_bfloat16*
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
   const int f0 = blockIdx.x * 8;  // f is a multiple of 8
   const int steps = (d + 31) / 32;
-  constexpr int UN = NT == 4 ? 2 : 4;
+  constexpr int UN = 2;  // slices in flight: more take registers from the warps that hide the latency (4: 22 us, 2: 17)
   const __nv_bfloat16* pg = Wg + (size_t)(f0 + g) * d + 8 * q;
   const __nv_bfloat16* pu = Wu + (size_t)(f0 + g) * d + 8 * q;
   const __nv_bfloat16* px = X + (size_t)g * d + 8 * q;
@@ -510,17 +513,21 @@ int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
 int pairs_of(int num_sms) { return std::max(1, num_sms / 2); }
 
+// Tokens of a tile that each CTA of the pair takes: the fewest, in steps of eight, that cover them in this
+// many tiles, rather than 128 and the rest past the end (17 x 2560 x 9728: 31 us instead of 42; 777 x 1000 x
+// 2744: 16.4 instead of 17.3).
+int rows_of(int64_t T, int tiles_m) { return 8 * cdiv(T, 16 * (int64_t)tiles_m); }
+
 // Columns of f in a forward tile. The pairs take `rounds` tiles each; a k-block of a tile costs the
-// loads of its 128 rows and c columns a CTA (2·(128 + c) cycles at the 64 bytes a cycle that an SM
-// takes in; at c = 128 the 512 cycles that its products take as well), and a tile some 1500
-// cycles besides. The fewest cycles win: 777 x 1000 x 2744 takes two rounds of 80 columns instead of
+// loads of its rows and c columns a CTA (about three cycles each) or the products (4·c cycles), and a tile
+// some 1500 cycles besides. The fewest cycles win: 777 x 1000 x 2744 takes two rounds of 80 columns instead of
 // two of 128.
-int columns_of(int tiles_m, int f, int kblocks, int num_sms) {
+int columns_of(int tiles_m, int rows, int f, int kblocks, int num_sms) {
   int best = kTileN / 2;
   double least = 0;
   for (int c = kTileN / 2; c >= 32; c -= 8) {
     const int rounds = cdiv((int64_t)tiles_m * cdiv(f, c), pairs_of(num_sms));
-    const double cost = (double)rounds * (kblocks * 2.0 * (128 + c) + 1500);
+    const double cost = (double)rounds * (kblocks * std::max(4.0 * c, 3.0 * (rows + c)) + 1500);
     if (c == kTileN / 2 || cost < least) {
       best = c;
       least = cost;
@@ -550,6 +557,7 @@ void plan_dx(FfnArgs& a, int64_t T, int d, int f, int num_sms) {
   a.N = d;
   a.kblocks = cdiv(f, FK);
   a.tiles_m = cdiv(T, kTileM);
+  a.rows = rows_of(T, a.tiles_m);
   a.tiles_n = cdiv(d, kTileN);
   plan_parts(a, 2 * a.kblocks, num_sms);
 }
@@ -559,6 +567,7 @@ void plan_dw(FfnArgs& a, int64_t T, int d, int f, int num_sms) {
   a.N = d;
   a.kblocks = cdiv(T, FK);
   a.tiles_m = 2 * cdiv(f, kTileM);
+  a.rows = FM;
   a.tiles_n = cdiv(d, kTileN);
   plan_parts(a, a.kblocks, num_sms);
 }
@@ -601,14 +610,12 @@ ttt_status gated_ffn(const void* X, const void* Wg, const void* Wu, int64_t T, i
   const __nv_bfloat16 *x = static_cast<const __nv_bfloat16*>(X), *wg = static_cast<const __nv_bfloat16*>(Wg),
                       *wu = static_cast<const __nv_bfloat16*>(Wu);
   __nv_bfloat16 *z = static_cast<__nv_bfloat16*>(Z), *g = static_cast<__nv_bfloat16*>(G), *u = static_cast<__nv_bfloat16*>(U);
-  if (T <= 32) {
+  if (T <= 16) {
     const int grid = f / 8, threads = 32 * kFewWarps;
     if (T <= 8)
       k_ffn_few<1><<<grid, threads, 0, s>>>(x, wg, wu, (int)T, d, f, act, z, g, u);
-    else if (T <= 16)
-      k_ffn_few<2><<<grid, threads, 0, s>>>(x, wg, wu, (int)T, d, f, act, z, g, u);
     else
-      k_ffn_few<4><<<grid, threads, 0, s>>>(x, wg, wu, (int)T, d, f, act, z, g, u);
+      k_ffn_few<2><<<grid, threads, 0, s>>>(x, wg, wu, (int)T, d, f, act, z, g, u);
     TTT_CUDA(cudaGetLastError());
     return TTT_OK;
   }
@@ -617,12 +624,13 @@ ttt_status gated_ffn(const void* X, const void* Wg, const void* Wu, int64_t T, i
   a.N = f;
   a.kblocks = cdiv(d, FK);
   a.tiles_m = cdiv(T, kTileM);
-  a.cols = columns_of(a.tiles_m, f, a.kblocks, num_sms);
+  a.rows = rows_of(T, a.tiles_m);
+  a.cols = columns_of(a.tiles_m, a.rows, f, a.kblocks, num_sms);
   a.tiles_n = cdiv(f, a.cols);
   a.whole = a.tiles_m * a.tiles_n;
   a.splits = 1;
   CUtensorMap tx, tg, tu;
-  TTT_TRY(map_bf16(&tx, X, d, T, FK, FM));
+  TTT_TRY(map_bf16(&tx, X, d, T, FK, a.rows));
   TTT_TRY(map_bf16(&tg, Wg, d, f, FK, a.cols));
   TTT_TRY(map_bf16(&tu, Wu, d, f, FK, a.cols));
   a.per_split = a.kblocks;
@@ -662,11 +670,11 @@ ttt_status gated_ffn_backward(const void* dZ, const void* X, const void* Wg, con
   a.part = part;
   CUtensorMap A0, A1, B0, B1;
   if (dX != nullptr) {
-    TTT_TRY(map_bf16(&A0, dg, f, T, FK, FM));
-    TTT_TRY(map_bf16(&A1, du, f, T, FK, FM));
+    plan_dx(a, T, d, f, num_sms);
+    TTT_TRY(map_bf16(&A0, dg, f, T, FK, a.rows));
+    TTT_TRY(map_bf16(&A1, du, f, T, FK, a.rows));
     TTT_TRY(map_bf16(&B0, Wg, d, f, 64, FK));
     TTT_TRY(map_bf16(&B1, Wu, d, f, 64, FK));
-    plan_dx(a, T, d, f, num_sms);
     a.z = static_cast<__nv_bfloat16*>(dX);
     TTT_TRY(launch_pair<DX>(A0, A1, B0, B1, a, num_sms, s));
   }

@@ -202,16 +202,8 @@ __device__ __forceinline__ void weigh_row(const uint8_t* X, uint8_t* hi, uint8_t
   }
 }
 
-// The low half of a tile's shared-memory descriptor (address and leading offset); moving along the tile
-// adds to it, and the other half (1024 bytes between groups of eight rows, 128-byte swizzle) is the same
-// for all. Building whole descriptors before every product took the issuing thread 140 cycles each.
-__device__ __forceinline__ uint32_t desc_of(const void* tile, uint32_t lbo = 16) {
-  return ((smem_u32(tile) & 0x3FFFFu) >> 4) | ((lbo >> 4) << 16);
-}
-__device__ __forceinline__ uint64_t desc_at(uint32_t low, int bytes) {
-  constexpr uint64_t high = (uint64_t)((1024u >> 4) | (1u << 14) | (2u << 29)) << 32;
-  return high | (low + (uint32_t)(bytes >> 4));
-}
+using tc::desc_at;
+using tc::desc_of;
 
 // [XW_hi | XW_lo]ᵀ·Y over 128 tokens into 64 TMEM columns: rows 0 .. 63 the first term's sums, 64 .. 127
 // the second's. Both operands MN-major (xw with the distance of the two terms' tiles).
