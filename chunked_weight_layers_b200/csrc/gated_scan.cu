@@ -58,9 +58,9 @@ struct GsArgs {
   int64_t gb, gh, gt;
   const float* start;                 // [pairs][nseg or 1][64][64] states the segments start from, or null (zero)
   float* end;                         // final state [pairs][64][64] (the last segment's), or null
-  float* local;                       // what each segment adds [pairs][nseg][64][64]
-  int few;                            // the outputs' CTAs combine `local` themselves (start: one state a pair)
-  float* seg_decay;                   // sums of the segments' gates, base-2 units [pairs][nseg]
+  int few;                            // start holds one state a pair: the CTAs add the segments' on their own
+  float* local[2];                    // what each segment adds [pairs][nseg][64][64], forward and in reverse
+  float* seg_decay[2];                // sums of the segments' gates, base-2 units [pairs][nseg]
   __nv_bfloat16* ckpt;                // state before every chunk, as two bf16 planes [pairs][nchunk][2][64][64]
   float* dg;                          // dense [pairs][T]
   DevStatus status;
@@ -75,29 +75,30 @@ __device__ __forceinline__ float exp2_fast(float x) {
 // ---- states --------------------------------------------------------------------------------
 
 // The states the segments start from, in place of what they add: start[s + 1] =
-// 2^decay[s]·start[s] + local[s], from `first` (or zero); REV: start[s − 1] from start[s]. One element
-// a thread, 16 segments' loads in flight. grid (pairs, 64·64 / 128).
-template <bool REV>
-__global__ void __launch_bounds__(128) k_gs_combine(float* local, const float* __restrict__ decay,
-                                                    const float* __restrict__ first, int nseg) {
+// 2^decay[s]·start[s] + local[s], from `first` (or zero); in reverse start[s − 1] from start[s]. One element
+// a thread, 16 segments' loads in flight. grid (pairs, 64·64 / 128, directions).
+__global__ void __launch_bounds__(128) k_gs_combine(const GsArgs a, const float* first_fwd, const float* first_rev) {
   constexpr int kAhead = 16;
-  const int at = blockIdx.y * 128 + threadIdx.x;
+  const int at = blockIdx.y * 128 + threadIdx.x, rev = blockIdx.z, nseg = a.nseg;
   const size_t pair = blockIdx.x;
+  const float* first = rev ? first_rev : first_fwd;
+  float* p = a.local[rev] + pair * nseg * kState + at;
+  const float* d = a.seg_decay[rev] + pair * nseg;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   float s = first != nullptr ? first[pair * kState + at] : 0.f;
-  float* p = local + pair * nseg * kState + at;
-  const float* d = decay + pair * nseg;
   for (int i0 = 0; i0 < nseg; i0 += kAhead) {
     float x[kAhead], f[kAhead];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      const int seg = REV ? nseg - 1 - (i0 + i) : i0 + i;
+      const int seg = rev ? nseg - 1 - (i0 + i) : i0 + i;
       const bool in = i0 + i < nseg;
       x[i] = in ? p[(size_t)seg * kState] : 0.f;
       f[i] = in ? d[seg] : 0.f;
     }
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      const int seg = REV ? nseg - 1 - (i0 + i) : i0 + i;
+      const int seg = rev ? nseg - 1 - (i0 + i) : i0 + i;
       if (i0 + i < nseg) p[(size_t)seg * kState] = s;
       s = fmaf(exp2_fast(f[i]), s, x[i]);
     }
@@ -282,6 +283,32 @@ __device__ __forceinline__ void store_row(const F2 (&S)[32], float* p) {
   }
 }
 
+// Row `id` of the state that a segment starts from. With few segments: what those before it add (REV: those
+// after it), in order, onto the pair's state.
+template <bool REV>
+__device__ __forceinline__ void load_start(F2 (&S)[32], const GsArgs& a, int pair, int seg, int id) {
+  load_row(S, a.start != nullptr ? a.start + ((size_t)(a.few ? pair : pair * a.nseg + seg) * kD + id) * kD : nullptr);
+  if (!a.few) return;
+  for (int i = REV ? a.nseg - 1 : 0; REV ? i > seg : i < seg; i += REV ? -1 : 1) {
+    const size_t at = (size_t)pair * a.nseg + i;
+    const float f = exp2_fast(a.seg_decay[REV][at]);
+    const F2 ff = f2(f, f);
+    const ulonglong2* x = reinterpret_cast<const ulonglong2*>(a.local[REV] + (at * kD + id) * kD);
+#pragma unroll
+    for (int c = 0; c < 16; ++c) {
+      const ulonglong2 y = x[c];
+      S[2 * c] = fma2(ff, S[2 * c], F2{y.x});
+      S[2 * c + 1] = fma2(ff, S[2 * c + 1], F2{y.y});
+    }
+  }
+}
+
+// Launched beside the end of the launch before it (programmatic dependent launch): until before_results()
+// returns, only what was there before that launch may be read, and nothing written. may_follow(): the
+// next launch's CTAs may start where there is room.
+__device__ __forceinline__ void before_results() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void may_follow() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // Row r of a state, rounded to bf16, into a [64][64] tile.
 __device__ __forceinline__ void put_state_row(uint8_t* tile, const F2 (&S)[32], int r) {
 #pragma unroll
@@ -401,24 +428,30 @@ __device__ __forceinline__ void split_parts(const F2 (&S)[32], uint8_t* swap, in
   }
 }
 
-// Runs the state alone over a segment. Forward: X = K, Y = V, weights w; REV: from the last chunk to
-// the first, X = Q, Y = dO, weights scale·2^b. All 256 threads weigh half a row of X each, and the tensor
+// Runs the state alone over a segment. Forward: X = K, Y = V, weights w; in reverse, from the last chunk to
+// the first: X = Q, Y = dO, weights scale·2^b. All 256 threads weigh half a row of X each, and the tensor
 // cores take the tile while the next is weighed; threads 128 .. 255 add the sums of the chunk before (two
 // sets of TMEM columns) to a row of the state each, rows 0 .. 63 the first terms' part of it and 64 .. 127
 // the second's, which are added at the end. CKPT: writes the state before every chunk, as two bf16 planes
-// (forward). grid: pairs · nseg.
-template <bool REV, bool CKPT>
-__global__ void __launch_bounds__(256, 2)
-    k_gs_segment(const __grid_constant__ Tiles tx, const __grid_constant__ Tiles ty, const GsArgs a) {
+// (forward). grid (pairs · nseg, directions).
+struct SegTiles {
+  Tiles x[2], y[2];
+};
+
+template <bool CKPT>
+__global__ void __launch_bounds__(256, 2) k_gs_segment(const __grid_constant__ SegTiles tiles, const GsArgs a) {
   extern __shared__ uint8_t smem_raw[];
   SegSmem& sm = *reinterpret_cast<SegSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, id = tid & 127;
   const int pair = blockIdx.x / a.nseg, seg = blockIdx.x % a.nseg;
-  if (!CKPT && seg == (REV ? 0 : a.nseg - 1)) return;  // no segment starts from what this one adds
+  const bool rev = blockIdx.y != 0;
+  const Tiles &tx = tiles.x[blockIdx.y], &ty = tiles.y[blockIdx.y];
+  may_follow();
+  if (!CKPT && seg == (rev ? 0 : a.nseg - 1)) return;  // no segment starts from what this one adds
   const int bi = pair / a.heads, hi_ = pair % a.heads;
   const float* gp = a.g + bi * a.gb + hi_ * a.gh;
   const int c0 = seg * a.per_seg, c1 = min(a.nchunk, c0 + a.per_seg), n = c1 - c0;
-  auto chunk_of = [&](int i) { return REV ? c1 - 1 - i : c0 + i; };
+  auto chunk_of = [&](int i) { return rev ? c1 - 1 - i : c0 + i; };
   auto load = [&](int i) {
     uint64_t* bar = &sm.full[i & 1];
     mbar_arrive_expect_tx(bar, 2 * kLTile);
@@ -450,7 +483,7 @@ __global__ void __launch_bounds__(256, 2)
   auto weigh_chunk = [&](int i) {
     const int ph = i & 1, c0_ = 4 * (tid >> 7);
     const Gates& gt = sm.gates[i % 3];
-    const float w = REV ? a.scale * exp2_fast(gt.b[id]) : gt.w[id];
+    const float w = rev ? a.scale * exp2_fast(gt.b[id]) : gt.w[id];
     const F2 ww = f2(w, w);
     mbar_wait(&sm.full[ph], (i >> 1) & 1, a.status, &sm.abort);
 #pragma unroll
@@ -491,7 +524,15 @@ __global__ void __launch_bounds__(256, 2)
   } else {
     const uint32_t tmem = sm.tmem + ((uint32_t)((warp & 3) * 32) << 16);
     F2 S[32];
-    load_row(S, a.start != nullptr && id < 64 ? a.start + ((size_t)blockIdx.x * kD + id) * kD : nullptr);
+    if (CKPT) {
+      before_results();
+      if (id < 64)
+        load_start<false>(S, a, pair, seg, id);
+      else
+        load_row(S, nullptr);
+    } else {
+      load_row(S, nullptr);
+    }
     float decay = 0.f;
     for (int i = 0; i <= n; ++i) {
       if (i < n) {
@@ -523,10 +564,10 @@ __global__ void __launch_bounds__(256, 2)
       }
     }
     asm volatile("bar.sync 3, 160;" ::: "memory");
-    if (a.local != nullptr) {
+    if (!CKPT) {
       join_parts(S, sm.X[0], id, 2);  // the products are done
-      if (id < 64) store_row(S, a.local + ((size_t)blockIdx.x * kD + id) * kD);
-      if (id == 0) a.seg_decay[blockIdx.x] = decay;
+      if (id < 64) store_row(S, a.local[rev] + ((size_t)blockIdx.x * kD + id) * kD);
+      if (id == 0) a.seg_decay[rev][blockIdx.x] = decay;
     }
   }
   tc::fence_before();
@@ -710,24 +751,9 @@ __global__ void __launch_bounds__(256, 2)
       make_gates(sm.raw[0], sm.gates[0], lane);
       if (n > 1) fetch_gates(a, gp, (int64_t)(c0 + 1) * kL, sm.raw[1], lane);
     }
+    before_results();
     if (id < 64) {
-      if (a.few) {
-        // Few segments: what those before this one add, in order, onto the initial state.
-        load_row(S, a.start != nullptr ? a.start + ((size_t)pair * kD + id) * kD : nullptr);
-        for (int before = 0; before < seg; ++before) {
-          const size_t at = (size_t)pair * a.nseg + before;
-          const float f = exp2_fast(a.seg_decay[at]);
-          const ulonglong2* x = reinterpret_cast<const ulonglong2*>(a.local + (at * kD + id) * kD);
-#pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            const ulonglong2 y = x[c];
-            S[2 * c] = fma2(f2(f, f), S[2 * c], F2{y.x});
-            S[2 * c + 1] = fma2(f2(f, f), S[2 * c + 1], F2{y.y});
-          }
-        }
-      } else {
-        load_row(S, a.start != nullptr ? a.start + ((size_t)blockIdx.x * kD + id) * kD : nullptr);
-      }
+      load_start<false>(S, a, pair, seg, id);
       put_state_row(sm.S, S, id);
     }
     fence_proxy_async_smem();
@@ -926,6 +952,7 @@ __global__ void __launch_bounds__(512, 1) k_gs_bwd(const __grid_constant__ BwdTi
     mbar_init(&sm.sent, 2);
     sm.abort = 0;
     fence_barrier_init();
+    before_results();  // the states before the chunks
     load(0);
   }
   if (warp == 4) tc::alloc(&sm.tmem, 512);
@@ -940,21 +967,11 @@ __global__ void __launch_bounds__(512, 1) k_gs_bwd(const __grid_constant__ BwdTi
   // 0 joins all groups twice a chunk.
   if (group == 2) {
     F2 S[32];  // a row of one part of dS
-    const bool first = id < 64;
-    load_row(S, a.start != nullptr && first ? a.start + ((size_t)(a.few ? pair : blockIdx.x) * kD + id) * kD : nullptr);
-    if (a.few && first) {
-      for (int later = a.nseg - 1; later > seg; --later) {
-        const size_t at = (size_t)pair * a.nseg + later;
-        const float f = exp2_fast(a.seg_decay[at]);
-        const ulonglong2* x = reinterpret_cast<const ulonglong2*>(a.local + (at * kD + id) * kD);
-#pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          const ulonglong2 y = x[c];
-          S[2 * c] = fma2(f2(f, f), S[2 * c], F2{y.x});
-          S[2 * c + 1] = fma2(f2(f, f), S[2 * c + 1], F2{y.y});
-        }
-      }
-    }
+    before_results();
+    if (id < 64)
+      load_start<true>(S, a, pair, seg, id);
+    else
+      load_row(S, nullptr);
     put_ds(sm, S, id);
     if (warp == 11) {
       fetch_gates(a, gp, (int64_t)(c1 - 1) * kL, sm.raw[0], lane);
@@ -1338,6 +1355,23 @@ static_assert(kBwdSmem <= 232448, "k_gs_bwd exceeds the 227 KB of shared memory 
 static_assert(2 * (kOutSmem + 1024) <= 233472, "two CTAs of k_gs_out do not fit an SM");
 static_assert(2 * (kSegSmem + 1024) <= 233472, "two CTAs of k_gs_segment do not fit an SM");
 
+// Launches fn so that it may start beside the end of the launch before it on the stream.
+template <class... P, class... A>
+ttt_status launch_after(void (*fn)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  TTT_CUDA(cudaLaunchKernelEx(&cfg, fn, args...));
+  return TTT_OK;
+}
+
 Rows rows_of(const void* p, const ttt_strides& s) {
   return Rows{static_cast<const __nv_bfloat16*>(p), s.batch, s.head};
 }
@@ -1392,31 +1426,32 @@ ttt_status gated_scan(const ttt_gated_scan_desc* d, const void* q, const void* k
   a.per_seg = p.per_seg;
   a.status = DevStatus{status, kWaitLimitNs};
   a.start = S0;
+  a.end = S_end;
   Tiles tq, tk, tv, to;
   TTT_TRY(tiles_of(&tq, q, d->q, d));
   TTT_TRY(tiles_of(&tk, k, d->k, d));
   TTT_TRY(tiles_of(&tv, v, d->v, d));
   TTT_TRY(tiles_of(&to, o, d->o, d));
-  if (p.nseg > 1) {
-    a.local = static_cast<float*>(ws);
-    a.seg_decay = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + round256((size_t)pairs * p.nseg * kState * 4));
-    a.start = nullptr;
-    TTT_TRY(raise_smem(k_gs_segment<false, false>, kSegSmem));
-    k_gs_segment<false, false><<<(unsigned)(pairs * a.nseg), 256, kSegSmem, s>>>(tk, tv, a);
-    TTT_CUDA(cudaGetLastError());
-    a.few = a.nseg <= kFewSegments && S_end != S0;  // with few, the last segment may write S_end before others read S0
-    a.start = S0;
-    if (!a.few) {
-      k_gs_combine<false><<<dim3((unsigned)pairs, kState / 128), 128, 0, s>>>(a.local, a.seg_decay, S0, a.nseg);
-      TTT_CUDA(cudaGetLastError());
-      a.start = a.local;
-    }
-  }
-  a.end = S_end;
   TTT_TRY(raise_smem(k_gs_out, kOutSmem));
-  k_gs_out<<<(unsigned)(pairs * p.nseg), 256, kOutSmem, s>>>(tq, tk, tv, to, a);
+  const dim3 grid((unsigned)(pairs * p.nseg));
+  if (p.nseg == 1) {
+    k_gs_out<<<grid, 256, kOutSmem, s>>>(tq, tk, tv, to, a);
+    TTT_CUDA(cudaGetLastError());
+    return TTT_OK;
+  }
+  a.local[0] = static_cast<float*>(ws);
+  a.seg_decay[0] = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + round256((size_t)pairs * p.nseg * kState * 4));
+  SegTiles t = {{tk, tk}, {tv, tv}};
+  TTT_TRY(raise_smem(k_gs_segment<false>, kSegSmem));
+  k_gs_segment<false><<<grid, 256, kSegSmem, s>>>(t, a);
   TTT_CUDA(cudaGetLastError());
-  return TTT_OK;
+  // The last segment may write S_end before others have read S0: then not on their own.
+  a.few = p.nseg <= kFewSegments && S_end != S0;
+  if (!a.few) {
+    TTT_TRY(launch_after(k_gs_combine, dim3((unsigned)pairs, kState / 128, 1), 128, 0, s, a, S0, S0));
+    a.start = a.local[0];
+  }
+  return launch_after(k_gs_out, grid, 256, kOutSmem, s, tq, tk, tv, to, a);
 }
 
 ttt_status gated_scan_backward(const ttt_gated_scan_desc* d, const void* dout, const void* q, const void* k,
@@ -1433,11 +1468,9 @@ ttt_status gated_scan_backward(const ttt_gated_scan_desc* d, const void* dout, c
   a.ckpt = reinterpret_cast<__nv_bfloat16*>(w);
   w += round256((size_t)pairs * p.nchunk * 2 * kState * 2);
   const size_t local_bytes = round256((size_t)pairs * p.nseg * kState * 4), decay_bytes = round256((size_t)pairs * p.nseg * 4);
-  float* local[2];
-  float* decay[2];
   for (int i = 0; i < 2; ++i) {
-    local[i] = reinterpret_cast<float*>(w + i * (local_bytes + decay_bytes));
-    decay[i] = reinterpret_cast<float*>(w + i * (local_bytes + decay_bytes) + local_bytes);
+    a.local[i] = reinterpret_cast<float*>(w + i * (local_bytes + decay_bytes));
+    a.seg_decay[i] = reinterpret_cast<float*>(w + i * (local_bytes + decay_bytes) + local_bytes);
   }
   BwdTiles t;
   TTT_TRY(tiles_of(&t.q, q, d->q, d));
@@ -1453,36 +1486,31 @@ ttt_status gated_scan_backward(const ttt_gated_scan_desc* d, const void* dout, c
   rows.tokens = (int64_t)p.nchunk * kL;
   dense = {(int64_t)d->heads * rows.tokens * kD, rows.tokens * kD, kD};
   TTT_TRY(tiles_of(&t.s, a.ckpt, dense, &rows));
-  const unsigned grid = (unsigned)(pairs * p.nseg);
-  TTT_TRY(raise_smem(k_gs_segment<false, true>, kSegSmem));
+  const dim3 grid((unsigned)(pairs * p.nseg));
+  TTT_TRY(raise_smem(k_gs_segment<false>, kSegSmem));
+  TTT_TRY(raise_smem(k_gs_segment<true>, kSegSmem));
+  TTT_TRY(raise_smem(k_gs_bwd, kBwdSmem));
+  const SegTiles both = {{t.k, t.q}, {t.v, t.g}};
+  a.start = S0;
   if (p.nseg > 1) {
-    TTT_TRY(raise_smem(k_gs_segment<false, false>, kSegSmem));
-    TTT_TRY(raise_smem(k_gs_segment<true, false>, kSegSmem));
-    a.local = local[0];
-    a.seg_decay = decay[0];
-    k_gs_segment<false, false><<<grid, 256, kSegSmem, s>>>(t.k, t.v, a);
+    // What the segments add in both directions at once.
+    k_gs_segment<false><<<dim3(grid.x, 2), 256, kSegSmem, s>>>(both, a);
     TTT_CUDA(cudaGetLastError());
-    k_gs_combine<false><<<dim3((unsigned)pairs, kState / 128), 128, 0, s>>>(a.local, a.seg_decay, S0, a.nseg);
-    TTT_CUDA(cudaGetLastError());
-    a.local = local[1];
-    a.seg_decay = decay[1];
-    k_gs_segment<true, false><<<grid, 256, kSegSmem, s>>>(t.q, t.g, a);
-    TTT_CUDA(cudaGetLastError());
-    k_gs_combine<true><<<dim3((unsigned)pairs, kState / 128), 128, 0, s>>>(a.local, a.seg_decay, dS_end, a.nseg);
+    a.few = p.nseg <= kFewSegments && dS0 != dS_end;
+    if (!a.few) {
+      TTT_TRY(launch_after(k_gs_combine, dim3((unsigned)pairs, kState / 128, 2), 128, 0, s, a, S0, dS_end));
+      a.start = a.local[0];
+    }
+    // The state before every chunk.
+    TTT_TRY(launch_after(k_gs_segment<true>, grid, 256, kSegSmem, s, both, a));
+  } else {
+    k_gs_segment<true><<<grid, 256, kSegSmem, s>>>(both, a);
     TTT_CUDA(cudaGetLastError());
   }
-  // The state before every chunk.
-  a.local = nullptr;
-  a.start = p.nseg > 1 ? local[0] : S0;
-  k_gs_segment<false, true><<<grid, 256, kSegSmem, s>>>(t.k, t.v, a);
-  TTT_CUDA(cudaGetLastError());
-  a.start = p.nseg > 1 ? local[1] : dS_end;
+  a.start = p.nseg > 1 && !a.few ? a.local[1] : dS_end;
   a.end = dS0;
   a.dg = dg;
-  TTT_TRY(raise_smem(k_gs_bwd, kBwdSmem));
-  k_gs_bwd<<<grid, 512, kBwdSmem, s>>>(t, a);
-  TTT_CUDA(cudaGetLastError());
-  return TTT_OK;
+  return launch_after(k_gs_bwd, grid, 512, kBwdSmem, s, t, a);
 }
 
 ttt_status gated_scan_step(const ttt_gated_scan_desc* d, const void* q, const void* k, const void* v, const float* g,
