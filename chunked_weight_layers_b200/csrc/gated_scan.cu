@@ -2,31 +2,40 @@
 // Hebbian update, S_t = e^{g_t}·S_{t-1} + k_tᵀ·v_t, o_t = scale · q_t·S_t, its gradients, and its
 // one-token form.
 //
-// Mathematics. Tokens are taken in chunks of 64. With b_i the sum of the chunk's gates up to and
-// with token i, S the state before the chunk and w_j = e^{b_64 - b_j}:
+// Mathematics. Tokens are taken in chunks of 128. With b_i the sum of the chunk's gates up to and
+// with token i, S the state before the chunk and w_j = e^{b_128 - b_j}:
 //   O  = scale · [ e^{b_i}·(Q·S)_i + Σ_{j <= i} e^{b_i - b_j}·(q_i·k_j)·v_j ]
-//   S' = e^{b_64}·S + (w ⊙ K)ᵀ·V
-// so a chunk is four 64 x 64 x 64 products, and only S goes from chunk to chunk. Backward, with
-// dS' the gradient of the state after the chunk and u_i = scale·e^{b_i}:
+//   S' = e^{b_128}·S + (w ⊙ K)ᵀ·V
+// so a chunk is four products, and only S goes from chunk to chunk. Backward, with dS' the gradient of
+// the state after the chunk and u_i = scale·e^{b_i}:
 //   dQ = u ⊙ (dO·Sᵀ) + A·K,      A_ij = scale·e^{b_i - b_j}·(do_i·v_j)  (j <= i)
 //   dK = w ⊙ (V·dS'ᵀ) + Aᵀ·Q
 //   dV = w ⊙ (K·dS') + Pᵀ·dO,    P_ij = scale·e^{b_i - b_j}·(q_i·k_j)  (j <= i)
-//   dS = e^{b_64}·dS' + (u ⊙ Q)ᵀ·dO
-//   dg_t = e^{b_64}·<S, dS'> + Σ_{i >= t} q_i·(u_i·S·do_i) + Σ_{j < t} k_j·(w_j·dS'·v_j)
+//   dS = e^{b_128}·dS' + (u ⊙ Q)ᵀ·dO
+//   dg_t = e^{b_128}·<S, dS'> + Σ_{i >= t} q_i·(u_i·S·do_i) + Σ_{j < t} k_j·(w_j·dS'·v_j)
 //          + Σ_{i >= t > j} A_ij·(q_i·k_j)
 // (the gate of token t scales every path from before t to t or after). Each chunk's dg starts
 // from the states, not from the chunk after it, so rounding does not add up along the sequence.
 //
-// Precision. The products run on the tensor cores with bf16 operands and fp32 sums. S and dS stay
-// in fp32 registers. Where a product's result is a bf16 output, one factor is rounded to bf16
-// (P, A, or the copy of S); where it feeds a fp32 output (the states and dg), the rounded factor
-// is kept as a sum of two bf16 numbers (2^-17 of its size), at the price of a second product.
-// The gates are summed in base-2 units; one below -150 (its factor is 0 in fp32, as for -inf,
-// which starts a new document) counts as -150, so that differences of sums stay finite.
+// Precision. The products run on the tensor cores (tcgen05) with bf16 operands and fp32 sums. S and
+// dS stay in fp32 registers. Where a product's result is a bf16 output, one factor is rounded to bf16
+// (P, A, or the copy of S); where it feeds a fp32 output (the states and dg), the rounded factor is
+// kept as a sum of two bf16 numbers (2^-17 of its size; the states come out within 3e-6, dg within
+// 5e-6 in two norms), at the price of a second product (a third term would cost half as much
+// again). The gates are summed in base-2 units; one below -150 (its factor is 0 in
+// fp32, as for -inf, which starts a new document) counts as -150, so that differences of sums stay
+// finite.
 //
 // Where there are fewer (sequence, head) pairs than the SMs hold CTAs, the sequence is cut into
-// segments: the states that the segments add are found first, combined in order, and then every
-// segment runs from its own start.
+// segments: the states that the segments add are found first (k_gs_segment), combined in order, and
+// then every segment runs from its own start.
+//
+// What bounds it (B200, 8 x 12 heads x 2048 tokens and 4 x 16 x 8192). Forward: k_gs_out takes 5700
+// cycles for a chunk on each of an SM's two CTAs, the rate at which HBM delivers a chunk's 64 KB; the
+// pass over K and V for the segments' starts and the launches' first and last microseconds come on top
+// (41 us, where the bytes need 16). Backward: shared memory, through which a chunk's operands and
+// results pass (some 650 KB): 11000 cycles a chunk (222 us of 321, where the bytes need 74), the state
+// passes another 100 us.
 #include <algorithm>
 
 #include "f32x2.cuh"

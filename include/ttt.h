@@ -537,7 +537,7 @@ size_t ttt_gated_scan_workspace(const ttt_gated_scan_desc* desc);
  * [batch, heads, tokens, 64]), dg (device, dense fp32 [batch, heads, tokens]; 0 where the gate's
  * factor is 0 in fp32) and, where not NULL, dS0 (fp32 like S0; may be dS_end itself). The gradients of an input with a
  * stride of 0 are those of its separate rows: the caller adds them up. The states before every
- * chunk of 64 tokens are made again, in the workspace (256 bytes per token, sequence and head). */
+ * chunk of 128 tokens are made again, in the workspace (128 bytes per token, sequence and head). */
 ttt_status ttt_gated_scan_backward(const ttt_gated_scan_desc* desc, const void* d_o, const void* q, const void* k,
                                    const void* v, const float* g, const float* S0, const float* dS_end, void* dq,
                                    void* dk, void* dv, float* dg, float* dS0, void* workspace,
