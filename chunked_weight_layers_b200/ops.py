@@ -169,7 +169,7 @@ def _qk_call(q, k, positions, freqs, q_weight, k_weight, norm, layout, eps, magn
     _dense_or_none(q_weight, "q_weight", _F32, (width,), dev)
     _dense_or_none(k_weight, "k_weight", _F32, (width,), dev)
     d = abi.ttt_qk_desc(1 if x.dtype is _BF16 else 0, batch, hq, hk, width, rot, _choice(NORMS, norm, "norm"),
-                        _choice(LAYOUTS, layout, "layout"), float(eps), float(magnitude), tokens, int(position0), pos_stride)
+                        _choice(LAYOUTS, layout, "layout"), eps, magnitude, tokens, position0, pos_stride)
     return d, x.dtype, (batch, hq, tokens, width), (batch, hk, tokens, width)
 
 
@@ -194,6 +194,7 @@ def qk_norm_rope(q, k, *, positions=None, freqs=None, magnitude=1.0, norm="rms",
     dense [batch, heads, tokens, width] or the pair ``out`` (which may be the inputs)."""
     dev = _current_device()
     raw, ctx = _place(stream, dev)
+    eps, magnitude, position0 = float(eps), float(magnitude), int(position0)
     try:
         key = (dev, _meta(q), _meta(k), _meta(positions), _meta(freqs), _meta(q_weight), _meta(k_weight), norm, layout, eps,
                magnitude, position0, None if out is None else (_meta(out[0]), _meta(out[1])))
@@ -229,6 +230,7 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, *, positions=None, freqs=None, m
     (None for a weight that is None). With norm "none" ``q`` and ``k`` are not read."""
     dev = _current_device()
     raw, ctx = _place(stream, dev)
+    eps, magnitude, position0 = float(eps), float(magnitude), int(position0)
     try:
         key = (dev, _meta(dq_out), _meta(dk_out), _meta(q), _meta(k), _meta(positions), _meta(freqs), _meta(q_weight),
                _meta(k_weight), norm, layout, eps, magnitude, position0)
@@ -285,8 +287,8 @@ def _scan_desc(shape, scale, q, k, v, o, g):
     o = torch.empty(shape, device="meta") if o is None else o
     if len(shape) == 3:  # one token
         two = lambda t: (*_strides(shape[:2], t.stride()[:2]), 0)  # noqa: E731
-        return abi.ttt_gated_scan_desc(shape[0], shape[1], 1, float(scale), *(abi.ttt_strides(*two(t)) for t in (q, k, v, o, g)))
-    return abi.ttt_gated_scan_desc(shape[0], shape[1], shape[2], float(scale),
+        return abi.ttt_gated_scan_desc(shape[0], shape[1], 1, scale, *(abi.ttt_strides(*two(t)) for t in (q, k, v, o, g)))
+    return abi.ttt_gated_scan_desc(shape[0], shape[1], shape[2], scale,
                                    *(abi.ttt_strides(*_strides(shape, t.stride())) for t in (q, k, v, o, g)))
 
 
@@ -299,6 +301,7 @@ def gated_scan(q, k, v, g, *, scale=1.0, initial=None, out=None, final=None, sta
     :func:`gated_ffn`."""
     dev = _current_device()
     raw, ctx = _place(stream, dev)
+    scale = float(scale)  # a plain number: the key must not hold a tensor, whose value may change
     try:
         key = (dev, _meta(q), _meta(k), _meta(v), _meta(g), _meta(initial), _meta(out), _meta(final), _meta(status), scale)
     except AttributeError:  # something that is no tensor: the checks will name it
@@ -335,6 +338,7 @@ def gated_scan_backward(do, q, k, v, g, *, scale=1.0, initial=None, dfinal=None,
     is."""
     dev = _current_device()
     raw, ctx = _place(stream, dev)
+    scale = float(scale)  # a plain number: the key must not hold a tensor, whose value may change
     try:
         key = (dev, _meta(do), _meta(q), _meta(k), _meta(v), _meta(g), _meta(initial), _meta(dfinal), _meta(status), scale)
     except AttributeError:
@@ -370,6 +374,7 @@ def gated_scan_step(state, q, k, v, g, *, scale=1.0, out=None, stream=None):
     rows). Returns o, bf16 [batch, heads, 64]."""
     dev = _current_device()
     raw, ctx = _place(stream, dev)
+    scale = float(scale)  # a plain number: the key must not hold a tensor, whose value may change
     try:
         key = (dev, _meta(state), _meta(q), _meta(k), _meta(v), _meta(g), _meta(out), scale)
     except AttributeError:

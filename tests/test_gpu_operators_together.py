@@ -163,3 +163,57 @@ def test_a_layer_in_one_graph(cwl):
         torch.cuda.synchronize()
         want = layer(x, want_S, torch.arange(i * T, (i + 1) * T, device="cuda"))
         assert torch.equal(o, want) and torch.equal(S, want_S)
+
+
+def test_numbers_given_as_tensors_are_read_at_every_call(cwl):
+    """A scale, epsilon or magnitude held in a tensor may change between calls."""
+    (q, k, v), _ = _projection(8)
+    g = torch.zeros((B, H, T), device="cuda")
+    scale, eps = torch.tensor(1.0), torch.tensor(1e-6)
+    a, _ = cwl.gated_scan(q, k, v, g, scale=scale)
+    x, _ = cwl.qk_norm_rope(q, None, eps=eps)
+    scale.fill_(2.0), eps.fill_(3.0)
+    b, _ = cwl.gated_scan(q, k, v, g, scale=scale)
+    y, _ = cwl.qk_norm_rope(q, None, eps=eps)
+    assert torch.equal(b, cwl.gated_scan(q, k, v, g, scale=2.0)[0]) and not torch.equal(a, b)
+    assert torch.equal(y, cwl.qk_norm_rope(q, None, eps=3.0)[0]) and not torch.equal(x, y)
+
+
+_FIRST_CALLS = """
+import sys, torch
+sys.path.insert(0, sys.argv[1])
+import chunked_weight_layers_b200 as cwl
+r = torch.Generator().manual_seed(1)
+rnd = lambda *s: torch.randn(s, generator=r).bfloat16().cuda()
+q, k, v, do = (rnd(1, 2, 900, 64) for _ in range(4))
+g = -torch.rand((1, 2, 900), generator=r).cuda()
+f, _ = cwl.rope_frequencies(64)
+S = torch.zeros((1, 2, 64, 64), device="cuda")
+x, wg, wu, dz = rnd(300, 128), rnd(200, 128), rnd(200, 128), rnd(300, 200)
+torch.cuda.synchronize()
+def calls():
+    Q, K = cwl.qk_norm_rope(q, k, freqs=f)
+    return [*cwl.gated_scan(Q, K, v, g), *cwl.gated_scan_backward(do, Q, K, v, g)[:4],
+            *cwl.qk_norm_rope_backward(do, do, q, k, freqs=f)[:2], cwl.gated_ffn(x[:3], wg, wu),
+            *cwl.gated_ffn(x, wg, wu, save=True), *cwl.gated_ffn_backward(dz, x, wg, wu, dz, dz)]
+gr = torch.cuda.CUDAGraph()
+with torch.cuda.graph(gr):
+    got = calls()
+    step = cwl.gated_scan_step(S, q[:, :, 0], k[:, :, 0], v[:, :, 0], g[:, :, 0])
+gr.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, calls()))
+assert S.abs().sum() > 0 and torch.isfinite(step.float()).all()
+del gr
+print("captured")
+"""
+
+
+def test_first_calls_of_a_process_are_captured(tmp_path):
+    """Nothing needs a call outside a capture first: a new process captures each operator's first call."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", _FIRST_CALLS, root], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stdout[-500:] + r.stderr[-1500:]
