@@ -34,8 +34,10 @@
 // cycles for a chunk on each of an SM's two CTAs, the rate at which HBM delivers a chunk's 64 KB; the
 // pass over K and V for the segments' starts and the launches' first and last microseconds come on top
 // (41 us, where the bytes need 16). Backward: shared memory, through which a chunk's operands and
-// results pass (some 650 KB): 11000 cycles a chunk (222 us of 321, where the bytes need 74), the state
-// passes another 100 us.
+// results pass (some 650 KB, and the products' operands once more, come to 8500 cycles): 10500 cycles a
+// chunk (210 us of 305, where the bytes need 74), the state passes the rest. The state before every chunk
+// is kept in pieces of eight columns, all rows of a piece after each other: a warp then writes whole
+// sectors, where rows of 128 bytes took 15 us more.
 #include <algorithm>
 
 #include "f32x2.cuh"
@@ -70,7 +72,7 @@ struct GsArgs {
   int few;                            // start holds one state a pair: the CTAs add the segments' on their own
   float* local[2];                    // what each segment adds [pairs][nseg][64][64], forward and in reverse
   float* seg_decay[2];                // sums of the segments' gates, base-2 units [pairs][nseg]
-  __nv_bfloat16* ckpt;                // state before every chunk, as two bf16 planes [pairs][nchunk][2][64][64]
+  __nv_bfloat16* ckpt;                // state before every chunk, as two bf16 terms [pairs][nchunk][2][8 pieces][64 rows][8]
   float* dg;                          // dense [pairs][T]
   DevStatus status;
 };
@@ -343,6 +345,16 @@ __device__ __forceinline__ void tma_prefetch_tile(const CUtensorMap* map, int t,
                : "memory");
 }
 
+// The same for consecutive bytes (16-byte aligned, a multiple of 16).
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)), "l"(src),
+               "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+__device__ __forceinline__ void bulk_prefetch(const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
+}
+
 __device__ __forceinline__ void tma_store_tile(const CUtensorMap* map, const void* src, int t, int h, int b) {
   asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%2, %3, %4, %5}], [%1];" ::"l"(
                    reinterpret_cast<uint64_t>(map)),
@@ -564,10 +576,10 @@ __global__ void __launch_bounds__(256, 2) k_gs_segment(const __grid_constant__ S
         decay += total;
       }
       if (CKPT && i < n) {
-        __nv_bfloat16* p = a.ckpt + ((size_t)pair * a.nchunk + chunk_of(i)) * 2 * kState + (id & 63) * kD;
+        uint4* p = reinterpret_cast<uint4*>(a.ckpt + ((size_t)pair * a.nchunk + chunk_of(i)) * 2 * kState) + id;
         split_parts(S, sm.swap, id, 2, [&](int c, uint4 h, uint4 l) {
-          reinterpret_cast<uint4*>(p)[c] = h;
-          reinterpret_cast<uint4*>(p + kState)[c] = l;
+          p[64 * c] = h;
+          p[64 * c + kState / 8] = l;
         });
         group_sync(2);
       }
@@ -816,7 +828,7 @@ __global__ void __launch_bounds__(256, 2)
 
 struct __align__(1024) BwdSmem {
   uint8_t Q[kLTile], K[kLTile], V[kLTile], G[kLTile];  // G: dO
-  uint8_t S[2][kTile];    // the state before the chunk: rounded, and what the rounding left
+  uint8_t S[2][kTile];    // the state before the chunk: rounded, and what the rounding left; [8 pieces][64 rows][16 bytes]
   uint8_t dS[2][kTile];   // the gradient of the state after the chunk, the same way
   uint8_t W[2][kLTile];   // u ⊙ Q, two terms; then dV and dK on their way out
   uint8_t P[2][kLTile];   // P and A, 128 queries x 128 keys, in halves of 64 keys
@@ -914,8 +926,14 @@ __device__ __forceinline__ void weigh_half(BwdSmem& sm, const GsArgs& a, int id,
 }
 
 struct BwdTiles {
-  Tiles q, k, v, g, s, dq, dk, dv;
+  Tiles q, k, v, g, dq, dk, dv;
 };
+
+// Descriptor of a K-major operand as S lies: pieces of 16 bytes of all 64 rows after each other.
+__device__ __forceinline__ uint64_t pieces_at(const void* tile, int bytes) {
+  constexpr uint64_t high = (uint64_t)((128u >> 4) | (1u << 14)) << 32;  // 128 bytes from eight rows to the next, no swizzle
+  return high | (desc_of(tile, kD * 16) + (uint32_t)(bytes >> 4));       // 1024 from piece to piece
+}
 
 // From the segment's last chunk to its first: 512 threads in four groups of 128, one CTA an SM; thread
 // `id` of a group holds row `id` of what the group reads from TMEM.
@@ -935,14 +953,15 @@ __global__ void __launch_bounds__(512, 1) k_gs_bwd(const __grid_constant__ BwdTi
   const int bi = pair / a.heads, hi_ = pair % a.heads;
   const float* gp = a.g + bi * a.gb + hi_ * a.gh;
   const int c0 = seg * a.per_seg, c1 = min(a.nchunk, c0 + a.per_seg), n = c1 - c0;
+  const __nv_bfloat16* states = a.ckpt + (size_t)pair * a.nchunk * 2 * kState;
   auto load = [&](int i) {
     const int t = (c1 - 1 - i) * kL;
-    mbar_arrive_expect_tx(&sm.in, 5 * kLTile);
+    mbar_arrive_expect_tx(&sm.in, 4 * kLTile + 2 * kTile);
     tma_load_tile(sm.Q, &tm_.q.map, &sm.in, t, hi_ * tm_.q.head, bi * tm_.q.batch);
     tma_load_tile(sm.K, &tm_.k.map, &sm.in, t, hi_ * tm_.k.head, bi * tm_.k.batch);
     tma_load_tile(sm.G, &tm_.g.map, &sm.in, t, hi_ * tm_.g.head, bi * tm_.g.batch);
     tma_load_tile(sm.V, &tm_.v.map, &sm.in, t, hi_ * tm_.v.head, bi * tm_.v.batch);
-    tma_load_tile(sm.S[0], &tm_.s.map, &sm.in, t, hi_, bi);  // both planes: 128 rows a chunk
+    bulk_load(sm.S, states + (size_t)(c1 - 1 - i) * 2 * kState, 2 * kTile, &sm.in);
   };
   auto prefetch = [&](int i) {
     const int t = (c1 - 1 - i) * kL;
@@ -950,7 +969,7 @@ __global__ void __launch_bounds__(512, 1) k_gs_bwd(const __grid_constant__ BwdTi
     tma_prefetch_tile(&tm_.k.map, t, hi_ * tm_.k.head, bi * tm_.k.batch);
     tma_prefetch_tile(&tm_.g.map, t, hi_ * tm_.g.head, bi * tm_.g.batch);
     tma_prefetch_tile(&tm_.v.map, t, hi_ * tm_.v.head, bi * tm_.v.batch);
-    tma_prefetch_tile(&tm_.s.map, t, hi_, bi);
+    bulk_prefetch(states + (size_t)(c1 - 1 - i) * 2 * kState, 2 * kTile);
   };
   if (tid == 0) {
     mbar_init(&sm.in, 1);
@@ -1010,7 +1029,7 @@ __global__ void __launch_bounds__(512, 1) k_gs_bwd(const __grid_constant__ BwdTi
       const int r = id & 63;
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
-        const uint32_t at = r * 128 + ((c ^ (r & 7)) << 4);
+        const uint32_t at = (64 * c + r) * 16;
         const uint4 x = *reinterpret_cast<const uint4*>(sm.S[0] + at), y = *reinterpret_cast<const uint4*>(sm.S[1] + at);
         d = fma2(S[4 * c], add(from_bf16(x.x), from_bf16(y.x)), d);
         d = fma2(S[4 * c + 1], add(from_bf16(x.y), from_bf16(y.y)), d);
@@ -1093,7 +1112,7 @@ __global__ void __launch_bounds__(512, 1) k_gs_bwd(const __grid_constant__ BwdTi
         // Warp 4 has no scores to weigh (its queries come before group 1's keys): it issues the products,
         // which holds it for as long as they run.
         if (tid == 128) {
-          const uint32_t dq = desc_of(sm.Q), dk = desc_of(sm.K), dv = desc_of(sm.V), dg = desc_of(sm.G), ds = desc_of(sm.S[0]),
+          const uint32_t dq = desc_of(sm.Q), dk = desc_of(sm.K), dv = desc_of(sm.V), dg = desc_of(sm.G),
                          dd = desc_of(sm.dS[0]);
           mbar_wait(&sm.in, ph, a.status, &sm.abort);
 #pragma unroll
@@ -1103,7 +1122,7 @@ __global__ void __launch_bounds__(512, 1) k_gs_bwd(const __grid_constant__ BwdTi
           tc::commit(&sm.scores);
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            tc::mma(tm + kColDqi, desc_at(dg, (kk & 3) * 32), desc_at(ds, (kk >> 2) * kTile + (kk & 3) * 32), tc::idesc_bf16(128, 64, 0, 0), kk != 0);
+            tc::mma(tm + kColDqi, desc_at(dg, (kk & 3) * 32), pieces_at(sm.S, kk * 2048), tc::idesc_bf16(128, 64, 0, 0), kk != 0);
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
             tc::mma(tm + kColDki, desc_at(dv, (kk & 3) * 32), desc_at(dd, (kk >> 2) * kTile + (kk & 3) * 32), tc::idesc_bf16(128, 64, 0, 0), kk != 0);
@@ -1486,15 +1505,10 @@ ttt_status gated_scan_backward(const ttt_gated_scan_desc* d, const void* dout, c
   TTT_TRY(tiles_of(&t.k, k, d->k, d));
   TTT_TRY(tiles_of(&t.v, v, d->v, d));
   TTT_TRY(tiles_of(&t.g, dout, d->o, d));
-  // The gradients are dense; the states' two planes lie as 128 rows of 64 a chunk.
-  ttt_gated_scan_desc rows = *d;
-  ttt_strides dense = {(int64_t)d->heads * d->tokens * kD, d->tokens * kD, kD};
-  TTT_TRY(tiles_of(&t.dq, dq, dense, &rows));
-  TTT_TRY(tiles_of(&t.dk, dk, dense, &rows));
-  TTT_TRY(tiles_of(&t.dv, dv, dense, &rows));
-  rows.tokens = (int64_t)p.nchunk * kL;
-  dense = {(int64_t)d->heads * rows.tokens * kD, rows.tokens * kD, kD};
-  TTT_TRY(tiles_of(&t.s, a.ckpt, dense, &rows));
+  const ttt_strides dense = {(int64_t)d->heads * d->tokens * kD, d->tokens * kD, kD};
+  TTT_TRY(tiles_of(&t.dq, dq, dense, d));
+  TTT_TRY(tiles_of(&t.dk, dk, dense, d));
+  TTT_TRY(tiles_of(&t.dv, dv, dense, d));
   const dim3 grid((unsigned)(pairs * p.nseg));
   TTT_TRY(raise_smem(k_gs_segment<false>, kSegSmem));
   TTT_TRY(raise_smem(k_gs_segment<true>, kSegSmem));
