@@ -24,6 +24,13 @@
 // Sizes need not be multiples of the tiles: TMA reads zeros past the ends, stores are clipped.
 //
 // k_ffn_few takes up to 16 tokens, where the weights' bytes are all that counts: see there.
+//
+// Measured (B200), d 2560, f 9728: forward over 8192 tokens 550 us at full clocks (1480 TFLOP/s, 88 % of a
+// large library product's rate), 620 to 640 us once the card runs at its power limit; over one token 17 us
+// (5.8 TB/s). Backward over 4096 tokens 690 to 750 us at the power limit; at full clocks 57 us for the
+// activation's part, 256 for dX (1590 TFLOP/s), 264 for the weights' gradients and 10 for the joins.
+// 777 tokens, d 1000, f 2744, keeping G and U: 19 us (450 TFLOP/s: two rounds of tiles of 16 k-blocks, whose
+// first loads and epilogues take half of it).
 #include <algorithm>
 
 #include "internal.h"

@@ -1282,7 +1282,8 @@ __global__ void __launch_bounds__(512, 1) k_gs_bwd(const __grid_constant__ BwdTi
 // ---- one token -----------------------------------------------------------------------------
 
 // S ← e^g·S + kᵀ·v in place, o = scale · q·S: one CTA of 128 threads per (sequence, head), each
-// thread four columns of eight rows, all its loads in flight at once.
+// thread four columns of eight rows, all its loads in flight at once. Bound by the states' bytes: 64 x 16
+// heads, 5.0 us for 34 MB (some of it from L2).
 struct StepArgs {
   Rows q, k, v;
   const float* g;

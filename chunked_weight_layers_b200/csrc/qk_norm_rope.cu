@@ -15,6 +15,11 @@
 // off by 0.004 turns at position 100000), then sine and cosine in 32 bits. All sums are fp32;
 // outputs are rounded once. The gains' gradients are summed per CTA, then over the CTAs in a
 // second launch in a fixed order (no atomics: the same bits every time).
+//
+// Measured (B200; the copy rate is 6.45 TB/s): 8 x 2048 tokens of 24 heads of 64: 22 us, 4.5 TB/s; 32768
+// tokens of 40 heads of 128, half of each rotated: 126 us, 5.3 TB/s. Backward, 4 x 8192 tokens of 32 heads of
+// 64 with the gains' gradients: 85 us, 4.7 TB/s (two CTAs an SM for its registers, so fewer loads in flight).
+// 32 tokens of 32 heads: 4 us, nearly all of it the launch's.
 #include <algorithm>
 
 #include "common.cuh"
