@@ -295,7 +295,8 @@ def _scan_desc(shape, scale, q, k, v, o, g):
 def gated_scan(q, k, v, g, *, scale=1.0, initial=None, out=None, final=None, status=None, stream=None):
     """ttt_gated_scan: S_t = e^{g_t}·S_{t-1} + k_tᵀ·v_t, o_t = scale·q_t·S_t per (sequence, head). ``q``,
     ``k``, ``v`` bf16 [batch, heads, tokens, 64] (any strides, dense rows), ``g`` fp32 [batch, heads,
-    tokens] (any strides; natural logarithms, -inf forgets everything before its token). Returns
+    tokens] (any strides; natural logarithms, -inf forgets everything before its token). All tokens
+    must hold finite numbers, padding too (0 · NaN is NaN). Returns
     (o, state): o in ``out`` or a new dense tensor; the state after the last token, fp32 [batch,
     heads, 64, 64], in ``final`` (which may be ``initial``) or a new tensor. ``status`` as for
     :func:`gated_ffn`."""

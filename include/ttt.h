@@ -524,7 +524,9 @@ typedef struct {
  * Writes o (device bf16) and, where not NULL, S_end (device fp32 like S0: the state after the last
  * token; may be S0 itself). tokens = 0 writes S_end = S0 (or 0) and nothing else. States and sums
  * are fp32; one factor of each product is rounded to bf16, but those that make S_end keep 16 bits
- * or more. `status` (device int32 or NULL): as for ttt_target_values_noalloc. Errors: INVALID_ARG,
+ * or more. Padding must hold finite numbers, since 0 · NaN is NaN: a NaN or an infinity may reach
+ * the outputs (and gradients) of all 128 tokens of its chunk, and through the state those after it,
+ * past a gate of −inf too. `status` (device int32 or NULL): as for ttt_target_values_noalloc. Errors: INVALID_ARG,
  * UNSUPPORTED (batch·heads above 2^24, tokens above 2^30, row strides from 2^39 on or, for tokens, 0),
  * CUDA. */
 ttt_status ttt_gated_scan(const ttt_gated_scan_desc* desc, const void* q, const void* k, const void* v,
