@@ -23,7 +23,8 @@
 // round into as many parts as there are pairs, whose fp32 results a small launch adds in order.
 // Sizes need not be multiples of the tiles: TMA reads zeros past the ends, stores are clipped.
 //
-// k_ffn_few takes up to 16 tokens, where the weights' bytes are all that counts: see there.
+// k_ffn_few takes up to 16 tokens, where the weights' bytes are all that counts, and k_ffn_rows some tens of
+// tokens against wide weights: see there.
 //
 // Measured (B200), d 2560, f 9728: forward over 8192 tokens 550 us at full clocks (1480 TFLOP/s, 88 % of a
 // large library product's rate), 620 to 640 us once the card runs at its power limit; over one token 17 us
@@ -504,6 +505,155 @@ __global__ void __launch_bounds__(32 * kFewWarps) k_ffn_few(const __nv_bfloat16*
   }
 }
 
+// ---- some tens of tokens ---------------------------------------------------------------------
+
+// Few tokens leave the pairs' 256 rows nearly empty, and their products cost as much as full ones; so here
+// the weights are the rows. A CTA takes `rows` rows of Wg and the same of Wu against all T tokens (up
+// to 160 columns), two accumulators of 128 lanes (those past `rows` hold what the products make of the next
+// bytes of the ring, and are not looked at), so that an epilogue thread finds g and u of its row in its own
+// lane. One tile a CTA, as many rows as spread f evenly over the SMs: bound by the weights' bytes, which
+// pass once, and for more tokens by X's, which every CTA reads from L2. 17 x 4096 x 14336: 40 us (5.9 TB/s),
+// 17 x 8192 x 28672: 148 us (6.3), 17 x 2560 x 9728: 21 us (4.7; the launch's ends are a fifth of it).
+struct RowsArgs {
+  int T, f, kblocks, rows, cols, stages;  // cols: T rounded up to 16
+  int act;
+  __nv_bfloat16 *z, *g, *u;  // g and u or null
+  DevStatus status;
+};
+
+constexpr int kRowsMaxStages = 8, kRowsEpi = 16, kRowsThreads = (2 + kRowsEpi) * 32;
+constexpr int kRowsSlack = kHalf;       // what the last stage's products read past its rows
+constexpr int kRowsRing = 200 * 1024;
+
+struct RowsSync {
+  uint64_t full[kRowsMaxStages], empty[kRowsMaxStages], done;
+  uint32_t tmem;
+  int abort;
+};
+
+// Bytes of a CTA's rows of one weight in a stage, and of a stage: whole groups of eight rows.
+__host__ __device__ inline int rows_part(int rows) { return (rows + 7) / 8 * 8 * FK * 2; }
+__host__ __device__ inline int rows_stage(int rows, int cols) { return 2 * rows_part(rows) + cols * FK * 2; }
+
+// Eight consecutive fp32 columns of this thread's TMEM lane.
+__device__ __forceinline__ void ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+
+// Columns of two tokens, one row a lane, to out[token][row]: each lane a pair of rows of one token.
+__device__ __forceinline__ void store_tokens(__nv_bfloat16* out, float a, float b, int t, int lane, int T, size_t ld, bool in) {
+  const bool odd = lane & 1;
+  const float got = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
+  if (in && t + odd < T) *reinterpret_cast<uint32_t*>(out + (size_t)(t + odd) * ld - odd) = odd ? pack_bf16(got, b) : pack_bf16(a, got);
+}
+
+__global__ void __launch_bounds__(kRowsThreads, 1)
+    k_ffn_rows(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmG, const __grid_constant__ CUtensorMap tmU,
+               const RowsArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ RowsSync sm;
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, f0 = blockIdx.x * a.rows;
+  const int part = rows_part(a.rows), stage = rows_stage(a.rows, a.cols);
+  const uint32_t up = a.cols <= 128 ? 128 : 256;  // TMEM column of the second accumulator
+  volatile int* abort = &sm.abort;
+  auto load = [&](int kb, int s) {
+    uint8_t* p = ring + s * stage;
+    mbar_arrive_expect_tx(&sm.full[s], (2 * a.rows + a.cols) * FK * 2);
+    tma_load_2d(p, &tmG, &sm.full[s], kb * FK, f0);
+    tma_load_2d(p + part, &tmU, &sm.full[s], kb * FK, f0);
+    tma_load_2d(p + 2 * part, &tmX, &sm.full[s], kb * FK, 0);
+  };
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < a.stages; ++i) {
+      mbar_init(&sm.full[i], 1);
+      mbar_init(&sm.empty[i], 1);
+    }
+    mbar_init(&sm.done, 1);
+    sm.abort = 0;
+    fence_barrier_init();
+    for (int kb = 0; kb < min(a.stages, a.kblocks); ++kb) load(kb, kb);
+  }
+  __syncwarp();
+  if (warp == 1) tc::alloc(&sm.tmem, 2 * up);
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = sm.tmem;
+  if (warp == 0) {
+    if (lane == 0) {
+      // The stage and the parity of its round are counted, not divided out of kb: with the divisions a
+      // k-block took 930 cycles whatever its size.
+      int kb = min(a.stages, a.kblocks);
+      uint32_t s = 0, round = 0;
+      for (; kb < a.kblocks; ++kb) {
+        if (*abort || !mbar_wait(&sm.empty[s], round & 1, a.status, abort)) break;
+        load(kb, s);
+        if (++s == (uint32_t)a.stages) s = 0, ++round;
+      }
+      // Nothing may still land in this CTA's shared memory when it exits.
+      for (int k = max(0, kb - a.stages); k < kb; ++k) mbar_wait(&sm.full[k % a.stages], (k / a.stages) & 1, a.status, nullptr);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t idesc = tc::idesc_bf16(128, a.cols, 0, 0);
+      const uint32_t first = tc::desc_of(ring);
+      bool ok = true;
+      uint32_t s = 0, round = 0, dg = first;
+      for (int kb = 0; kb < a.kblocks; ++kb) {
+        if (!(ok = mbar_wait(&sm.full[s], round & 1, a.status, abort))) break;
+        tc::fence_after();
+        const uint32_t du = dg + (part >> 4), dx = du + (part >> 4);
+#pragma unroll
+        for (int kk = 0; kk < FK / 16; ++kk) {
+          tc::mma(tmem, tc::desc_at(dg, kk * 32), tc::desc_at(dx, kk * 32), idesc, kb != 0 || kk != 0);
+          tc::mma(tmem + up, tc::desc_at(du, kk * 32), tc::desc_at(dx, kk * 32), idesc, kb != 0 || kk != 0);
+        }
+        tc::commit(&sm.empty[s]);
+        dg += stage >> 4;
+        if (++s == (uint32_t)a.stages) s = 0, ++round, dg = first;
+      }
+      tc::commit(&sm.done);  // of all products, so that TMEM can be freed
+      if (!ok) *abort = 1;
+    }
+  }
+  __syncwarp();
+  if (warp >= 2) {
+    const int q = warp & 3, r = 32 * q + lane;
+    const bool in = r < a.rows && f0 + r < a.f;
+    const bool ok = mbar_wait(&sm.done, 0, a.status, nullptr);
+    tc::fence_after();
+    if (__all_sync(0xffffffffu, ok) && *abort == 0 && 32 * q < a.rows) {
+      const uint32_t tb = tmem + ((uint32_t)(32 * q) << 16);
+      const size_t at = (size_t)f0 + r;
+#pragma unroll 1
+      for (int c = 8 * ((warp - 2) >> 2); c < a.cols; c += 8 * (kRowsEpi / 4)) {
+        uint32_t g[8], u[8];
+        ld8(tb + c, g);
+        ld8(tb + up + c, u);
+        tc::wait_ld();
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+          const float g0 = __uint_as_float(g[i]), g1 = __uint_as_float(g[i + 1]), u0 = __uint_as_float(u[i]), u1 = __uint_as_float(u[i + 1]);
+          if (a.g != nullptr) {
+            store_tokens(a.g + at, g0, g1, c + i, lane, a.T, a.f, in);
+            store_tokens(a.u + at, u0, u1, c + i, lane, a.T, a.f, in);
+          }
+          store_tokens(a.z + at, act_of(g0, a.act) * u0, act_of(g1, a.act) * u1, c + i, lane, a.T, a.f, in);
+        }
+      }
+    }
+  } else if (warp == 1) {
+    mbar_wait(&sm.done, 0, a.status, nullptr);
+  }
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  if (warp == 1) tc::dealloc(tmem, 2 * up);
+}
+
 // ---- host ------------------------------------------------------------------------------------
 
 constexpr size_t kFfnSmem = sizeof(FfnSmem) + 1024;
@@ -519,6 +669,16 @@ ttt_status map_bf16(CUtensorMap* m, const void* base, int64_t inner, int64_t out
 int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
 int pairs_of(int num_sms) { return std::max(1, num_sms / 2); }
+
+// Up to 8 tokens take k_ffn_few, and up to 16 where the weights are short or narrow. k_ffn_rows takes up to
+// 160 where the pairs would need a second round of tiles, which costs them as much as the first (f above 9472
+// on 148 SMs): 17 x 2560 x 9728: 21 us against 31, 128 tokens: 27 against 31, 192: 35 against 33; 17 x 8192 x
+// 28672: 148 against 278. In one round the pairs are as fast or faster (17 x 2048 x 7168: 17.3 against 17.6, 128
+// tokens: 18.7 against 22.8). 16 x 2048 x 11264: 19 us against 29 of k_ffn_few; 16 x 512 x 28672: 17.5 against
+// 15.6.
+bool takes_rows(int64_t T, int d, int f, int num_sms) {
+  return f > FM * pairs_of(num_sms) && T <= 160 && (T > 16 || (T > 8 && d >= 1024));
+}
 
 // Tokens of a tile that each CTA of the pair takes: the fewest, in steps of eight, that cover them in this
 // many tiles, rather than 128 and the rest past the end (17 x 2560 x 9728: 31 us instead of 42; 777 x 1000 x
@@ -617,12 +777,37 @@ ttt_status gated_ffn(const void* X, const void* Wg, const void* Wu, int64_t T, i
   const __nv_bfloat16 *x = static_cast<const __nv_bfloat16*>(X), *wg = static_cast<const __nv_bfloat16*>(Wg),
                       *wu = static_cast<const __nv_bfloat16*>(Wu);
   __nv_bfloat16 *z = static_cast<__nv_bfloat16*>(Z), *g = static_cast<__nv_bfloat16*>(G), *u = static_cast<__nv_bfloat16*>(U);
-  if (T <= 16) {
+  const bool by_rows = takes_rows(T, d, f, num_sms);
+  if (T <= 16 && !by_rows) {
     const int grid = f / 8, threads = 32 * kFewWarps;
     if (T <= 8)
       k_ffn_few<1><<<grid, threads, 0, s>>>(x, wg, wu, (int)T, d, f, act, z, g, u);
     else
       k_ffn_few<2><<<grid, threads, 0, s>>>(x, wg, wu, (int)T, d, f, act, z, g, u);
+    TTT_CUDA(cudaGetLastError());
+    return TTT_OK;
+  }
+  if (by_rows) {
+    RowsArgs a = {};
+    a.T = (int)T;
+    a.f = f;
+    a.kblocks = cdiv(d, FK);
+    const int rounds = cdiv(f, (int64_t)FM * num_sms);
+    a.rows = 2 * cdiv(f, (int64_t)2 * rounds * num_sms);
+    a.cols = 16 * cdiv(T, 16);
+    a.stages = std::min(kRowsMaxStages, kRowsRing / rows_stage(a.rows, a.cols));
+    a.act = act;
+    a.z = z;
+    a.g = g;
+    a.u = u;
+    a.status = DevStatus{status, kWaitLimitNs};
+    CUtensorMap tx, tg, tu;
+    TTT_TRY(map_bf16(&tx, X, d, T, FK, a.cols));
+    TTT_TRY(map_bf16(&tg, Wg, d, f, FK, a.rows));
+    TTT_TRY(map_bf16(&tu, Wu, d, f, FK, a.rows));
+    const int smem = a.stages * rows_stage(a.rows, a.cols) + kRowsSlack + 1024;
+    TTT_CUDA(cudaFuncSetAttribute(k_ffn_rows, cudaFuncAttributeMaxDynamicSharedMemorySize, kRowsRing + kRowsSlack + 1024));
+    k_ffn_rows<<<cdiv(f, a.rows), kRowsThreads, smem, s>>>(tx, tg, tu, a);
     TTT_CUDA(cudaGetLastError());
     return TTT_OK;
   }

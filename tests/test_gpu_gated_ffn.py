@@ -103,6 +103,31 @@ def test_large_and_persistent(cwl):
     assert (z.double() - ref).abs().max() <= 2.0 ** -8 * ref.abs().max() * 1.01
 
 
+@pytest.mark.parametrize("T,d,f", [(T, d, f) for T in (17, 48, 65, 113, 128, 129, 160, 161) for d, f in
+                                   ((8, 9480), (584, 1224), (200, 9608), (72, 20000))]
+                         + [(T, 1032, 9480) for T in (8, 9, 15, 16)])
+def test_some_tens_of_tokens(cwl, T, d, f):
+    """Around the changes of form: one k-block and several rounds of the ring, a last tile with few rows,
+    more rows than one tile an SM takes."""
+    x, wg, wu, _ = _case(T, d, f, T + f)
+    z, g, u = cwl.gated_ffn(x.cuda(), wg.cuda(), wu.cuda(), save=True)
+    _check_forward((z, g, u), x, wg, wu, "silu")
+    big = torch.full((T + 3, f), 7.0, device="cuda", dtype=torch.bfloat16)
+    cwl.gated_ffn(x.cuda(), wg.cuda(), wu.cuda(), out=big[:T])
+    assert torch.equal(big[:T], z) and torch.all(big[T:] == 7.0)
+
+
+def test_a_token_stays_its_own(cwl):
+    """A NaN in one token's row reaches no other token."""
+    for T, f in ((3, 200), (40, 200), (40, 9480), (300, 200)):
+        x, wg, wu, _ = (t.cuda() for t in _case(T, 136, f, 8))
+        want = cwl.gated_ffn(x, wg, wu)
+        x[T // 2] = float("nan")
+        got = cwl.gated_ffn(x, wg, wu)
+        rest = torch.arange(T, device="cuda") != T // 2
+        assert torch.equal(got[rest], want[rest]) and torch.isnan(got[T // 2]).all()
+
+
 def test_outputs_stay_inside(cwl):
     """Rows of a larger buffer behind the call's tokens are left as they were."""
     for T in (5, 40, 300):
