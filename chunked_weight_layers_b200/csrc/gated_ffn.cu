@@ -513,7 +513,7 @@ __global__ void __launch_bounds__(32 * kFewWarps) k_ffn_few(const __nv_bfloat16*
 // bytes of the ring, and are not looked at), so that an epilogue thread finds g and u of its row in its own
 // lane. One tile a CTA, as many rows as spread f evenly over the SMs: bound by the weights' bytes, which
 // pass once, and for more tokens by X's, which every CTA reads from L2. 17 x 4096 x 14336: 40 us (5.9 TB/s),
-// 17 x 8192 x 28672: 148 us (6.3), 17 x 2560 x 9728: 21 us (4.7; the launch's ends are a fifth of it).
+// 17 x 8192 x 28672: 148 us (6.3), 17 x 2560 x 9728: 20.5 us (4.9; the launch's ends are a fifth of it).
 struct RowsArgs {
   int T, f, kblocks, rows, cols, stages;  // cols: T rounded up to 16
   int act;
@@ -521,7 +521,7 @@ struct RowsArgs {
   DevStatus status;
 };
 
-constexpr int kRowsMaxStages = 8, kRowsEpi = 16, kRowsThreads = (2 + kRowsEpi) * 32;
+constexpr int kRowsMaxStages = 8, kRowsEpi = 16, kRowsThreads = (3 + kRowsEpi) * 32;
 constexpr int kRowsSlack = kHalf;       // what the last stage's products read past its rows
 constexpr int kRowsRing = 200 * 1024;
 
@@ -569,9 +569,9 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < a.stages; ++i) {
       mbar_init(&sm.full[i], 1);
-      mbar_init(&sm.empty[i], 1);
+      mbar_init(&sm.empty[i], 2);
     }
-    mbar_init(&sm.done, 1);
+    mbar_init(&sm.done, 2);
     sm.abort = 0;
     fence_barrier_init();
     for (int kb = 0; kb < min(a.stages, a.kblocks); ++kb) load(kb, kb);
@@ -596,31 +596,30 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       // Nothing may still land in this CTA's shared memory when it exits.
       for (int k = max(0, kb - a.stages); k < kb; ++k) mbar_wait(&sm.full[k % a.stages], (k / a.stages) & 1, a.status, nullptr);
     }
-  } else if (warp == 1) {
+  } else if (warp <= 2) {
+    // One thread issues the gate's products, another up's: beside the products (47 cycles each) a k-block
+    // costs the issuing thread some 400 cycles.
     if (lane == 0) {
-      const uint32_t idesc = tc::idesc_bf16(128, a.cols, 0, 0);
+      const bool second = warp == 2;
+      const uint32_t idesc = tc::idesc_bf16(128, a.cols, 0, 0), acc = tmem + (second ? up : 0), skip = second ? part >> 4 : 0;
       const uint32_t first = tc::desc_of(ring);
       bool ok = true;
-      uint32_t s = 0, round = 0, dg = first;
+      uint32_t s = 0, round = 0;
       for (int kb = 0; kb < a.kblocks; ++kb) {
         if (!(ok = mbar_wait(&sm.full[s], round & 1, a.status, abort))) break;
         tc::fence_after();
-        const uint32_t du = dg + (part >> 4), dx = du + (part >> 4);
+        const uint32_t dw = first + s * (stage >> 4) + skip, dx = first + s * (stage >> 4) + (2 * part >> 4);
 #pragma unroll
-        for (int kk = 0; kk < FK / 16; ++kk) {
-          tc::mma(tmem, tc::desc_at(dg, kk * 32), tc::desc_at(dx, kk * 32), idesc, kb != 0 || kk != 0);
-          tc::mma(tmem + up, tc::desc_at(du, kk * 32), tc::desc_at(dx, kk * 32), idesc, kb != 0 || kk != 0);
-        }
+        for (int kk = 0; kk < FK / 16; ++kk) tc::mma(acc, tc::desc_at(dw, kk * 32), tc::desc_at(dx, kk * 32), idesc, kb != 0 || kk != 0);
         tc::commit(&sm.empty[s]);
-        dg += stage >> 4;
-        if (++s == (uint32_t)a.stages) s = 0, ++round, dg = first;
+        if (++s == (uint32_t)a.stages) s = 0, ++round;
       }
       tc::commit(&sm.done);  // of all products, so that TMEM can be freed
       if (!ok) *abort = 1;
     }
   }
   __syncwarp();
-  if (warp >= 2) {
+  if (warp >= 3) {
     const int q = warp & 3, r = 32 * q + lane;
     const bool in = r < a.rows && f0 + r < a.f;
     const bool ok = mbar_wait(&sm.done, 0, a.status, nullptr);
@@ -629,7 +628,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       const uint32_t tb = tmem + ((uint32_t)(32 * q) << 16);
       const size_t at = (size_t)f0 + r;
 #pragma unroll 1
-      for (int c = 8 * ((warp - 2) >> 2); c < a.cols; c += 8 * (kRowsEpi / 4)) {
+      for (int c = 8 * ((warp - 3) >> 2); c < a.cols; c += 8 * (kRowsEpi / 4)) {
         uint32_t g[8], u[8];
         ld8(tb + c, g);
         ld8(tb + up + c, u);
@@ -670,14 +669,14 @@ int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
 int pairs_of(int num_sms) { return std::max(1, num_sms / 2); }
 
-// Up to 8 tokens take k_ffn_few, and up to 16 where the weights are short or narrow. k_ffn_rows takes up to
-// 160 where the pairs would need a second round of tiles, which costs them as much as the first (f above 9472
-// on 148 SMs): 17 x 2560 x 9728: 21 us against 31, 128 tokens: 27 against 31, 192: 35 against 33; 17 x 8192 x
-// 28672: 148 against 278. In one round the pairs are as fast or faster (17 x 2048 x 7168: 17.3 against 17.6, 128
-// tokens: 18.7 against 22.8). 16 x 2048 x 11264: 19 us against 29 of k_ffn_few; 16 x 512 x 28672: 17.5 against
-// 15.6.
+// k_ffn_rows takes up to 160 tokens where the pairs would need a second round of tiles, which costs them as
+// much as the first (f above 9472 on 148 SMs): 17 x 2560 x 9728: 20.5 us against 31, 128 tokens: 27 against 31,
+// 192: 35 against 33; 17 x 8192 x 28672: 148 against 278. In one round the pairs are as fast or faster (17 x 2048
+// x 7168: 17.3 against 17.6, 128 tokens: 18.7 against 22.8). Against k_ffn_few it needs long rows: 8 x 2560 x
+// 9728: 20 us against 18, 8 x 4096 x 14336: 41 against 46 (one token: 40 against 42); 16 x 512 x 28672: 17.5
+// against 15.6, 16 x 2048 x 11264: 19 against 29.
 bool takes_rows(int64_t T, int d, int f, int num_sms) {
-  return f > FM * pairs_of(num_sms) && T <= 160 && (T > 16 || (T > 8 && d >= 1024));
+  return f > FM * pairs_of(num_sms) && T <= 160 && T > (d >= 4096 ? 0 : d >= 1024 ? 8 : 16);
 }
 
 // Tokens of a tile that each CTA of the pair takes: the fewest, in steps of eight, that cover them in this

@@ -105,7 +105,7 @@ def test_large_and_persistent(cwl):
 
 @pytest.mark.parametrize("T,d,f", [(T, d, f) for T in (17, 48, 65, 113, 128, 129, 160, 161) for d, f in
                                    ((8, 9480), (584, 1224), (200, 9608), (72, 20000))]
-                         + [(T, 1032, 9480) for T in (8, 9, 15, 16)])
+                         + [(T, 1032, 9480) for T in (8, 9, 15, 16)] + [(T, 4104, 9480) for T in (1, 2, 8)])
 def test_some_tens_of_tokens(cwl, T, d, f):
     """Around the changes of form: one k-block and several rounds of the ring, a last tile with few rows,
     more rows than one tile an SM takes."""
