@@ -30,10 +30,11 @@
 // segments: the states that the segments add are found first (k_gs_segment), combined in order, and
 // then every segment runs from its own start.
 //
-// What bounds it (B200, 8 x 12 heads x 2048 tokens and 4 x 16 x 8192). Forward: k_gs_out takes 5700
-// cycles for a chunk on each of an SM's two CTAs, the rate at which HBM delivers a chunk's 64 KB; the
-// pass over K and V for the segments' starts and the launches' first and last microseconds come on top
-// (41 us, where the bytes need 16). Backward: shared memory, through which a chunk's operands and
+// What bounds it (B200, 8 x 12 heads x 2048 tokens and 4 x 16 x 8192). Forward: a chunk's chain (scores,
+// their weights, P·V, outputs; 5200 cycles for a CTA alone on its SM, 5700 for each of two, whose TMEM leaves
+// no room for a third), at two thirds of the rate at which HBM could deliver its 64 KB; the pass over K and V
+// for the segments' starts and the launches' first and last microseconds come on top (41 us, where the bytes
+// need 16). Backward: shared memory, through which a chunk's operands and
 // results pass (some 650 KB, and the products' operands once more, come to 8500 cycles): 10500 cycles a
 // chunk (210 us of 305, where the bytes need 74), the state passes the rest. The state before every chunk
 // is kept in pieces of eight columns, all rows of a piece after each other: a warp then writes whole
