@@ -420,7 +420,11 @@ __global__ void __launch_bounds__(256) k_ffn_act_bwd(const __nv_bfloat16* __rest
 // w takes every fourth 32-wide slice of the sum, the next slices' loads in flight while it works on
 // these, and the warps' results are added in order at the end. A lane's 16-byte load holds eight
 // consecutive k of one row; the products' k slots are filled in that order for the weights and for X
-// alike, which a sum does not mind. NT: token blocks of eight.
+// alike, which a sum does not mind. NT: token blocks of eight; MT: such blocks of rows a CTA, two for the two
+// blocks of tokens, since every CTA reads all of X (9 x 5120 x 5120: 23 us against 31 with one). The CTAs
+// an SM must hold leave room for the loads to go ahead of the products: left to itself the compiler took few
+// registers and 22 us for one token of 5120 x 5120, so 17.4; six CTAs: 18.6; for two blocks of rows three:
+// 23, five: 27.
 constexpr int kFewWarps = 4;
 
 __device__ __forceinline__ uint4 load_once(const __nv_bfloat16* p) {
@@ -429,32 +433,35 @@ __device__ __forceinline__ uint4 load_once(const __nv_bfloat16* p) {
   return v;
 }
 
-template <int NT>
-__global__ void __launch_bounds__(32 * kFewWarps) k_ffn_few(const __nv_bfloat16* __restrict__ X, const __nv_bfloat16* __restrict__ Wg,
+template <int NT, int MT>
+__global__ void __launch_bounds__(32 * kFewWarps, MT == 1 ? 5 : 3) k_ffn_few(const __nv_bfloat16* __restrict__ X, const __nv_bfloat16* __restrict__ Wg,
                                                             const __nv_bfloat16* __restrict__ Wu, int T, int d, int f, int act,
                                                             __nv_bfloat16* __restrict__ z, __nv_bfloat16* __restrict__ gout,
                                                             __nv_bfloat16* __restrict__ uout) {
-  __shared__ float part[kFewWarps][2][8 * NT][9];  // [warp][gate, up][token][row]
+  __shared__ float part[kFewWarps][2][8 * NT][8 * MT + 1];  // [warp][gate, up][token][row]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-  const int f0 = blockIdx.x * 8;  // f is a multiple of 8
+  const int f0 = blockIdx.x * 8 * MT, blocks = min(MT, (f - f0) / 8);  // f is a multiple of 8
   const int steps = (d + 31) / 32;
   constexpr int UN = 2;  // slices in flight: more take registers from the warps that hide the latency (4: 22 us, 2: 17)
   const __nv_bfloat16* pg = Wg + (size_t)(f0 + g) * d + 8 * q;
   const __nv_bfloat16* pu = Wu + (size_t)(f0 + g) * d + 8 * q;
   const __nv_bfloat16* px = X + (size_t)g * d + 8 * q;
   const uint4 none = make_uint4(0, 0, 0, 0);
-  uint4 wg[2][UN], wu[2][UN];
-  auto fetch = [&](int st, uint4 (&G)[UN], uint4 (&U)[UN]) {
+  uint4 wg[2][UN][MT], wu[2][UN][MT];
+  auto fetch = [&](int st, uint4 (&G)[UN][MT], uint4 (&U)[UN][MT]) {
 #pragma unroll
     for (int i = 0; i < UN; ++i) {
       const int k = (st + kFewWarps * i) * 32;
-      const bool in = k + 8 * q < d;
-      G[i] = in ? load_once(pg + k) : none;
-      U[i] = in ? load_once(pu + k) : none;
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        const bool in = k + 8 * q < d && m < blocks;
+        G[i][m] = in ? load_once(pg + (size_t)(8 * m) * d + k) : none;
+        U[i][m] = in ? load_once(pu + (size_t)(8 * m) * d + k) : none;
+      }
     }
   };
-  float acc[NT][4] = {};
-  auto work = [&](int st, const uint4 (&G)[UN], const uint4 (&U)[UN]) {
+  float acc[MT][NT][4] = {};
+  auto work = [&](int st, const uint4 (&G)[UN][MT], const uint4 (&U)[UN][MT]) {
     uint4 x[UN][NT];
 #pragma unroll
     for (int i = 0; i < UN; ++i) {
@@ -464,14 +471,16 @@ __global__ void __launch_bounds__(32 * kFewWarps) k_ffn_few(const __nv_bfloat16*
         x[i][nt] = k + 8 * q < d && 8 * nt + g < T ? *reinterpret_cast<const uint4*>(px + (size_t)(8 * nt) * d + k) : none;
     }
 #pragma unroll
-    for (int i = 0; i < UN; ++i) {
-      const uint32_t a0[4] = {G[i].x, U[i].x, G[i].y, U[i].y}, a1[4] = {G[i].z, U[i].z, G[i].w, U[i].w};
+    for (int i = 0; i < UN; ++i)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        wm::mma(acc[nt], a0, x[i][nt].x, x[i][nt].y);
-        wm::mma(acc[nt], a1, x[i][nt].z, x[i][nt].w);
+      for (int m = 0; m < MT; ++m) {
+        const uint32_t a0[4] = {G[i][m].x, U[i][m].x, G[i][m].y, U[i][m].y}, a1[4] = {G[i][m].z, U[i][m].z, G[i][m].w, U[i][m].w};
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          wm::mma(acc[m][nt], a0, x[i][nt].x, x[i][nt].y);
+          wm::mma(acc[m][nt], a1, x[i][nt].z, x[i][nt].w);
+        }
       }
-    }
   };
   constexpr int kStep = kFewWarps * UN;
   fetch(warp, wg[0], wu[0]);
@@ -483,13 +492,15 @@ __global__ void __launch_bounds__(32 * kFewWarps) k_ffn_few(const __nv_bfloat16*
   }
   // A lane holds row g of the gate (0, 1) and of up (2, 3) for tokens 2q, 2q + 1 of each block.
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
+  for (int m = 0; m < MT; ++m)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) part[warp][e >> 1][8 * nt + 2 * q + (e & 1)][g] = acc[nt][e];
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) part[warp][e >> 1][8 * nt + 2 * q + (e & 1)][8 * m + g] = acc[m][nt][e];
   __syncthreads();
-  for (int i = threadIdx.x; i < NT * 64; i += 32 * kFewWarps) {
-    const int r = i & 7, t = i >> 3;
-    if (t >= T) continue;
+  for (int i = threadIdx.x; i < NT * MT * 64; i += 32 * kFewWarps) {
+    const int r = i % (8 * MT), t = i / (8 * MT);
+    if (t >= T || r >= 8 * blocks) continue;
     float sg = 0.f, su = 0.f;
 #pragma unroll
     for (int w = 0; w < kFewWarps; ++w) {
@@ -672,11 +683,11 @@ int pairs_of(int num_sms) { return std::max(1, num_sms / 2); }
 // k_ffn_rows takes up to 160 tokens where the pairs would need a second round of tiles, which costs them as
 // much as the first (f above 9472 on 148 SMs): 17 x 2560 x 9728: 20.5 us against 31, 128 tokens: 27 against 31,
 // 192: 35 against 33; 17 x 8192 x 28672: 148 against 278. In one round the pairs are as fast or faster (17 x 2048
-// x 7168: 17.3 against 17.6, 128 tokens: 18.7 against 22.8). Against k_ffn_few it needs long rows: 8 x 2560 x
-// 9728: 20 us against 18, 8 x 4096 x 14336: 41 against 46 (one token: 40 against 42); 16 x 512 x 28672: 17.5
-// against 15.6, 16 x 2048 x 11264: 19 against 29.
+// x 7168: 17.3 against 17.6, 128 tokens: 18.7 against 22.8). Against k_ffn_few it needs more than 8 tokens and
+// long rows: 16 x 4096 x 14336: 41 us against 52, 16 x 512 x 28672: 17.5 against 15.4; 8 x 4096 x 14336: 41
+// against 39.5.
 bool takes_rows(int64_t T, int d, int f, int num_sms) {
-  return f > FM * pairs_of(num_sms) && T <= 160 && T > (d >= 4096 ? 0 : d >= 1024 ? 8 : 16);
+  return f > FM * pairs_of(num_sms) && T <= 160 && T > (d >= 1024 ? 8 : 16);
 }
 
 // Tokens of a tile that each CTA of the pair takes: the fewest, in steps of eight, that cover them in this
@@ -778,11 +789,11 @@ ttt_status gated_ffn(const void* X, const void* Wg, const void* Wu, int64_t T, i
   __nv_bfloat16 *z = static_cast<__nv_bfloat16*>(Z), *g = static_cast<__nv_bfloat16*>(G), *u = static_cast<__nv_bfloat16*>(U);
   const bool by_rows = takes_rows(T, d, f, num_sms);
   if (T <= 16 && !by_rows) {
-    const int grid = f / 8, threads = 32 * kFewWarps;
+    const int threads = 32 * kFewWarps;
     if (T <= 8)
-      k_ffn_few<1><<<grid, threads, 0, s>>>(x, wg, wu, (int)T, d, f, act, z, g, u);
+      k_ffn_few<1, 1><<<f / 8, threads, 0, s>>>(x, wg, wu, (int)T, d, f, act, z, g, u);
     else
-      k_ffn_few<2><<<grid, threads, 0, s>>>(x, wg, wu, (int)T, d, f, act, z, g, u);
+      k_ffn_few<2, 2><<<cdiv(f, 16), threads, 0, s>>>(x, wg, wu, (int)T, d, f, act, z, g, u);
     TTT_CUDA(cudaGetLastError());
     return TTT_OK;
   }
