@@ -122,10 +122,12 @@ __global__ void __launch_bounds__(128) k_gs_combine(const GsArgs a, const float*
 constexpr int kL = 128;                   // tokens per chunk
 constexpr int kLTile = kL * 128;          // bytes of a [128][64] bf16 tile with 128-byte rows
 
-// A chunk's gates, made by one warp a chunk ahead. Every decay is the sum of the gates it spans,
-// never a difference of longer sums, except within a block of 32 tokens.
+// A chunk's gates, made by one warp a chunk ahead. A decay between two tokens is a difference of sums from
+// the chunk's start, which gates that both sums hold (150 for each document's start before the two) can make far
+// longer than itself; so the sums are made in 64 bits and kept as two fp32 numbers.
 struct __align__(16) Gates {
   float b[kL];    // sum from the chunk's start up to and with token t
+  float lo[kL];   // what the rounding of b left
   float end[kL];  // 2^(sum of the gates after t to the end of t's block of 32)
   float w[kL];    // 2^(sum of the gates after t to the chunk's end)
   float total;    // sum of all
@@ -145,12 +147,15 @@ __device__ __forceinline__ void fetch_gates(const GsArgs& a, const float* gp, in
   wm::cp_commit();
 }
 
-// From the raw gates of the last fetch_gates of this warp.
+// From the raw gates of the last fetch_gates of this warp. Sum: float makes no lo, for decays from or to the
+// chunk's ends alone (64 bits cost k_gs_segment 1 us of 16).
+template <class Sum>
 __device__ __forceinline__ void make_gates(const float* raw, Gates& s, int lane) {
   wm::cp_wait<0>();
   __syncwarp();
   const float4 r = *reinterpret_cast<const float4*>(raw + 4 * lane);
-  float x[4] = {r.x, r.y, r.z, r.w}, pre[4];
+  float x[4] = {r.x, r.y, r.z, r.w};
+  Sum pre[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     x[i] *= kLog2e;
@@ -160,10 +165,12 @@ __device__ __forceinline__ void make_gates(const float* raw, Gates& s, int lane)
 #pragma unroll
   for (int i = 1; i < 4; ++i) pre[i] = pre[i - 1] + x[i];
   // Inclusive sums over the lanes up to this one, from this one on, and from it to the end of its eight.
-  float up = pre[3], down = pre[3], seg = pre[3];
+  Sum up = pre[3];
+  float down = (float)pre[3], seg = down;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const float u = __shfl_up_sync(0xffffffffu, up, o), d = __shfl_down_sync(0xffffffffu, down, o);
+    const Sum u = __shfl_up_sync(0xffffffffu, up, o);
+    const float d = __shfl_down_sync(0xffffffffu, down, o);
     if (lane >= o) up += u;
     if (lane + o < 32) down += d;
     if (o < 8) {
@@ -172,22 +179,29 @@ __device__ __forceinline__ void make_gates(const float* raw, Gates& s, int lane)
     }
   }
   // The neighbours' sums are those without this lane (a subtraction would cancel).
-  float base = __shfl_up_sync(0xffffffffu, up, 1), after = __shfl_down_sync(0xffffffffu, down, 1),
-        after8 = __shfl_down_sync(0xffffffffu, seg, 1);
-  if (lane == 0) base = 0.f;
+  Sum base = __shfl_up_sync(0xffffffffu, up, 1);
+  float after = __shfl_down_sync(0xffffffffu, down, 1), after8 = __shfl_down_sync(0xffffffffu, seg, 1);
+  if (lane == 0) base = 0;
   if (lane == 31) after = 0.f;
   if ((lane & 7) == 7) after8 = 0.f;
-  float w[4], e[4], suf = 0.f;
+  float b[4], lo[4], w[4], e[4], suf = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const Sum sum = base + pre[i];
+    b[i] = (float)sum;
+    if constexpr (sizeof(Sum) == 8) lo[i] = (float)(sum - b[i]);
+  }
 #pragma unroll
   for (int i = 3; i >= 0; --i) {
     w[i] = exp2_fast(after + suf);
     e[i] = exp2_fast(after8 + suf);
     suf += x[i];
   }
-  *reinterpret_cast<float4*>(s.b + 4 * lane) = make_float4(base + pre[0], base + pre[1], base + pre[2], base + pre[3]);
+  *reinterpret_cast<float4*>(s.b + 4 * lane) = make_float4(b[0], b[1], b[2], b[3]);
+  if constexpr (sizeof(Sum) == 8) *reinterpret_cast<float4*>(s.lo + 4 * lane) = make_float4(lo[0], lo[1], lo[2], lo[3]);
   *reinterpret_cast<float4*>(s.w + 4 * lane) = make_float4(w[0], w[1], w[2], w[3]);
   *reinterpret_cast<float4*>(s.end + 4 * lane) = make_float4(e[0], e[1], e[2], e[3]);
-  if (lane == 31) s.total = up;
+  if (lane == 31) s.total = (float)up;
   __syncwarp();  // the raw gates have been read
 }
 
@@ -498,7 +512,7 @@ __global__ void __launch_bounds__(256, 2) k_gs_segment(const __grid_constant__ S
   if (warp == 4) tc::alloc(&sm.tmem, 128);
   if (warp == 3) {
     fetch_gates(a, gp, (int64_t)chunk_of(0) * kL, sm.raw[0], lane);
-    make_gates(sm.raw[0], sm.gates[0], lane);
+    make_gates<float>(sm.raw[0], sm.gates[0], lane);
     if (n > 1) fetch_gates(a, gp, (int64_t)chunk_of(1) * kL, sm.raw[1], lane);
   }
   // Half a row of chunk i's X: its first term in place, its second beside.
@@ -537,7 +551,7 @@ __global__ void __launch_bounds__(256, 2) k_gs_segment(const __grid_constant__ S
         tc::commit(&sm.done[ph]);
       }
       if (warp == 3 && i + 1 < n) {
-        make_gates(sm.raw[ph ^ 1], sm.gates[(i + 1) % 3], lane);
+        make_gates<float>(sm.raw[ph ^ 1], sm.gates[(i + 1) % 3], lane);
         if (i + 2 < n) fetch_gates(a, gp, (int64_t)chunk_of(i + 2) * kL, sm.raw[ph], lane);
       }
       group_sync(1);  // the next chunk's gates are there
@@ -684,7 +698,7 @@ __global__ void __launch_bounds__(256, 2)
         }
       }
       __syncwarp();
-      const float bi_ = gt.b[id];
+      const float bi_ = gt.b[id], lo_ = gt.lo[id];
       const float u = a.scale * exp2_fast(bi_);
       mbar_wait(&sm.scores, ph, a.status, &sm.abort);
       tc::fence_after();
@@ -693,7 +707,7 @@ __global__ void __launch_bounds__(256, 2)
       uint32_t sc[32], p[16];
       tc::ld32(tmem, sc);
       for (int jb = 0; jb < warp; ++jb) {
-        const float f = a.scale * exp2_fast(bi_ - gt.b[32 * jb + 31]);
+        const float f = a.scale * exp2_fast((bi_ - gt.b[32 * jb + 31]) + (lo_ - gt.lo[32 * jb + 31]));
         const F2 ff = f2(f, f);
         tc::wait_ld();
 #pragma unroll
@@ -706,12 +720,14 @@ __global__ void __launch_bounds__(256, 2)
         tc::st16(tmem + kColP + 16 * jb, p);
       }
       {
-        const F2 bb = f2(bi_, bi_), one = f2(-1.f, -1.f), sl = f2(a.scale, a.scale);
+        const F2 bb = f2(bi_, bi_), ll = f2(lo_, lo_), one = f2(-1.f, -1.f), sl = f2(a.scale, a.scale);
         tc::wait_ld();
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
           const ulonglong2 bj = *reinterpret_cast<const ulonglong2*>(gt.b + 32 * warp + 4 * c);
-          const float2 x = split(fma2(one, F2{bj.x}, bb)), y = split(fma2(one, F2{bj.y}, bb));
+          const ulonglong2 lj = *reinterpret_cast<const ulonglong2*>(gt.lo + 32 * warp + 4 * c);
+          const float2 x = split(add(fma2(one, F2{bj.x}, bb), fma2(one, F2{lj.x}, ll)));
+          const float2 y = split(add(fma2(one, F2{bj.y}, bb), fma2(one, F2{lj.y}, ll)));
           p[2 * c] = causal(to_bf16(mul(mul(sl, f2(exp2_fast(x.x), exp2_fast(x.y))), f2u(sc[4 * c], sc[4 * c + 1]))), lane - 4 * c);
           p[2 * c + 1] =
               causal(to_bf16(mul(mul(sl, f2(exp2_fast(y.x), exp2_fast(y.y))), f2u(sc[4 * c + 2], sc[4 * c + 3]))), lane - 4 * c - 2);
@@ -770,7 +786,7 @@ __global__ void __launch_bounds__(256, 2)
     F2 S[32];
     if (warp == 7) {
       fetch_gates(a, gp, (int64_t)c0 * kL, sm.raw[0], lane);
-      make_gates(sm.raw[0], sm.gates[0], lane);
+      make_gates<double>(sm.raw[0], sm.gates[0], lane);
       if (n > 1) fetch_gates(a, gp, (int64_t)(c0 + 1) * kL, sm.raw[1], lane);
     }
     before_results();
@@ -807,7 +823,7 @@ __global__ void __launch_bounds__(256, 2)
       update_state(S, tmem + kColD, sm.W[1], id, exp2_fast(gt.total), 2);
       if (id < 64) put_state_row(sm.S, S, id);
       if (warp == 7 && i + 1 < n) {
-        make_gates(sm.raw[ph ^ 1], sm.gates[ph ^ 1], lane);
+        make_gates<double>(sm.raw[ph ^ 1], sm.gates[ph ^ 1], lane);
         if (i + 2 < n) fetch_gates(a, gp, (int64_t)(c0 + i + 2) * kL, sm.raw[ph], lane);
       }
       fence_proxy_async_smem();
@@ -1004,7 +1020,7 @@ __global__ void __launch_bounds__(512, 1) k_gs_bwd(const __grid_constant__ BwdTi
     put_ds(sm, S, id);
     if (warp == 11) {
       fetch_gates(a, gp, (int64_t)(c1 - 1) * kL, sm.raw[0], lane);
-      make_gates(sm.raw[0], sm.gates[0], lane);
+      make_gates<double>(sm.raw[0], sm.gates[0], lane);
       if (n > 1) fetch_gates(a, gp, (int64_t)(c1 - 2) * kL, sm.raw[1], lane);
     }
     fence_proxy_async_smem();
@@ -1049,7 +1065,7 @@ __global__ void __launch_bounds__(512, 1) k_gs_bwd(const __grid_constant__ BwdTi
       put_ds(sm, S, id);
       fence_proxy_async_smem();
       if (warp == 11 && i + 1 < n) {
-        make_gates(sm.raw[(i + 1) % 3], sm.gates[ph ^ 1], lane);
+        make_gates<double>(sm.raw[(i + 1) % 3], sm.gates[ph ^ 1], lane);
         if (i + 2 < n) fetch_gates(a, gp, (int64_t)(chunk - 2) * kL, sm.raw[(i + 2) % 3], lane);
       }
       tc::fence_before();
@@ -1137,11 +1153,12 @@ __global__ void __launch_bounds__(512, 1) k_gs_bwd(const __grid_constant__ BwdTi
         // lane holds four queries and four keys, so a key's sum over the warp's queries takes four
         // exchanges for 16 keys, where whole rows in a lane would take 16.
         const int w = warp & 3, fg = lane >> 2, fq = lane & 3;
-        float br[4];
+        float br[4], lr[4];
         F2 sum[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           br[r] = gt.b[32 * w + 8 * r + fg];
+          lr[r] = gt.lo[32 * w + 8 * r + fg];
           sum[r] = f2(0.f, 0.f);
         }
         mbar_wait(&sm.scores, ph, a.status, &sm.abort);
@@ -1161,10 +1178,10 @@ __global__ void __launch_bounds__(512, 1) k_gs_bwd(const __grid_constant__ BwdTi
             }
           F2 dec[2][2][4];  // the decays, scaled: [16 keys][8 keys][queries]
           if (jb < w) {
-            const float end = gt.b[32 * jb + 31];
+            const float end = gt.b[32 * jb + 31], lend = gt.lo[32 * jb + 31];
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-              const float f = a.scale * exp2_fast(br[r] - end);
+              const float f = a.scale * exp2_fast((br[r] - end) + (lr[r] - lend));
 #pragma unroll
               for (int c = 0; c < 4; ++c)
                 dec[c >> 1][c & 1][r] = mul(f2(f, f), *reinterpret_cast<const F2*>(gt.end + 32 * jb + 8 * c + 2 * fq));
@@ -1173,10 +1190,12 @@ __global__ void __launch_bounds__(512, 1) k_gs_bwd(const __grid_constant__ BwdTi
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
               const float2 b = *reinterpret_cast<const float2*>(gt.b + 32 * jb + 8 * c + 2 * fq);
+              const float2 lo = *reinterpret_cast<const float2*>(gt.lo + 32 * jb + 8 * c + 2 * fq);
 #pragma unroll
               for (int r = 0; r < 4; ++r) {
                 const int own = 8 * (r - c) + fg - 2 * fq;  // the query's place after the pair's first key
-                dec[c >> 1][c & 1][r] = f2(own >= 0 ? a.scale * exp2_fast(br[r] - b.x) : 0.f, own > 0 ? a.scale * exp2_fast(br[r] - b.y) : 0.f);
+                dec[c >> 1][c & 1][r] = f2(own >= 0 ? a.scale * exp2_fast((br[r] - b.x) + (lr[r] - lo.x)) : 0.f,
+                                           own > 0 ? a.scale * exp2_fast((br[r] - b.y) + (lr[r] - lo.y)) : 0.f);
               }
             }
           }
