@@ -1177,6 +1177,10 @@ __global__ void __launch_bounds__(512, 1) k_gs_bwd(const __grid_constant__ BwdTi
               tc::ld_frag16(tmem + ((uint32_t)(16 * h) << 16) + kColDp + 32 * jb + 16 * sub, d[sub][h]);
             }
           F2 dec[2][2][4];  // the decays, scaled: [16 keys][8 keys][queries]
+          // A token's own pair would drop out of dg, being in its row's and its column's sum alike, but only up to
+          // rounding: its decay is 1, and in a head that forgets fast the pairs that dg is made of are lost beside it
+          // (gates of -12: dg off by 4e-2, without the own pairs 7e-7).
+          const bool own_first = jb == w && fg == 2 * fq, own_second = jb == w && fg == 2 * fq + 1;
           if (jb < w) {
             const float end = gt.b[32 * jb + 31], lend = gt.lo[32 * jb + 31];
 #pragma unroll
@@ -1212,8 +1216,11 @@ __global__ void __launch_bounds__(512, 1) k_gs_bwd(const __grid_constant__ BwdTi
                 const F2 sc = f2u(sp[0], sp[1]), at = mul(dec[sub][n][r], f2u(dp[0], dp[1]));
                 sp[0] = to_bf16(mul(dec[sub][n][r], sc));
                 dp[0] = to_bf16(at);
-                // A token's own pair is in its row's and its column's sum alike, and drops out of dg.
-                const F2 m = mul(at, sc);
+                F2 m = mul(at, sc);
+                if (r == 2 * sub + n) {  // the eight queries and the eight keys are the same tokens
+                  const float2 f = split(m);
+                  m = f2(own_first ? 0.f : f.x, own_second ? 0.f : f.y);
+                }
                 sum[r] = add(sum[r], m);
                 col[n] = r == 0 ? m : add(col[n], m);
               }

@@ -1,4 +1,5 @@
-"""The gated scan where gates are extreme: many document starts before a document.
+"""The gated scan where gates are extreme: many document starts before a document, and heads that forget
+nearly all at each token.
 
 dg is fp32 and made of sums over pairs m_ij = A_ij·(q_i·k_j), i >= t > j. With q·k and do·v sums of 64
 products of bf16 numbers, each off by at most 64 steps of 2^-23 of its terms' size, a decay off by 2^-21
@@ -56,3 +57,30 @@ def test_a_document_after_many_short_ones(cwl, before, at):
         for t in range(at + 1, 128):
             bound = (2.0 ** -16 + 2.0 ** -20) * off[t:, :t].sum() + 2.0 ** -18 * (off.sum() + own.sum())
             assert abs(got[0, h, t] - want[0, h, t]) <= bound, (h, t, got[0, h, t], want[0, h, t], bound)
+
+
+@pytest.mark.parametrize("strength", [8.0, 12.0, 16.0, 20.0])
+@pytest.mark.parametrize("T", [40, 128, 300])
+@pytest.mark.parametrize("initial", [False, True])
+def test_small_gates_keep_their_gradients(cwl, strength, T, initial):
+    """Every head forgets nearly all at each token: dg is e^-strength of a token's own pair, and is right
+    relative to itself. Its parts from beyond the chunk come from states and operands of 2^-16, so 2^-15
+    of the terms; where gates are -20 the nearest pair's decay spans 29 base-2 units, which their sums
+    give to 2^-18."""
+    r = torch.Generator().manual_seed(int(strength) + T)
+    q, k, v, do = (torch.randn((1, 2, T, 64), generator=r).bfloat16() for _ in range(4))
+    g = -strength - 0.5 * torch.rand((1, 2, T), generator=r)
+    S0, dS = (torch.randn((1, 2, 64, 64), generator=r) if initial else None for _ in range(2))
+    c = [t.cuda() if t is not None else None for t in (do, q, k, v, g, S0, dS)]
+    got = to_np(cwl.gated_scan_backward(*c[:5], scale=0.125, initial=c[5], dfinal=c[6])[3])
+    n = [to_np(t) if t is not None else None for t in (do, q, k, v, g, S0, dS)]
+    a = [np.abs(t) if t is not None and i != 4 else t for i, t in enumerate(n)]
+    want = op.gated_scan_backward(*n[:5], 0.125, *n[5:])[3]
+    top = op.gated_scan_backward(*a[:5], 0.125, *a[5:])[3]
+    for h in range(2):
+        for t0 in range(0, T, 128):
+            e = slice(t0, min(T, t0 + 128))
+            off, _ = _pairs(n[1][0, h, e], n[2][0, h, e], n[3][0, h, e], n[0][0, h, e], n[4][0, h, e], 0.125)
+            bound = (2.0 ** -15 + 2.0 ** -18) * top[0, h, e] + 2.0 ** -18 * off.sum()
+            err = np.abs(got[0, h, e] - want[0, h, e])
+            assert np.all(err <= bound), f"{np.max(err / bound):.3g} x the bound"
