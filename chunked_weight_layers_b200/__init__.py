@@ -23,10 +23,11 @@ import torch
 from . import abi
 from .abi import TTTError, check  # noqa: F401
 from .ops import (gated_ffn, gated_ffn_backward, gated_scan, gated_scan_backward, gated_scan_step,  # noqa: F401
-                  qk_norm_rope, qk_norm_rope_backward, rope_frequencies)
+                  poll_operators, qk_norm_rope, qk_norm_rope_backward, rope_frequencies)
 
 __all__ = ["FastWeightState", "TTTError", "config", "abi", "qk_norm_rope", "qk_norm_rope_backward", "rope_frequencies",
-           "gated_scan", "gated_scan_backward", "gated_scan_step", "gated_ffn", "gated_ffn_backward"]
+           "gated_scan", "gated_scan_backward", "gated_scan_step", "gated_ffn", "gated_ffn_backward",
+           "poll_operators"]
 
 
 # torch's current CUDA device of this thread (its direct accessor when present: it is called

@@ -147,6 +147,8 @@ _SIGNATURES = {
     "ttt_last_error_string": (ctypes.c_char_p, []),
     "ttt_target_values_noalloc": (_st, [_vp, _vp, _vp, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32,
                                         ctypes.c_int32, ctypes.c_int32, _vp, _vp, _vp]),
+    "ttt_operators_poll": (_st, []),
+    "ttt_operators_set_option": (_st, [_i32, _i64]),
     "ttt_qk_norm_rope": (_st, [_vp] * 10),
     "ttt_qk_norm_rope_workspace": (_sz, [_vp]),
     "ttt_qk_norm_rope_backward": (_st, [_vp] * 14 + [_sz, _vp]),

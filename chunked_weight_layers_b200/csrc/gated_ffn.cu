@@ -74,6 +74,7 @@ struct FfnArgs {
   __nv_bfloat16 *z, *g, *u;  // FWD: outputs (g and u or null); DX: z = dX; DW: g = dWg, u = dWu
   float* part;               // [tiles after the whole ones][splits][256][256]
   DevStatus status;
+  int stall;                 // a k-block of every pair that is never loaded (tests), or -1
 };
 
 __device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
@@ -191,6 +192,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
             ok = false;
             break;
           }
+          if ((int)it == a.stall) continue;
           uint8_t *sa = sm.ring[s], *sb = sa + kHalf;
           // Both CTAs' loads complete on the first CTA's barrier, which expects the bytes of both.
           if (rank == 0) mbar_arrive_expect_tx(&sm.full[s], 2 * (a.rows + bcols) * FK * 2);
@@ -530,6 +532,7 @@ struct RowsArgs {
   int act;
   __nv_bfloat16 *z, *g, *u;  // g and u or null
   DevStatus status;
+  int stall;  // a k-block that is never loaded (tests), or -1
 };
 
 constexpr int kRowsMaxStages = 8, kRowsEpi = 16, kRowsThreads = (3 + kRowsEpi) * 32;
@@ -571,6 +574,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
   const uint32_t up = a.cols <= 128 ? 128 : 256;  // TMEM column of the second accumulator
   volatile int* abort = &sm.abort;
   auto load = [&](int kb, int s) {
+    if (kb == a.stall) return;
     uint8_t* p = ring + s * stage;
     mbar_arrive_expect_tx(&sm.full[s], (2 * a.rows + a.cols) * FK * 2);
     tma_load_2d(p, &tmG, &sm.full[s], kb * FK, f0);
@@ -783,7 +787,7 @@ size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 }  // namespace
 
 ttt_status gated_ffn(const void* X, const void* Wg, const void* Wu, int64_t T, int d, int f, int act, void* Z, void* G, void* U,
-                     int32_t* status, int num_sms, cudaStream_t s) {
+                     const DevStatus& status, int num_sms, cudaStream_t s) {
   const __nv_bfloat16 *x = static_cast<const __nv_bfloat16*>(X), *wg = static_cast<const __nv_bfloat16*>(Wg),
                       *wu = static_cast<const __nv_bfloat16*>(Wu);
   __nv_bfloat16 *z = static_cast<__nv_bfloat16*>(Z), *g = static_cast<__nv_bfloat16*>(G), *u = static_cast<__nv_bfloat16*>(U);
@@ -810,7 +814,8 @@ ttt_status gated_ffn(const void* X, const void* Wg, const void* Wu, int64_t T, i
     a.z = z;
     a.g = g;
     a.u = u;
-    a.status = DevStatus{status, kWaitLimitNs};
+    a.status = status;
+    a.stall = op_stall(a.kblocks > 1);
     CUtensorMap tx, tg, tu;
     TTT_TRY(map_bf16(&tx, X, d, T, FK, a.cols));
     TTT_TRY(map_bf16(&tg, Wg, d, f, FK, a.rows));
@@ -840,7 +845,8 @@ ttt_status gated_ffn(const void* X, const void* Wg, const void* Wu, int64_t T, i
   a.z = z;
   a.g = g;
   a.u = u;
-  a.status = DevStatus{status, kWaitLimitNs};
+  a.status = status;
+  a.stall = op_stall(a.kblocks > 1);
   return launch_pair<FWD>(tx, tx, tg, tu, a, num_sms, s);
 }
 
@@ -852,8 +858,8 @@ size_t gated_ffn_backward_workspace(int64_t T, int d, int f, int num_sms) {
 }
 
 ttt_status gated_ffn_backward(const void* dZ, const void* X, const void* Wg, const void* Wu, const void* G, const void* U,
-                              int64_t T, int d, int f, int act, void* dX, void* dWg, void* dWu, void* ws, int32_t* status,
-                              int num_sms, cudaStream_t s) {
+                              int64_t T, int d, int f, int act, void* dX, void* dWg, void* dWu, void* ws,
+                              const DevStatus& status, int num_sms, cudaStream_t s) {
   const size_t n = (size_t)T * f;
   uint8_t* w = static_cast<uint8_t*>(ws);
   __nv_bfloat16* dg = reinterpret_cast<__nv_bfloat16*>(w);
@@ -868,7 +874,8 @@ ttt_status gated_ffn_backward(const void* dZ, const void* X, const void* Wg, con
     k_ffn_act_bwd<TTT_ACT_GELU><<<blocks, 256, 0, s>>>(z, g, u, dg, du, n);
   TTT_CUDA(cudaGetLastError());
   FfnArgs a = {};
-  a.status = DevStatus{status, kWaitLimitNs};
+  a.status = status;
+  a.stall = op_stall(dX != nullptr || (dWg != nullptr && T > FK));
   a.part = part;
   CUtensorMap A0, A1, B0, B1;
   if (dX != nullptr) {

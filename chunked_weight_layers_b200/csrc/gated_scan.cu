@@ -76,6 +76,7 @@ struct GsArgs {
   __nv_bfloat16* ckpt;                // state before every chunk, as two bf16 terms [pairs][nchunk][2][8 pieces][64 rows][8]
   float* dg;                          // dense [pairs][T]
   DevStatus status;
+  int stall;                          // a chunk of every segment that is never loaded (tests), or -1
 };
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -489,6 +490,7 @@ __global__ void __launch_bounds__(256, 2) k_gs_segment(const __grid_constant__ S
   const int c0 = seg * a.per_seg, c1 = min(a.nchunk, c0 + a.per_seg), n = c1 - c0;
   auto chunk_of = [&](int i) { return rev ? c1 - 1 - i : c0 + i; };
   auto load = [&](int i) {
+    if (!CKPT && i == a.stall) return;
     uint64_t* bar = &sm.full[i & 1];
     mbar_arrive_expect_tx(bar, 2 * kLTile);
     tma_load_tile(sm.X[i & 1], &tx.map, bar, chunk_of(i) * kL, hi_ * tx.head, bi * tx.batch);
@@ -656,6 +658,7 @@ __global__ void __launch_bounds__(256, 2)
     tma_load_tile(sm.K, &tk.map, &sm.qk, (c0 + i) * kL, hi_ * tk.head, bi * tk.batch);
   };
   auto load_v = [&](int i) {
+    if (i == a.stall) return;
     mbar_arrive_expect_tx(&sm.v[i & 1], kLTile);
     tma_load_tile(sm.V[i & 1], &tv.map, &sm.v[i & 1], (c0 + i) * kL, hi_ * tv.head, bi * tv.batch);
   };
@@ -972,6 +975,7 @@ __global__ void __launch_bounds__(512, 1) k_gs_bwd(const __grid_constant__ BwdTi
   const int c0 = seg * a.per_seg, c1 = min(a.nchunk, c0 + a.per_seg), n = c1 - c0;
   const __nv_bfloat16* states = a.ckpt + (size_t)pair * a.nchunk * 2 * kState;
   auto load = [&](int i) {
+    if (i == a.stall) return;
     const int t = (c1 - 1 - i) * kL;
     mbar_arrive_expect_tx(&sm.in, 4 * kLTile + 2 * kTile);
     tma_load_tile(sm.Q, &tm_.q.map, &sm.in, t, hi_ * tm_.q.head, bi * tm_.q.batch);
@@ -1473,14 +1477,16 @@ static ttt_status tiles_of(Tiles* t, const void* p, const ttt_strides& s, const 
 }
 
 ttt_status gated_scan(const ttt_gated_scan_desc* d, const void* q, const void* k, const void* v, const float* g,
-                      const float* S0, void* o, float* S_end, void* ws, int32_t* status, int num_sms, cudaStream_t s) {
+                      const float* S0, void* o, float* S_end, void* ws, const DevStatus& status, int num_sms,
+                      cudaStream_t s) {
   const int64_t pairs = (int64_t)d->batch * d->heads;
   const Plan p = plan_for(d, num_sms);
   GsArgs a = base_args(d, g);
   a.nchunk = p.nchunk;
   a.nseg = p.nseg;
   a.per_seg = p.per_seg;
-  a.status = DevStatus{status, kWaitLimitNs};
+  a.status = status;
+  a.stall = op_stall(p.per_seg > 1);
   a.start = S0;
   a.end = S_end;
   Tiles tq, tk, tv, to;
@@ -1512,14 +1518,16 @@ ttt_status gated_scan(const ttt_gated_scan_desc* d, const void* q, const void* k
 
 ttt_status gated_scan_backward(const ttt_gated_scan_desc* d, const void* dout, const void* q, const void* k,
                                const void* v, const float* g, const float* S0, const float* dS_end, void* dq, void* dk,
-                               void* dv, float* dg, float* dS0, void* ws, int32_t* status, int num_sms, cudaStream_t s) {
+                               void* dv, float* dg, float* dS0, void* ws, const DevStatus& status, int num_sms,
+                               cudaStream_t s) {
   const int64_t pairs = (int64_t)d->batch * d->heads;
   const Plan p = plan_for(d, num_sms);
   GsArgs a = base_args(d, g);
   a.nchunk = p.nchunk;
   a.nseg = p.nseg;
   a.per_seg = p.per_seg;
-  a.status = DevStatus{status, kWaitLimitNs};
+  a.status = status;
+  a.stall = op_stall(p.per_seg > 1);
   uint8_t* w = static_cast<uint8_t*>(ws);
   a.ckpt = reinterpret_cast<__nv_bfloat16*>(w);
   w += round256((size_t)pairs * p.nchunk * 2 * kState * 2);

@@ -8,6 +8,7 @@
 
 #include <string>
 
+#include "common.cuh"
 #include "ttt.h"
 
 namespace ttt {
@@ -233,6 +234,14 @@ int gate_rank(const ttt_config& c);
 
 // ---- operators around the scans (stateless; arguments checked by their C entry points) --------
 
+// Where a call's kernels report a wait that ran out: the caller's word, or without one the device's, which
+// ttt_operators_poll reads.
+ttt_status op_status(int32_t* callers, DevStatus* out);
+// Fault injection (TTT_OPT_INJECT_STALL): the tile or k-block that the call's kernels never load, counted
+// from 0 within each segment or CTA, or -1. A call with more than one of them (`can`) uses a pending injection
+// up.
+int op_stall(bool can);
+
 ttt_status qk_norm_rope(const ttt_qk_desc* d, const void* q, const void* k, const float* qw, const float* kw,
                         const int64_t* positions, const double* freqs, void* qo, void* ko, int num_sms, cudaStream_t s);
 ttt_status qk_norm_rope_backward(const ttt_qk_desc* d, const void* dqo, const void* dko, const void* q, const void* k,
@@ -241,20 +250,21 @@ ttt_status qk_norm_rope_backward(const ttt_qk_desc* d, const void* dqo, const vo
 size_t qk_norm_rope_workspace(const ttt_qk_desc* d, int num_sms);
 
 ttt_status gated_scan(const ttt_gated_scan_desc* d, const void* q, const void* k, const void* v, const float* g,
-                      const float* S0, void* o, float* S_end, void* ws, int32_t* status, int num_sms,
+                      const float* S0, void* o, float* S_end, void* ws, const DevStatus& status, int num_sms,
                       cudaStream_t s);
 ttt_status gated_scan_backward(const ttt_gated_scan_desc* d, const void* dout, const void* q, const void* k,
                                const void* v, const float* g, const float* S0, const float* dS_end, void* dq, void* dk,
-                               void* dv, float* dg, float* dS0, void* ws, int32_t* status, int num_sms, cudaStream_t s);
+                               void* dv, float* dg, float* dS0, void* ws, const DevStatus& status, int num_sms,
+                               cudaStream_t s);
 ttt_status gated_scan_step(const ttt_gated_scan_desc* d, const void* q, const void* k, const void* v, const float* g,
                            float* state, void* o, cudaStream_t s);
 size_t gated_scan_workspace(const ttt_gated_scan_desc* d, bool backward, int num_sms);
 
 ttt_status gated_ffn(const void* X, const void* Wg, const void* Wu, int64_t T, int d, int f, int act, void* Z, void* G, void* U,
-                     int32_t* status, int num_sms, cudaStream_t s);
+                     const DevStatus& status, int num_sms, cudaStream_t s);
 ttt_status gated_ffn_backward(const void* dZ, const void* X, const void* Wg, const void* Wu, const void* G, const void* U,
-                              int64_t T, int d, int f, int act, void* dX, void* dWg, void* dWu, void* ws, int32_t* status,
-                              int num_sms, cudaStream_t s);
+                              int64_t T, int d, int f, int act, void* dX, void* dWg, void* dWu, void* ws,
+                              const DevStatus& status, int num_sms, cudaStream_t s);
 size_t gated_ffn_backward_workspace(int64_t T, int d, int f, int num_sms);
 
 // Small utility kernels.

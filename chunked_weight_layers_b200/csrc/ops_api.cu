@@ -56,6 +56,27 @@ ttt_status need_device(int* sms) {
   return TTT_OK;
 }
 
+// Where kernels of calls without a status word of their own report: code and site, one pair a device.
+__device__ int g_op_status[2];
+std::atomic<int*> g_op_words[kMaxDevices];
+
+std::atomic<uint64_t> g_op_limit{kWaitLimitNs};
+std::atomic<int> g_op_inject{0};
+
+// The device's pair, of the current device (found once per device).
+ttt_status op_words(int** out) {
+  int dev = -1;
+  TTT_CUDA(cudaGetDevice(&dev));
+  if (dev < 0 || dev >= kMaxDevices) return fail(TTT_ERR_UNSUPPORTED, "device ordinal %d out of range", dev);
+  *out = g_op_words[dev].load(std::memory_order_acquire);
+  if (*out != nullptr) return TTT_OK;
+  void* p = nullptr;
+  TTT_CUDA(cudaGetSymbolAddress(&p, g_op_status));
+  *out = static_cast<int*>(p);
+  g_op_words[dev].store(*out, std::memory_order_release);
+  return TTT_OK;
+}
+
 ttt_status check_workspace(const void* ws, size_t have, size_t want) {
   if (want == 0) return TTT_OK;
   if (ws == nullptr || !aligned(ws, 256)) return fail(TTT_ERR_INVALID_ARG, "workspace must be a 256-byte aligned device pointer");
@@ -168,6 +189,17 @@ ttt_status check_status(const int32_t* status) {
 cudaStream_t cs(ttt_stream s) { return reinterpret_cast<cudaStream_t>(s); }
 
 }  // namespace
+
+ttt_status op_status(int32_t* callers, DevStatus* out) {
+  *out = DevStatus{callers, g_op_limit.load(std::memory_order_relaxed)};
+  if (callers == nullptr) {
+    TTT_TRY(op_words(&out->word));
+    out->site = out->word + 1;
+  }
+  return TTT_OK;
+}
+
+int op_stall(bool can) { return can && g_op_inject.load(std::memory_order_relaxed) != 0 && g_op_inject.exchange(0) != 0 ? 1 : -1; }
 
 }  // namespace ttt
 
@@ -316,7 +348,9 @@ extern "C" ttt_status ttt_gated_scan(const ttt_gated_scan_desc* d, const void* q
   TTT_TRY(need_device(&sms));
   TTT_TRY(check_workspace(ws, ws_bytes, gated_scan_workspace(d, false, sms)));
   if (status != nullptr) TTT_CUDA(cudaMemsetAsync(status, 0, sizeof(int32_t), cs(stream)));
-  return gated_scan(d, q, k, v, g, S0, o, S_end, ws, status, sms, cs(stream));
+  DevStatus report;
+  TTT_TRY(op_status(status, &report));
+  return gated_scan(d, q, k, v, g, S0, o, S_end, ws, report, sms, cs(stream));
 }
 
 extern "C" ttt_status ttt_gated_scan_backward(const ttt_gated_scan_desc* d, const void* d_o, const void* q, const void* k,
@@ -347,7 +381,9 @@ extern "C" ttt_status ttt_gated_scan_backward(const ttt_gated_scan_desc* d, cons
   TTT_TRY(need_device(&sms));
   TTT_TRY(check_workspace(ws, ws_bytes, gated_scan_workspace(d, true, sms)));
   if (status != nullptr) TTT_CUDA(cudaMemsetAsync(status, 0, sizeof(int32_t), cs(stream)));
-  return gated_scan_backward(d, d_o, q, k, v, g, S0, dS_end, dq, dk, dv, dg, dS0, ws, status, sms, cs(stream));
+  DevStatus report;
+  TTT_TRY(op_status(status, &report));
+  return gated_scan_backward(d, d_o, q, k, v, g, S0, dS_end, dq, dk, dv, dg, dS0, ws, report, sms, cs(stream));
 }
 
 extern "C" ttt_status ttt_gated_scan_step(const ttt_gated_scan_desc* d, const void* q, const void* k, const void* v,
@@ -382,7 +418,9 @@ extern "C" ttt_status ttt_gated_ffn(const void* X, const void* Wg, const void* W
   }
   if (status != nullptr) TTT_CUDA(cudaMemsetAsync(status, 0, sizeof(int32_t), cs(stream)));
   if (T == 0) return TTT_OK;
-  return gated_ffn(X, Wg, Wu, T, d, f, act, Z, G, U, status, sms, cs(stream));
+  DevStatus report;
+  TTT_TRY(op_status(status, &report));
+  return gated_ffn(X, Wg, Wu, T, d, f, act, Z, G, U, report, sms, cs(stream));
 }
 
 extern "C" size_t ttt_gated_ffn_backward_workspace(int64_t T, int32_t d, int32_t f) {
@@ -422,5 +460,35 @@ extern "C" ttt_status ttt_gated_ffn_backward(const void* dZ, const void* X, cons
     }
     return TTT_OK;
   }
-  return gated_ffn_backward(dZ, X, Wg, Wu, G, U, T, d, f, act, dX, dWg, dWu, ws, status, sms, cs(stream));
+  DevStatus report;
+  TTT_TRY(op_status(status, &report));
+  return gated_ffn_backward(dZ, X, Wg, Wu, G, U, T, d, f, act, dX, dWg, dWu, ws, report, sms, cs(stream));
+}
+
+extern "C" ttt_status ttt_operators_set_option(int32_t option, int64_t value) {
+  switch (option) {
+    case TTT_OPT_WAIT_LIMIT_NS:
+      if (value < 1000000 || value > 60000000000ll)
+        return fail(TTT_ERR_INVALID_ARG, "TTT_OPT_WAIT_LIMIT_NS of the operators must lie in [1e6, 6e10] (got %lld)", (long long)value);
+      g_op_limit.store((uint64_t)value);
+      return TTT_OK;
+    case TTT_OPT_INJECT_STALL:
+      if (value != 0 && value != 1) return fail(TTT_ERR_INVALID_ARG, "TTT_OPT_INJECT_STALL must be 0 or 1");
+      g_op_inject.store((int)value);
+      return TTT_OK;
+    default:
+      return fail(TTT_ERR_INVALID_ARG, "option %d is not one of the operators'", option);
+  }
+}
+
+extern "C" ttt_status ttt_operators_poll(void) {
+  int sms, *words;
+  TTT_TRY(need_device(&sms));
+  TTT_TRY(op_words(&words));
+  TTT_CUDA(cudaDeviceSynchronize());
+  int v[2] = {0, 0};
+  TTT_CUDA(cudaMemcpy(v, words, sizeof(v), cudaMemcpyDeviceToHost));
+  if (v[0] == 0) return TTT_OK;
+  TTT_CUDA(cudaMemset(words, 0, sizeof(v)));
+  return fail(TTT_ERR_TIMEOUT, "a bounded device-side wait ran out (mbarrier at shared offset 0x%x)", v[1] & 0xFFFF);
 }

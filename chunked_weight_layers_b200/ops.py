@@ -9,7 +9,9 @@ Tensors are checked before the call as in the rest of the package: element type,
 device, and strides (rows of the last dimension dense, so that views of a projection's output are
 taken as they lie). A tensor that fails raises ValueError and nothing is launched; what the library
 refuses raises TTTError. Outputs and workspaces that a call makes are allocated on the stream it
-runs on. Every call can be captured into a CUDA graph.
+runs on. Every call can be captured into a CUDA graph. A call whose bounded device-side waits ran out
+leaves its outputs incomplete: it says so in ``status`` where that is given, and otherwise through
+:func:`poll_operators`.
 """
 
 from __future__ import annotations
@@ -22,7 +24,7 @@ import torch
 from . import abi
 from .abi import check
 
-__all__ = ["qk_norm_rope", "qk_norm_rope_backward", "rope_frequencies", "gated_scan", "gated_scan_backward",
+__all__ = ["poll_operators", "qk_norm_rope", "qk_norm_rope_backward", "rope_frequencies", "gated_scan", "gated_scan_backward",
            "gated_scan_step", "gated_ffn", "gated_ffn_backward"]
 
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
@@ -122,6 +124,12 @@ def _ptr(t):
 def _like(t):
     """A new dense tensor of t's shape and type."""
     return torch.empty_like(t, memory_format=torch.contiguous_format)
+
+
+def poll_operators():
+    """ttt_operators_poll: synchronises the device and raises TTTError if a bounded wait ran out, since the
+    last poll, in a call on it that was given no ``status``."""
+    check(abi.load().ttt_operators_poll())
 
 
 # ---- queries and keys ---------------------------------------------------------------------
@@ -420,7 +428,7 @@ def gated_ffn(x, w_gate, w_up, *, activation="silu", save=False, out=None, statu
     ``w_gate`` and ``w_up`` bf16 [f, d], contiguous; ``activation`` "silu" or "gelu". Returns z [tokens,
     f], or with ``save`` (z, gate, up) with the pre-activations that :func:`gated_ffn_backward` takes.
     ``status`` (int32 device tensor of one element, optional) is set to 0, or to TTT_ERR_TIMEOUT if
-    a bounded device-side wait ran out."""
+    a bounded device-side wait ran out (without it :func:`poll_operators` tells)."""
     dev = _current_device()
     raw, ctx = _place(stream, dev)
     try:

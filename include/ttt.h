@@ -41,7 +41,7 @@
  *    the row-major layout stated for it. The caller owns all such buffers; the library
  *    never frees or retains them beyond the call.
  *  - All work is enqueued on `stream` (a cudaStream_t; NULL is the legacy default
- *    stream). Calls that synchronise: ttt_state_poll(), ttt_chunk_scan_host(),
+ *    stream). Calls that synchronise: ttt_state_poll(), ttt_operators_poll(), ttt_chunk_scan_host(),
  *    ttt_chunk_scan_docs() (it uploads the document layout from host memory) and
  *    ttt_state_destroy() always; ttt_state_create(), the first ttt_chunk_scan() of an
  *    In-Place BF16 state (it builds and uploads its tile schedules) and a scan that must
@@ -427,9 +427,25 @@ ttt_status ttt_state_destroy(ttt_state* st);
  *    the bytes that its *_workspace function returns for the same arguments on the same device
  *    (0: may be NULL). Two calls whose GPU work may overlap need two workspaces. Its contents do
  *    not matter before a call and mean nothing after it.
+ *  - A bounded device-side wait that runs out leaves the outputs incomplete. A call given a
+ *    `status` word reports it there (see the declarations); the kernels of a call without one
+ *    record it on the device, for ttt_operators_poll().
  * They allocate nothing, so they can be captured into a CUDA graph from the first call on. Unless
  * a declaration says otherwise, outputs may not overlap inputs or one another. Every row of a call
  * is read: padding must hold finite numbers, since 0 · NaN is NaN. */
+
+/* Synchronise the device and return TTT_ERR_TIMEOUT if a wait ran out, since the last poll, in a call
+ * on the current device that was given no status word; TTT_OK otherwise. Clears the record. Not
+ * while a stream of the process is being captured. Errors: CUDA. */
+ttt_status ttt_operators_poll(void);
+
+/* Options of the calls below, for the whole process, from the next call on (a captured call keeps
+ * those it was captured with): TTT_OPT_WAIT_LIMIT_NS, the limit of every spin-wait, [1e6, 60e9], default
+ * 2e9; and for tests TTT_OPT_INJECT_STALL = 1, which makes the next call that can (a gated scan or its
+ * gradients with segments of more than 128 tokens, a feed-forward block of more than 16 tokens and
+ * d > 64, or its gradients) never load its second tile, so that a wait runs out. 0 cancels a pending
+ * injection. Errors: INVALID_ARG. */
+ttt_status ttt_operators_set_option(int32_t option, int64_t value);
 
 typedef struct {
   int64_t batch, head, token; /* elements between neighbours in that dimension */

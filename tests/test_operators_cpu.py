@@ -151,3 +151,11 @@ def test_binding_refuses_host_tensors():
             cwl.gated_scan(q, q, q, torch.zeros((1, 1, 2)))
         with pytest.raises(Exception):
             cwl.gated_ffn(q[0, 0], q[0, 0], q[0, 0])
+
+
+def test_operator_options(lib, abi):
+    call = lib.ttt_operators_set_option
+    for option, bad in ((abi.TTT_OPT_WAIT_LIMIT_NS, 999_999), (abi.TTT_OPT_WAIT_LIMIT_NS, 60_000_000_001),
+                        (abi.TTT_OPT_INJECT_STALL, 2), (abi.TTT_OPT_SM_PAIR, 0), (0, 0)):
+        assert call(option, bad) == abi.TTT_ERR_INVALID_ARG
+    assert call(abi.TTT_OPT_WAIT_LIMIT_NS, 2_000_000_000) == 0 and call(abi.TTT_OPT_INJECT_STALL, 0) == 0
