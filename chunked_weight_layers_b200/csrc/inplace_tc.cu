@@ -55,6 +55,8 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "tc_common.cuh"
+#include "tc_pair.cuh"
 
 namespace ttt {
 
@@ -146,123 +148,47 @@ struct TCArgs {
   int* tgt_done;
 };
 
-// ---- tcgen05 wrappers -----------------------------------------------------------------
+// ---- one CTA or an SM pair ---------------------------------------------------------------
 
-__device__ __forceinline__ uint64_t umma_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-  uint64_t d = 0;
-  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
-  d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
-  d |= (uint64_t)((sbo >> 4) & 0x3FFFu) << 32;
-  d |= (uint64_t)1 << 46;  // descriptor version for tcgen05
-  d |= (uint64_t)2 << 61;  // 128-byte swizzle
-  return d;
-}
-
-// kind::f16 instruction descriptor: D fp32, A and B bf16, M = m, N = 256.
-__host__ __device__ constexpr uint32_t idesc_bf16(int m, int a_mn, int b_mn) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) |
-         ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
-}
+// kind::f16 instruction descriptor: M = m, N = 256.
+__host__ __device__ constexpr uint32_t idesc_bf16(int m, int a_mn, int b_mn) { return tc::idesc_bf16(m, BN, a_mn, b_mn); }
 
 // PAIR: issued by the first CTA of an SM pair for both (cta_group::2); A and B are read from
 // the same shared-memory offsets in both CTAs and D lands in both CTAs' TMEM.
 template <bool PAIR>
 __device__ __forceinline__ void umma(uint32_t tmem_d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-  if constexpr (PAIR) {
-    asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(tmem_d),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-        : "memory");
-  } else {
-    asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(tmem_d),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-        : "memory");
-  }
+  if constexpr (PAIR)
+    pair::mma(tmem_d, a, b, idesc, accumulate);
+  else
+    tc::mma(tmem_d, a, b, idesc, accumulate);
 }
 
 // The mbarrier at this offset arrives once the MMAs issued before have completed; PAIR: the
-// arrival goes to the barrier at the same offset in both CTAs of the pair (CTA mask 0b11).
+// arrival goes to the barrier at the same offset in both CTAs of the pair.
 template <bool PAIR>
 __device__ __forceinline__ void umma_commit(uint64_t* bar) {
-  if constexpr (PAIR) {
-    asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-            smem_u32(bar)),
-        "h"((uint16_t)3)
-        : "memory");
-  } else {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-                 : "memory");
-  }
+  if constexpr (PAIR)
+    pair::commit(bar);
+  else
+    tc::commit(bar);
 }
 
 // TMEM allocation by one warp; PAIR: by one warp in each CTA of the pair, same columns in both.
 template <bool PAIR>
 __device__ __forceinline__ void tmem_alloc(uint32_t* dst, uint32_t cols) {
-  if constexpr (PAIR) {
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "r"(cols));
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
-  } else {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "r"(cols));
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
-  }
+  if constexpr (PAIR)
+    pair::alloc(dst, cols);
+  else
+    tc::alloc(dst, cols);
 }
 
 template <bool PAIR>
 __device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t cols) {
   if constexpr (PAIR)
-    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(cols));
+    pair::dealloc(taddr, cols);
   else
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(cols));
+    tc::dealloc(taddr, cols);
 }
-
-// ---- thread-block clusters (SM pairs) ----------------------------------------------------
-
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-
-// Every thread of both CTAs; what each wrote before is visible to the other after it.
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-// Address of this CTA's shared-memory object `p` in the first CTA of the cluster.
-__device__ __forceinline__ uint32_t in_first_cta(const void* p) {
-  uint32_t a;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem_u32(p)));
-  return a;
-}
-
-// Arrive on the mbarrier at shared::cluster address `addr` (in the other CTA of the pair),
-// relaxed: it orders nothing before it. It signals that this thread's tcgen05.ld reads of TMEM
-// have finished (tcgen05.wait::ld before it), not writes made visible by it. A release at
-// cluster scope would wait for every memory operation the thread has in flight (its output
-// stores): measured on B200, a release arrive took ~1400 cycles.
-__device__ __forceinline__ void mbar_arrive_remote(uint32_t addr) {
-  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
-}
-
-__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr));
-}
-
-__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ int kblocks(int type, const TCArgs& a) {
   if (type == APPLY) return (a.f + BK - 1) / BK;
@@ -298,11 +224,7 @@ __device__ __forceinline__ const CUtensorMap* pick3(const CUtensorMap& a, const 
 template <bool PAIR>
 __device__ __forceinline__ void tma_load_2d_to(void* dst, const CUtensorMap* map, uint32_t bar, int32_t c0, int32_t c1) {
   if constexpr (PAIR) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1)
-        : "memory");
+    pair::load_2d(dst, map, bar, c0, c1);
   } else {
     asm volatile(
         "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
@@ -367,7 +289,7 @@ __global__ void __launch_bounds__(kThreadsTC, 1)
   extern __shared__ uint8_t smem_raw[];
   TCSmem& sm = *reinterpret_cast<TCSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = PAIR ? (int)cluster_rank() : 0;  // 0: the CTA that issues the MMAs
+  const int rank = PAIR ? (int)pair::rank() : 0;  // 0: the CTA that issues the MMAs
   const int nlists = PAIR ? (int)gridDim.x / 2 : (int)gridDim.x;
   const int list_id = PAIR ? (int)blockIdx.x / 2 : (int)blockIdx.x;
   // In round r the CTA (pair) runs tile list (list_id + r·rotate) mod nlists: over the rounds
@@ -419,10 +341,10 @@ __global__ void __launch_bounds__(kThreadsTC, 1)
     fence_barrier_init();
   }
   if (warp == 1) tmem_alloc<PAIR>(&sm.tmem_base, kTmemCols);
-  tc_fence_before();
+  tc::fence_before();
   __syncthreads();
-  if constexpr (PAIR) cluster_sync();  // both CTAs' barriers exist before either arrives remotely
-  tc_fence_after();
+  if constexpr (PAIR) pair::sync();  // both CTAs' barriers exist before either arrives remotely
+  tc::fence_after();
   const uint32_t tmem = sm.tmem_base;
   volatile int* abort = &sm.abort;
 
@@ -461,7 +383,7 @@ __global__ void __launch_bounds__(kThreadsTC, 1)
           // the bytes of both (a load may complete before the expectation is posted: the phase
           // cannot end before it is).
           if (rank == 0) mbar_arrive_expect_tx(&sm.full[s], PAIR ? 2 * kStage : kStage);
-          const uint32_t fb = PAIR ? in_first_cta(&sm.full[s]) : smem_u32(&sm.full[s]);
+          const uint32_t fb = PAIR ? pair::in_first(&sm.full[s]) : smem_u32(&sm.full[s]);
           if (type == APPLY) {
             tma_load_2d_to<PAIR>(sa, &tmZk, fb, kb * BK, chunk * args.C + r0);
             tma_load_2d_to<PAIR>(sb, wk, fb, kb * BK, b0);
@@ -578,7 +500,7 @@ __global__ void __launch_bounds__(kThreadsTC, 1)
           ok = false;
           return false;
         }
-        tc_fence_after();
+        tc::fence_after();
         const uint32_t d_tmem = tmem + (uint32_t)(acc * BN);
         constexpr int kM = PAIR ? kTileP : BM;
         const uint32_t idesc = type == APPLY    ? idesc_bf16(kM, 0, 0)
@@ -590,17 +512,17 @@ __global__ void __launch_bounds__(kThreadsTC, 1)
             ok = false;
             break;
           }
-          tc_fence_after();
+          tc::fence_after();
           const uint32_t a0 = smem_u32(sm.ring + s * kStage), b0 = a0 + kABytes;
 #pragma unroll
           for (int kk = 0; kk < BK / 16; ++kk) {
             uint64_t ad, bd;
             if (type == UPDATE) {
-              ad = umma_desc(a0 + kk * 2048, 8192, 1024);
-              bd = umma_desc(b0 + kk * 2048, 8192, 1024);
+              ad = tc::smem_desc(a0 + kk * 2048, 8192, 1024);
+              bd = tc::smem_desc(b0 + kk * 2048, 8192, 1024);
             } else {
-              ad = umma_desc(a0 + kk * 32, 16, 1024);
-              bd = type == APPLY ? umma_desc(b0 + kk * 32, 16, 1024) : umma_desc(b0 + kk * 2048, 8192, 1024);
+              ad = tc::smem_desc(a0 + kk * 32, 16, 1024);
+              bd = type == APPLY ? tc::smem_desc(b0 + kk * 32, 16, 1024) : tc::smem_desc(b0 + kk * 2048, 8192, 1024);
             }
             umma<PAIR>(d_tmem, ad, bd, idesc, (kb | kk) != 0);
           }
@@ -641,7 +563,7 @@ __global__ void __launch_bounds__(kThreadsTC, 1)
       if (!ok && lane == 0) sm.tflag[half][tcount & 1] = 1;
       named_sync_half(half);
       if (*reinterpret_cast<volatile int*>(&sm.tflag[half][tcount & 1])) return false;
-      tc_fence_after();
+      tc::fence_after();
       // The accumulator is complete, so every operand of this tile has been read: an APPLY
       // tile no longer needs its buffer of the bf16 copy of W.
       if (type == APPLY && args.app_done != nullptr && warp == 2 && lane == 0) {
@@ -660,8 +582,8 @@ __global__ void __launch_bounds__(kThreadsTC, 1)
           okw = __all_sync(0xffffffffu, okw);
           if (okw) {
             uint32_t r[32];
-            tmem_ld32(tbase + j * kWCols, r);
-            tmem_wait_ld();
+            tc::ld32(tbase + j * kWCols, r);
+            tc::wait_ld();
             uint8_t* wrow = sm.Wr[slot] + row_in_tile * 128;
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
@@ -722,8 +644,8 @@ __global__ void __launch_bounds__(kThreadsTC, 1)
         for (int jc = 0; jc < 4; ++jc) {
           const int col0 = n * BN + half * 128 + jc * 32;
           uint32_t r[32];
-          tmem_ld32(tbase + jc * 32, r);
-          tmem_wait_ld();
+          tc::ld32(tbase + jc * 32, r);
+          tc::wait_ld();
           float v[32];
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
@@ -741,11 +663,11 @@ __global__ void __launch_bounds__(kThreadsTC, 1)
           }
         }
       }
-      tc_fence_before();
+      tc::fence_before();
       __syncwarp();
       if (lane == 0) {
         if (PAIR && rank != 0)
-          mbar_arrive_remote(in_first_cta(&sm.tempty[acc]));
+          pair::arrive(pair::in_first(&sm.tempty[acc]));
         else
           mbar_arrive(&sm.tempty[acc]);
       }
@@ -755,12 +677,12 @@ __global__ void __launch_bounds__(kThreadsTC, 1)
     if (leader) bulk_wait<0>();
   }
 
-  tc_fence_before();
+  tc::fence_before();
   __syncthreads();
   // PAIR: neither CTA exits (or frees TMEM) while the other may still arrive on its barriers
   // or the MMAs may still write its TMEM.
-  if constexpr (PAIR) cluster_sync();
-  tc_fence_after();
+  if constexpr (PAIR) pair::sync();
+  tc::fence_after();
   if (warp == 1) tmem_dealloc<PAIR>(tmem, kTmemCols);
   if (args.ring != nullptr && threadIdx.x == 0) {
     // This CTA read ring[0] before its first barrier.
