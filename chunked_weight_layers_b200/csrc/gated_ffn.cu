@@ -774,10 +774,12 @@ ttt_status launch_pair(const CUtensorMap& A0, const CUtensorMap& A1, const CUten
   cfg.attrs = &at;
   cfg.numAttrs = 1;
   TTT_CUDA(cudaLaunchKernelEx(&cfg, k_ffn_pair<MODE>, A0, A1, B0, B1, a));
-  const int rest = a.tiles_m * a.tiles_n - a.whole;
-  if (MODE != FWD && rest > 0) {
-    k_ffn_join<MODE><<<dim3(kTileM / 8, rest), 256, 0, s>>>(a);
-    TTT_CUDA(cudaGetLastError());
+  if constexpr (MODE != FWD) {
+    const int rest = a.tiles_m * a.tiles_n - a.whole;
+    if (rest > 0) {
+      k_ffn_join<MODE><<<dim3(kTileM / 8, rest), 256, 0, s>>>(a);
+      TTT_CUDA(cudaGetLastError());
+    }
   }
   return TTT_OK;
 }
