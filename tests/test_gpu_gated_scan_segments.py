@@ -38,7 +38,7 @@ def test_around_chunks_and_blocks(cwl, T, initial):
 
 @pytest.mark.parametrize("H,T,documents", [(2, 6000, True), (1, 6000, False), (1, 88 * 128, False), (1, 88 * 128 - 37, True)])
 def test_many_segments(cwl, H, T, documents):
-    """Ten segments of five chunks and a shorter one, and 22 of four."""
+    """Ten segments of five chunks (the last of two), and 22 of four."""
     x = base._inputs(1, H, T, 7 * T + H)
     r = torch.Generator().manual_seed(T)
     x["g"] = -2e-3 * torch.rand((1, H, T), generator=r)
