@@ -470,18 +470,26 @@ int lanes_of(int width) { return width <= 64 ? 8 : width <= 128 ? 16 : 32; }
 
 int64_t groups_per_block(int width) { return kThreadsQK / lanes_of(width); }
 
+// Resident CTAs of the backward kernel (its registers allow two).
+constexpr int kBwdCtasPerSm = 2;
+
 // Parts of a token's heads: one, unless the tokens alone give the GPU fewer than 512 threads an SM.
-// Backward, two where there are 16 heads or more: its CTAs walk over several items each, and
-// smaller ones end closer together (4 x 8192 tokens of 32 heads: 83 us against 89; three: 102, as
-// the parts no longer end where the queries do, four: 90).
+// Backward, where CTAs walk over several items each, two parts of six heads or more if that saves half a
+// round out of five or fewer: 4 x 8192 tokens (four rounds, or seven of half the size) of 12, 16, 24, 32 and 48
+// heads of 64 take 46.6, 49.6, 67.0, 83.2 and 122.6 us in two, 48.9, 51.9, 71.1, 89.4 and 128.7 in one, 10000 of
+// 32 heads 37.0 against 43.3, 21000 of 24 heads of 128 (five rounds) 85.7 against 89.3. Two are slower over more
+// rounds (60000 tokens, seven: 16 heads of 64 83.8 against 81.1; 146000, 16: 193 against 186), with as many
+// (2 x 4096 tokens of 16 heads of 128: 31.5 against 30.3) and with few heads (30000 tokens of 8 of 128: 54.7
+// against 50.5).
 int splits_of(const ttt_qk_desc* d, bool back, int num_sms) {
   const int64_t rows = (int64_t)d->batch * d->tokens, heads = (int64_t)d->q_heads + d->k_heads;
   const int64_t want = (int64_t)num_sms * 512 / lanes_of(d->width);
-  return (int)std::max<int64_t>(back && heads >= 16 ? 2 : 1, std::min(heads, want / std::max<int64_t>(1, rows)));
+  const int64_t splits = std::max<int64_t>(1, std::min(heads, want / std::max<int64_t>(1, rows)));
+  if (!back || splits > 1 || heads < 12) return (int)splits;
+  const int64_t round = groups_per_block(d->width) * num_sms * kBwdCtasPerSm;
+  const int64_t one = (rows + round - 1) / round, two = (2 * rows + round - 1) / round;
+  return one <= 5 && two < 2 * one ? 2 : 1;
 }
-
-// Resident CTAs of the backward kernel (its registers allow two).
-constexpr int kBwdCtasPerSm = 2;
 
 int64_t bwd_blocks(int64_t items, int width, int num_sms) {
   const int64_t g = groups_per_block(width);
