@@ -6,9 +6,11 @@ gate (:func:`gated_scan_step` its one-token form); :func:`gated_ffn` makes the k
 scan. Each has its gradients in a call of its own (``*_backward``).
 
 Tensors are checked before the call as in the rest of the package: element type, shape, the current
-device, and strides (rows of the last dimension dense, so that views of a projection's output are
-taken as they lie). A tensor that fails raises ValueError and nothing is launched; what the library
-refuses raises TTTError. Outputs and workspaces that a call makes are allocated on the stream it
+device, and strides. Rows of the last dimension are dense and start on 16-byte boundaries; the other
+dimensions may lie in any order, so that views of a projection's output are taken as they are. An input
+may repeat rows along a dimension (stride 0, as expand() makes), an output may not; tokens of a gated
+scan have rows of their own. A tensor that fails raises ValueError and nothing is launched; what the
+library refuses (alignment, strides, sizes out of its range) raises TTTError. Outputs and workspaces that a call makes are allocated on the stream it
 runs on. Every call can be captured into a CUDA graph. A call whose bounded device-side waits ran out
 leaves its outputs incomplete: it says so in ``status`` where that is given, and otherwise through
 :func:`poll_operators`.
@@ -194,8 +196,8 @@ def qk_norm_rope(q, k, *, positions=None, freqs=None, magnitude=1.0, norm="rms",
                  q_weight=None, k_weight=None, position0=0, out=None, stream=None):
     """ttt_qk_norm_rope: the norm ("rms", "l2" or "none") of each query and key head and its rotary
     position in one pass. ``q`` [batch, q_heads, tokens, width] and ``k`` [batch, k_heads, tokens,
-    width], bf16 or fp32, any strides with a dense last dimension (a transposed view of a
-    token-major projection, say); one of them may be None. ``positions`` int64 [tokens] or [batch,
+    width], bf16 or fp32, rows as the module says (a transposed view of a token-major projection, say); one of
+    them may be None, and an empty batch or no tokens is a no-op. ``positions`` int64 [tokens] or [batch,
     tokens] (default: ``position0`` + t); ``freqs`` and ``magnitude`` from :func:`rope_frequencies`
     (None: no rotation); the first 2·len(freqs) values of each row are rotated, in pairs by
     ``layout`` "half" or "interleaved". ``q_weight``, ``k_weight`` fp32 [width] (RMS). Returns (q, k),
@@ -302,8 +304,9 @@ def _scan_desc(shape, scale, q, k, v, o, g):
 
 def gated_scan(q, k, v, g, *, scale=1.0, initial=None, out=None, final=None, status=None, stream=None):
     """ttt_gated_scan: S_t = e^{g_t}·S_{t-1} + k_tᵀ·v_t, o_t = scale·q_t·S_t per (sequence, head). ``q``,
-    ``k``, ``v`` bf16 [batch, heads, tokens, 64] (any strides, dense rows), ``g`` fp32 [batch, heads,
-    tokens] (any strides; natural logarithms, -inf forgets everything before its token). All tokens
+    ``k``, ``v`` bf16 [batch, heads, tokens, 64] (rows as the module says; at least one sequence and head, tokens
+    may be 0), ``g`` fp32 [batch, heads, tokens] (any strides; natural logarithms, -inf forgets everything
+    before its token). All tokens
     must hold finite numbers, padding too (0 · NaN is NaN). Returns
     (o, state): o in ``out`` or a new dense tensor; the state after the last token, fp32 [batch,
     heads, 64, 64], in ``final`` (which may be ``initial``) or a new tensor. ``status`` as for
@@ -379,8 +382,8 @@ def gated_scan_backward(do, q, k, v, g, *, scale=1.0, initial=None, dfinal=None,
 
 def gated_scan_step(state, q, k, v, g, *, scale=1.0, out=None, stream=None):
     """ttt_gated_scan_step: one token of every sequence. ``state`` fp32 [batch, heads, 64, 64] is updated
-    in place; ``q``, ``k``, ``v`` bf16 [batch, heads, 64], ``g`` fp32 [batch, heads] (any strides, dense
-    rows). Returns o, bf16 [batch, heads, 64]."""
+    in place; ``q``, ``k``, ``v`` bf16 [batch, heads, 64] (rows as the module says), ``g`` fp32 [batch, heads] (any
+    strides). Returns o, bf16 [batch, heads, 64]."""
     dev = _current_device()
     raw, ctx = _place(stream, dev)
     scale = float(scale)  # a plain number: the key must not hold a tensor, whose value may change

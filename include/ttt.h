@@ -524,8 +524,8 @@ ttt_status ttt_rope_frequencies(int32_t rot, double base, int32_t scaling, doubl
 
 /* One gated scan: [batch, heads, tokens, 64] bf16 rows and [batch, heads, tokens] fp32 gates. */
 typedef struct {
-  int32_t batch, heads;
-  int64_t tokens;
+  int32_t batch, heads;      /* at least 1 each */
+  int64_t tokens;            /* 0 or more */
   float scale;               /* factor on the outputs, e.g. 1/√64 */
   ttt_strides q, k, v;       /* of rows; token strides not 0 (batch and head strides may be) */
   ttt_strides o;             /* the outputs; backward: their gradients */
