@@ -19,10 +19,10 @@
 //
 // Precision. The products run on the tensor cores (tcgen05) with bf16 operands and fp32 sums. S and
 // dS stay in fp32 registers. Where a product's result is a bf16 output, one factor is rounded to bf16
-// (P, A, or the copy of S); where it feeds a fp32 output (the states and dg), the rounded factor is
-// kept as a sum of two bf16 numbers (2^-17 of its size; the states come out within 3e-6, dg within
-// 5e-6 in two norms), at the price of a second product (a third term would cost half as much
-// again). The gates are summed in base-2 units; one below -150 (its factor is 0 in
+// (P, A, or the copy of S); where it feeds a fp32 output (the states and dg), the factor is kept as a sum of
+// three bf16 numbers, which is all of its fp32 value, at the price of as many products: the states come out
+// within 3e-7 and dg within 6e-7 in two norms (1.1e-6 for gates of -30), about as from products in fp32 (with two
+// numbers 2.5e-6 and 5e-6, and 5 to 7 % less time). The gates are summed in base-2 units; one below -150 (its factor is 0 in
 // fp32, as for -inf, which starts a new document) counts as -150, so that differences of sums stay
 // finite.
 //
@@ -30,14 +30,14 @@
 // segments: the states that the segments add are found first (k_gs_segment), combined in order, and
 // then every segment runs from its own start.
 //
-// What bounds it (B200, 8 x 12 heads x 2048 tokens and 4 x 16 x 8192). Forward: a chunk's chain (scores,
-// their weights, P·V, outputs; 5200 cycles for a CTA alone on its SM, 5700 for each of two, whose TMEM leaves
-// no room for a third), at two thirds of the rate at which HBM could deliver its 64 KB; the pass over K and V
-// for the segments' starts and the launches' first and last microseconds come on top (41 us, where the bytes
-// need 16). Backward: shared memory, through which a chunk's operands and
-// results pass (some 650 KB, and the products' operands once more, come to 8500 cycles): 10500 cycles a
-// chunk (210 us of 305, where the bytes need 74), the state passes the rest. The state before every chunk
-// is kept in pieces of eight columns, all rows of a piece after each other: a warp then writes whole
+// What bounds it (B200, 8 x 12 heads x 2048 tokens and 4 x 16 x 8192). Latency: no unit is near its limit (the
+// tensor pipe 17 %, HBM 32 %, instruction issue 28 % of the time). Forward: a chunk's chain of scores, their weights,
+// P·V and outputs takes 6300 cycles in a CTA alone on its SM and 9500 in each of two, whose TMEM leaves no room for
+// a third; the pass over K and V for the segments' starts and the launches' first and last microseconds come
+// on top (45 us, where the bytes need 16). Backward: one CTA an SM, whose chunk (12 400 cycles alone, 14 400
+// with all SMs at work) passes through one set of tiles in shared memory: the next chunk's come when its last
+// product has read them. 215 us of 318, where the bytes need 74; the state passes take the rest. The state before
+// every chunk is kept in pieces of eight columns, all rows of a piece after each other: a warp then writes whole
 // sectors, where rows of 128 bytes took 15 us more.
 #include <algorithm>
 
@@ -73,7 +73,7 @@ struct GsArgs {
   int few;                            // start holds one state a pair: the CTAs add the segments' on their own
   float* local[2];                    // what each segment adds [pairs][nseg][64][64], forward and in reverse
   float* seg_decay[2];                // sums of the segments' gates, base-2 units [pairs][nseg]
-  __nv_bfloat16* ckpt;                // state before every chunk, as two bf16 terms [pairs][nchunk][2][8 pieces][64 rows][8]
+  __nv_bfloat16* ckpt;                // state before every chunk, as three bf16 terms [pairs][nchunk][3][8 pieces][64 rows][8]
   float* dg;                          // dense [pairs][T]
   DevStatus status;
   int stall;                          // a chunk of every segment that is never loaded (tests), or -1
@@ -148,11 +148,14 @@ __device__ __forceinline__ void fetch_gates(const GsArgs& a, const float* gp, in
   wm::cp_commit();
 }
 
-// From the raw gates of the last fetch_gates of this warp. Sum: float makes no lo, for decays from or to the
+// From the raw gates of the last fetch_gates of this warp, or of the one before (another). Sum: float makes no lo, for decays from or to the
 // chunk's ends alone (64 bits cost k_gs_segment 1 us of 16).
 template <class Sum>
-__device__ __forceinline__ void make_gates(const float* raw, Gates& s, int lane) {
-  wm::cp_wait<0>();
+__device__ __forceinline__ void make_gates(const float* raw, Gates& s, int lane, bool another = false) {
+  if (another)
+    wm::cp_wait<1>();
+  else
+    wm::cp_wait<0>();
   __syncwarp();
   const float4 r = *reinterpret_cast<const float4*>(raw + 4 * lane);
   float x[4] = {r.x, r.y, r.z, r.w};
@@ -206,39 +209,32 @@ __device__ __forceinline__ void make_gates(const float* raw, Gates& s, int lane)
   __syncwarp();  // the raw gates have been read
 }
 
-// x ⊙ w (two values) as two bf16 terms: the product rounded, and what the rounding left.
-__device__ __forceinline__ void weigh(uint32_t x, F2 w, uint32_t& hi, uint32_t& lo) {
-  const F2 p = mul(from_bf16(x), w);
-  hi = to_bf16(p);
-  lo = to_bf16(fma2(from_bf16(hi), f2(-1.f, -1.f), p));
+// Two fp32 values as three bf16 terms: each the rounded rest of those before.
+__device__ __forceinline__ void terms_of(F2 p, uint32_t& a, uint32_t& b, uint32_t& c) {
+  const F2 minus = f2(-1.f, -1.f);
+  a = to_bf16(p);
+  p = fma2(from_bf16(a), minus, p);
+  b = to_bf16(p);
+  c = to_bf16(fma2(from_bf16(b), minus, p));
 }
 
-// Token t's row of X (a [128][64] tile), weighted by w, as two bf16 terms into the rows of hi and lo.
-__device__ __forceinline__ void weigh_row(const uint8_t* X, uint8_t* hi, uint8_t* lo, int t, float w) {
-  const F2 ww = f2(w, w);
-#pragma unroll
-  for (int c = 0; c < 8; ++c) {
-    const uint32_t at = t * 128 + ((c ^ (t & 7)) << 4);
-    const uint4 x = *reinterpret_cast<const uint4*>(X + at);
-    uint4 h, l;
-    weigh(x.x, ww, h.x, l.x);
-    weigh(x.y, ww, h.y, l.y);
-    weigh(x.z, ww, h.z, l.z);
-    weigh(x.w, ww, h.w, l.w);
-    *reinterpret_cast<uint4*>(hi + at) = h;
-    *reinterpret_cast<uint4*>(lo + at) = l;
-  }
+// A 16-byte piece of a row, weighted, as three bf16 terms.
+__device__ __forceinline__ void weigh(const uint4& x, F2 w, uint4 (&t)[3]) {
+  terms_of(mul(from_bf16(x.x), w), t[0].x, t[1].x, t[2].x);
+  terms_of(mul(from_bf16(x.y), w), t[0].y, t[1].y, t[2].y);
+  terms_of(mul(from_bf16(x.z), w), t[0].z, t[1].z, t[2].z);
+  terms_of(mul(from_bf16(x.w), w), t[0].w, t[1].w, t[2].w);
 }
 
 using tc::desc_at;
 using tc::desc_of;
 
-// [XW_hi | XW_lo]ᵀ·Y over 128 tokens into 64 TMEM columns: rows 0 .. 63 the first term's sums, 64 .. 127
-// the second's. Both operands MN-major (xw with the distance of the two terms' tiles).
-__device__ __forceinline__ void outer_mma(uint32_t tmem_d, uint32_t xw, uint32_t y) {
+// XWᵀ·Y over 128 tokens into 64 TMEM columns, XW one of three terms (a tile); the least come first. Both
+// operands MN-major. The 64 rows lie in the first 16 lanes of each warp's 32.
+__device__ __forceinline__ void outer_mma(uint32_t tmem_d, uint32_t x, uint32_t y, bool first) {
 #pragma unroll
   for (int kk = 0; kk < kL / 16; ++kk)
-    tc::mma(tmem_d, desc_at(xw, kk * 2048), desc_at(y, kk * 2048), tc::idesc_bf16(128, 64, 1, 1), kk != 0);
+    tc::mma(tmem_d, desc_at(x, kk * 2048), desc_at(y, kk * 2048), tc::idesc_bf16(64, 64, 1, 1), !first || kk != 0);
 }
 
 // Of two bf16 values at columns 0 and 1: both where the row is 1 or more, the first where it is 0, none
@@ -257,72 +253,54 @@ __device__ __forceinline__ void cta_sync() {
 
 __device__ __forceinline__ void group_sync(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
 
-// The state's update from the sums that outer_mma left in TMEM, by a group of four warps: the lanes of
-// the second term hand theirs over through `swap` (16 KB), those of the first keep one row of S each (32
-// pairs): S ← keep·S + both.
-__device__ __forceinline__ void update_state(F2 (&S)[32], uint32_t tmem, uint8_t* swap, int row, float keep, int bar) {
-  const bool second = row >= 64;
-  const int r = row & 63;
-  uint4* at = reinterpret_cast<uint4*>(swap + r * 256);
+// A group of four warps holds a state, half a row a thread as 16 pairs: the row of its TMEM lane in the warp's
+// first 16, columns 0 .. 31 in threads 0 .. 15 of the warp and 32 .. 63 in the others.
+__device__ __forceinline__ int row_of(int id) { return 16 * (id >> 5) + (id & 15); }
+__device__ __forceinline__ int half_of(int id) { return (id >> 4) & 1; }
+// Where the thread's half row is in a [64][64] fp32 state.
+__device__ __forceinline__ int half_row(int id) { return row_of(id) * kD + 32 * half_of(id); }
+
+// S ← keep·S + what outer_mma left in TMEM (tmem: the warp's lanes).
+__device__ __forceinline__ void take_sums(F2 (&S)[16], uint32_t tmem, float keep) {
+  const F2 k = f2(keep, keep);
   uint32_t d[32];
-  if (second) {
+  tc::ld_half32(tmem, d);
+  tc::wait_ld();
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      tc::ld32(tmem + 32 * half, d);
-      tc::wait_ld();
-#pragma unroll
-      for (int c = 0; c < 8; ++c) at[(8 * half + c) ^ (r & 7)] = make_uint4(d[4 * c], d[4 * c + 1], d[4 * c + 2], d[4 * c + 3]);
-    }
-  }
-  group_sync(bar);
-  if (!second) {
-    const F2 k = f2(keep, keep);
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      tc::ld32(tmem + 32 * half, d);
-      tc::wait_ld();
-#pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        const uint4 x = at[(8 * half + c) ^ (r & 7)];
-        const int i = 16 * half + 2 * c;
-        S[i] = fma2(k, S[i], add(f2u(d[4 * c], d[4 * c + 1]), f2u(x.x, x.y)));
-        S[i + 1] = fma2(k, S[i + 1], add(f2u(d[4 * c + 2], d[4 * c + 3]), f2u(x.z, x.w)));
-      }
-    }
-  }
+  for (int c = 0; c < 16; ++c) S[c] = fma2(k, S[c], f2u(d[2 * c], d[2 * c + 1]));
 }
 
-// One row of a state between registers and global memory (null: zeros).
-__device__ __forceinline__ void load_row(F2 (&S)[32], const float* p) {
+// A half row between registers and global memory (null: zeros).
+__device__ __forceinline__ void load_row(F2 (&S)[16], const float* p) {
 #pragma unroll
-  for (int c = 0; c < 16; ++c) {
+  for (int c = 0; c < 8; ++c) {
     const float4 x = p != nullptr ? reinterpret_cast<const float4*>(p)[c] : make_float4(0.f, 0.f, 0.f, 0.f);
     S[2 * c] = f2(x.x, x.y);
     S[2 * c + 1] = f2(x.z, x.w);
   }
 }
 
-__device__ __forceinline__ void store_row(const F2 (&S)[32], float* p) {
+__device__ __forceinline__ void store_row(const F2 (&S)[16], float* p) {
 #pragma unroll
-  for (int c = 0; c < 16; ++c) {
+  for (int c = 0; c < 8; ++c) {
     const float2 x = split(S[2 * c]), y = split(S[2 * c + 1]);
     reinterpret_cast<float4*>(p)[c] = make_float4(x.x, x.y, y.x, y.y);
   }
 }
 
-// Row `id` of the state that a segment starts from. With few segments: what those before it add (REV: those
-// after it), in order, onto the pair's state.
+// The thread's half row of the state that a segment starts from. With few segments: what those before it add
+// (REV: those after it), in order, onto the pair's state.
 template <bool REV>
-__device__ __forceinline__ void load_start(F2 (&S)[32], const GsArgs& a, int pair, int seg, int id) {
-  load_row(S, a.start != nullptr ? a.start + ((size_t)(a.few ? pair : pair * a.nseg + seg) * kD + id) * kD : nullptr);
+__device__ __forceinline__ void load_start(F2 (&S)[16], const GsArgs& a, int pair, int seg, int id) {
+  load_row(S, a.start != nullptr ? a.start + (size_t)(a.few ? pair : pair * a.nseg + seg) * kState + half_row(id) : nullptr);
   if (!a.few) return;
   for (int i = REV ? a.nseg - 1 : 0; REV ? i > seg : i < seg; i += REV ? -1 : 1) {
     const size_t at = (size_t)pair * a.nseg + i;
     const float f = exp2_fast(a.seg_decay[REV][at]);
     const F2 ff = f2(f, f);
-    const ulonglong2* x = reinterpret_cast<const ulonglong2*>(a.local[REV] + (at * kD + id) * kD);
+    const ulonglong2* x = reinterpret_cast<const ulonglong2*>(a.local[REV] + at * kState + half_row(id));
 #pragma unroll
-    for (int c = 0; c < 16; ++c) {
+    for (int c = 0; c < 8; ++c) {
       const ulonglong2 y = x[c];
       S[2 * c] = fma2(ff, S[2 * c], F2{y.x});
       S[2 * c + 1] = fma2(ff, S[2 * c + 1], F2{y.y});
@@ -336,11 +314,12 @@ __device__ __forceinline__ void load_start(F2 (&S)[32], const GsArgs& a, int pai
 __device__ __forceinline__ void before_results() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void may_follow() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
-// Row r of a state, rounded to bf16, into a [64][64] tile.
-__device__ __forceinline__ void put_state_row(uint8_t* tile, const F2 (&S)[32], int r) {
+// The thread's half row, rounded to bf16, into a [64][64] tile.
+__device__ __forceinline__ void put_state_row(uint8_t* tile, const F2 (&S)[16], int id) {
+  const int r = row_of(id);
 #pragma unroll
-  for (int c = 0; c < 8; ++c)
-    *reinterpret_cast<uint4*>(tile + r * 128 + ((c ^ (r & 7)) << 4)) =
+  for (int c = 0; c < 4; ++c)
+    *reinterpret_cast<uint4*>(tile + r * 128 + (((4 * half_of(id) + c) ^ (r & 7)) << 4)) =
         make_uint4(to_bf16(S[4 * c]), to_bf16(S[4 * c + 1]), to_bf16(S[4 * c + 2]), to_bf16(S[4 * c + 3]));
 }
 
@@ -396,87 +375,30 @@ __device__ __forceinline__ void let_land(const volatile int* abort) {
 
 struct __align__(1024) SegSmem {
   uint8_t X[2][kLTile];  // X; once weighed, the first term of w ⊙ X
-  uint8_t L[2][kLTile];  // the second term
   uint8_t Y[2][kLTile];
-  uint8_t swap[kTile];   // CKPT: the second terms' part of the state, 2^-9 of it, rounded to bf16
-  Gates gates[3];
+  uint8_t L[2][kLTile];  // the second and third terms
+  Gates gates[4];
   __align__(16) float raw[2][kL];
-  uint64_t full[2], done[2];
+  uint64_t full[2], done[2], gated[4], read[4];
   uint32_t tmem;
   int abort;
 };
 
-// Adds what outer_mma left in TMEM onto a row of one part of the state: S ← keep·S + sums.
-__device__ __forceinline__ void take_sums(F2 (&S)[32], uint32_t tmem, float keep) {
-  const F2 k = f2(keep, keep);
-#pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    uint32_t d[32];
-    tc::ld32(tmem + 32 * half, d);
-    tc::wait_ld();
-#pragma unroll
-    for (int c = 0; c < 16; ++c) S[16 * half + c] = fma2(k, S[16 * half + c], f2u(d[2 * c], d[2 * c + 1]));
-  }
-}
-
-// The two parts of a state, rows of the first in threads 0 .. 63 of a group and of the second in 64 .. 127,
-// added up in the first through `swap` (16 KB), in fp32.
-__device__ __forceinline__ void join_parts(F2 (&S)[32], uint8_t* swap, int id, int bar) {
-  float4* at = reinterpret_cast<float4*>(swap) + (id & 63) * 16;
-  if (id >= 64) {
-#pragma unroll
-    for (int c = 0; c < 16; ++c) {
-      const float2 x = split(S[2 * c]), y = split(S[2 * c + 1]);
-      at[c ^ (id & 7)] = make_float4(x.x, x.y, y.x, y.y);
-    }
-  }
-  group_sync(bar);
-  if (id < 64) {
-#pragma unroll
-    for (int c = 0; c < 16; ++c) {
-      const float4 x = at[c ^ (id & 7)];
-      S[2 * c] = add(S[2 * c], f2(x.x, x.y));
-      S[2 * c + 1] = add(S[2 * c + 1], f2(x.z, x.w));
-    }
-  }
-}
-
-// The two parts added up and rounded to bf16 twice, the value and what that rounding left, eight pairs of
-// pieces at a time to put(16-byte piece, value, rest); the second part comes through `swap` in bf16 (it is
-// 2^-9 of the state).
-template <class Put>
-__device__ __forceinline__ void split_parts(const F2 (&S)[32], uint8_t* swap, int id, int bar, Put put) {
-  if (id >= 64) put_state_row(swap, S, id & 63);
-  group_sync(bar);
-  if (id < 64) {
-#pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      const uint4 x = *reinterpret_cast<const uint4*>(swap + id * 128 + ((c ^ (id & 7)) << 4));
-      const uint32_t second[4] = {x.x, x.y, x.z, x.w};
-      uint32_t h[4], l[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const F2 both = add(S[4 * c + e], from_bf16(second[e]));
-        h[e] = to_bf16(both);
-        l[e] = to_bf16(fma2(from_bf16(h[e]), f2(-1.f, -1.f), both));
-      }
-      put(c, make_uint4(h[0], h[1], h[2], h[3]), make_uint4(l[0], l[1], l[2], l[3]));
-    }
-  }
-}
+constexpr int kSegThreads = 320;
 
 // Runs the state alone over a segment. Forward: X = K, Y = V, weights w; in reverse, from the last chunk to
-// the first: X = Q, Y = dO, weights scale·2^b. All 256 threads weigh half a row of X each, and the tensor
-// cores take the tile while the next is weighed; threads 128 .. 255 add the sums of the chunk before (two
-// sets of TMEM columns) to a row of the state each, rows 0 .. 63 the first terms' part of it and 64 .. 127
-// the second's, which are added at the end. CKPT: writes the state before every chunk, as two bf16 planes
-// (forward). grid (pairs · nseg, directions).
+// the first: X = Q, Y = dO, weights scale·2^b. Warps 0 .. 7 weigh half a row of X a thread while the tensor
+// cores take the tile before; warps 4 .. 7 then add the sums of the chunk before (two sets of TMEM columns) to
+// half a row of the state each. Warp 8 asks for the tiles and issues the products, warp 9 makes the gates: in a
+// weighing warp both held up the next chunk's weighing (8 x 12 heads x 2048 tokens: 19.5 us against 17.9). A chunk
+// takes some 3000 cycles, of which the 24 products' instructions take 1900 with two CTAs at it. CKPT: writes the
+// state before every chunk, as three bf16 planes (forward). grid (pairs · nseg, directions).
 struct SegTiles {
   Tiles x[2], y[2];
 };
 
 template <bool CKPT>
-__global__ void __launch_bounds__(256, 2) k_gs_segment(const __grid_constant__ SegTiles tiles, const GsArgs a) {
+__global__ void __launch_bounds__(kSegThreads, 2) k_gs_segment(const __grid_constant__ SegTiles tiles, const GsArgs a) {
   extern __shared__ uint8_t smem_raw[];
   SegSmem& sm = *reinterpret_cast<SegSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, id = tid & 127;
@@ -485,10 +407,10 @@ __global__ void __launch_bounds__(256, 2) k_gs_segment(const __grid_constant__ S
   const Tiles &tx = tiles.x[blockIdx.y], &ty = tiles.y[blockIdx.y];
   may_follow();
   if (!CKPT && seg == (rev ? 0 : a.nseg - 1)) return;  // no segment starts from what this one adds
-  const int bi = pair / a.heads, hi_ = pair % a.heads;
-  const float* gp = a.g + bi * a.gb + hi_ * a.gh;
   const int c0 = seg * a.per_seg, c1 = min(a.nchunk, c0 + a.per_seg), n = c1 - c0;
   auto chunk_of = [&](int i) { return rev ? c1 - 1 - i : c0 + i; };
+  const int bi = pair / a.heads, hi_ = pair % a.heads;
+  const float* gp = a.g + bi * a.gb + hi_ * a.gh;
   auto load = [&](int i) {
     if (!CKPT && i == a.stall) return;
     uint64_t* bar = &sm.full[i & 1];
@@ -496,120 +418,124 @@ __global__ void __launch_bounds__(256, 2) k_gs_segment(const __grid_constant__ S
     tma_load_tile(sm.X[i & 1], &tx.map, bar, chunk_of(i) * kL, hi_ * tx.head, bi * tx.batch);
     tma_load_tile(sm.Y[i & 1], &ty.map, bar, chunk_of(i) * kL, hi_ * ty.head, bi * ty.batch);
   };
-  auto prefetch = [&](int i) {
-    tma_prefetch_tile(&tx.map, chunk_of(i) * kL, hi_ * tx.head, bi * tx.batch);
-    tma_prefetch_tile(&ty.map, chunk_of(i) * kL, hi_ * ty.head, bi * ty.batch);
-  };
-  if (tid == 0) {
+  if (tid == 256) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.full[i], 1);
       mbar_init(&sm.done[i], 1);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&sm.gated[i], 1);
+      mbar_init(&sm.read[i], 4);
     }
     sm.abort = 0;
     fence_barrier_init();
     load(0);
     if (n > 1) load(1);
-    if (n > 2) prefetch(2);
   }
+  if (warp == 9) fetch_gates(a, gp, (int64_t)chunk_of(0) * kL, sm.raw[0], lane);
   if (warp == 4) tc::alloc(&sm.tmem, 128);
-  if (warp == 3) {
-    fetch_gates(a, gp, (int64_t)chunk_of(0) * kL, sm.raw[0], lane);
-    make_gates<float>(sm.raw[0], sm.gates[0], lane);
-    if (n > 1) fetch_gates(a, gp, (int64_t)chunk_of(1) * kL, sm.raw[1], lane);
-  }
-  // Half a row of chunk i's X: its first term in place, its second beside.
-  auto weigh_chunk = [&](int i) {
-    const int ph = i & 1, c0_ = 4 * (tid >> 7);
-    const Gates& gt = sm.gates[i % 3];
-    const float w = rev ? a.scale * exp2_fast(gt.b[id]) : gt.w[id];
-    const F2 ww = f2(w, w);
-    mbar_wait(&sm.full[ph], (i >> 1) & 1, a.status, &sm.abort);
-#pragma unroll
-    for (int c = c0_; c < c0_ + 4; ++c) {
-      const uint32_t at = id * 128 + ((c ^ (id & 7)) << 4);
-      const uint4 x = *reinterpret_cast<const uint4*>(sm.X[ph] + at);
-      uint4 h, l;
-      weigh(x.x, ww, h.x, l.x);
-      weigh(x.y, ww, h.y, l.y);
-      weigh(x.z, ww, h.z, l.z);
-      weigh(x.w, ww, h.w, l.w);
-      *reinterpret_cast<uint4*>(sm.X[ph] + at) = h;
-      *reinterpret_cast<uint4*>(sm.L[ph] + at) = l;
-    }
-    fence_proxy_async_smem();
-  };
   tc::fence_before();
-  cta_sync<256>();
+  cta_sync<kSegThreads>();
   tc::fence_after();
-  if (warp < 4) {
-    const uint32_t tm = sm.tmem, dx = desc_of(sm.X[0], 2 * kLTile), dy = desc_of(sm.Y[0]);
+  const uint32_t tm = sm.tmem;
+  if (warp == 8) {
+    const uint32_t dx = desc_of(sm.X[0]), dl = desc_of(sm.L[0]), dy = desc_of(sm.Y[0]);
     for (int i = 0; i < n; ++i) {
       const int ph = i & 1;
-      weigh_chunk(i);
-      cta_sync<256>();  // also: the sums two chunks back have been taken
-      if (tid == 0) {
+      if (i > 0) {
+        mbar_wait(&sm.done[ph ^ 1], ((i - 1) >> 1) & 1, a.status, &sm.abort);
+        if (lane == 0 && i + 1 < n) load(i + 1);  // the tiles of the chunk before have been read
+        __syncwarp();
+      }
+      asm volatile("bar.sync 1, 288;" ::: "memory");  // the chunk is weighed, and the sums two chunks back have been taken
+      if (lane == 0) {
         tc::fence_after();
-        outer_mma(tm + 64 * ph, dx + ph * (kLTile >> 4), dy + ph * (kLTile >> 4));
+        const uint32_t d = tm + 64 * ph, y = dy + ph * (kLTile >> 4);
+        outer_mma(d, dl + (kLTile >> 4), y, true);
+        outer_mma(d, dl, y, false);
+        outer_mma(d, dx + ph * (kLTile >> 4), y, false);
         tc::commit(&sm.done[ph]);
       }
-      if (warp == 3 && i + 1 < n) {
-        make_gates<float>(sm.raw[ph ^ 1], sm.gates[(i + 1) % 3], lane);
-        if (i + 2 < n) fetch_gates(a, gp, (int64_t)chunk_of(i + 2) * kL, sm.raw[ph], lane);
-      }
-      group_sync(1);  // the next chunk's gates are there
-      if (warp == 3) asm volatile("bar.arrive 3, 160;" ::: "memory");
+      __syncwarp();
+    }
+  } else if (warp == 9) {
+    for (int i = 0; i < n; ++i) {
+      if (i + 1 < n) fetch_gates(a, gp, (int64_t)chunk_of(i + 1) * kL, sm.raw[(i + 1) & 1], lane);
+      if (i > 3) mbar_wait(&sm.read[i & 3], ((i >> 2) - 1) & 1, a.status, &sm.abort);
+      make_gates<float>(sm.raw[i & 1], sm.gates[i & 3], lane, i + 1 < n);
+      if (lane == 0) mbar_arrive(&sm.gated[i & 3]);
     }
   } else {
-    const uint32_t tmem = sm.tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    F2 S[32];
-    if (CKPT) {
-      before_results();
-      if (id < 64)
-        load_start<false>(S, a, pair, seg, id);
-      else
-        load_row(S, nullptr);
+    // Half a row of chunk i's X: its first term in place, the others beside once the products of the chunk before
+    // have read theirs.
+    const int first = 4 * (tid >> 7);
+    auto weigh_chunk = [&](int i) {
+      const int ph = i & 1;
+      const Gates& gt = sm.gates[i & 3];
+      mbar_wait(&sm.gated[i & 3], (i >> 2) & 1, a.status, &sm.abort);
+      const float w = rev ? a.scale * exp2_fast(gt.b[id]) : gt.w[id];
+      mbar_wait(&sm.full[ph], (i >> 1) & 1, a.status, &sm.abort);
+      uint4 t[4][3];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint4* x = reinterpret_cast<uint4*>(sm.X[ph] + id * 128 + (((first + c) ^ (id & 7)) << 4));
+        weigh(*x, f2(w, w), t[c]);
+        *x = t[c][0];
+      }
+      if (i > 0) mbar_wait(&sm.done[ph ^ 1], ((i - 1) >> 1) & 1, a.status, &sm.abort);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const uint32_t at = id * 128 + (((first + c) ^ (id & 7)) << 4);
+        *reinterpret_cast<uint4*>(sm.L[0] + at) = t[c][1];
+        *reinterpret_cast<uint4*>(sm.L[1] + at) = t[c][2];
+      }
+      fence_proxy_async_smem();
+      tc::fence_before();
+      asm volatile("bar.arrive 1, 288;" ::: "memory");
+    };
+    if (warp < 4) {
+      for (int i = 0; i < n; ++i) weigh_chunk(i);
     } else {
-      load_row(S, nullptr);
-    }
-    float decay = 0.f;
-    for (int i = 0; i <= n; ++i) {
-      if (i < n) {
-        if (i > 0) asm volatile("bar.sync 3, 160;" ::: "memory");  // this chunk's gates are there
-        weigh_chunk(i);
-        tc::fence_before();
-        cta_sync<256>();
+      const uint32_t tmem = tm + ((uint32_t)((warp & 3) * 32) << 16);
+      F2 S[16];
+      if (CKPT) {
+        before_results();
+        load_start<false>(S, a, pair, seg, id);
+      } else {
+        load_row(S, nullptr);
       }
-      if (i > 0) {
-        const int last = (i - 1) & 1;
-        mbar_wait(&sm.done[last], ((i - 1) >> 1) & 1, a.status, &sm.abort);
-        tc::fence_after();
-        if (id == 0 && i + 1 < n) {
-          load(i + 1);  // the tiles of the chunk before have been read
-          if (i + 2 < n) prefetch(i + 2);
+      float decay = 0.f;
+      for (int i = 0; i <= n; ++i) {
+        if (i < n) weigh_chunk(i);
+        if (i > 0) {
+          const int last = (i - 1) & 1;
+          mbar_wait(&sm.done[last], ((i - 1) >> 1) & 1, a.status, &sm.abort);
+          tc::fence_after();
+          const float total = sm.gates[(i - 1) & 3].total;
+          if (lane == 0) mbar_arrive(&sm.read[(i - 1) & 3]);
+          take_sums(S, tmem + 64 * last, exp2_fast(total));
+          decay += total;
         }
-        __syncwarp();
-        const float total = sm.gates[(i - 1) % 3].total;
-        take_sums(S, tmem + 64 * last, exp2_fast(total));
-        decay += total;
+        if (CKPT && i < n) {
+          uint4* p = reinterpret_cast<uint4*>(a.ckpt + ((size_t)pair * a.nchunk + chunk_of(i)) * 3 * kState) + 256 * half_of(id) + row_of(id);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t t[3][4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) terms_of(S[4 * c + e], t[0][e], t[1][e], t[2][e]);
+#pragma unroll
+            for (int k = 0; k < 3; ++k) p[64 * c + k * (kState / 8)] = make_uint4(t[k][0], t[k][1], t[k][2], t[k][3]);
+          }
+        }
       }
-      if (CKPT && i < n) {
-        uint4* p = reinterpret_cast<uint4*>(a.ckpt + ((size_t)pair * a.nchunk + chunk_of(i)) * 2 * kState) + id;
-        split_parts(S, sm.swap, id, 2, [&](int c, uint4 h, uint4 l) {
-          p[64 * c] = h;
-          p[64 * c + kState / 8] = l;
-        });
-        group_sync(2);
+      if (!CKPT) {
+        store_row(S, a.local[rev] + (size_t)blockIdx.x * kState + half_row(id));
+        if (id == 0) a.seg_decay[rev][blockIdx.x] = decay;
       }
-    }
-    asm volatile("bar.sync 3, 160;" ::: "memory");
-    if (!CKPT) {
-      join_parts(S, sm.X[0], id, 2);  // the products are done
-      if (id < 64) store_row(S, a.local[rev] + ((size_t)blockIdx.x * kD + id) * kD);
-      if (id == 0) a.seg_decay[rev][blockIdx.x] = decay;
     }
   }
   tc::fence_before();
-  cta_sync<256>();
+  cta_sync<kSegThreads>();
   tc::fence_after();
   if (warp == 4) {
     let_land(&sm.abort);
@@ -621,7 +547,7 @@ __global__ void __launch_bounds__(256, 2) k_gs_segment(const __grid_constant__ S
 struct __align__(1024) OutSmem {
   uint8_t Q[kLTile], K[kLTile];
   uint8_t V[2][kLTile];    // a chunk's V; after its products its outputs on their way out
-  uint8_t W[2][kLTile];    // the weighted K, two terms
+  uint8_t W[2][kLTile];    // the weighted K's second and third terms; the first takes K's place
   uint8_t S[kTile];        // bf16 copy of the state before the chunk
   Gates gates[2];
   __align__(16) float raw[2][kL];
@@ -638,8 +564,9 @@ constexpr int kColP = 0, kColO = 64, kColQS = 128, kColD = 192, kOutCols = 256;
 // 256 threads, two CTAs an SM, so that one's products and loads run under the other's arithmetic.
 // Threads 0 .. 127 take a row of the chunk's outputs each: Q·Kᵀ comes from TMEM, is weighted, rounded
 // and put back as the first operand of P·V without passing through shared memory. Threads 128 .. 255
-// weigh K and carry the state (the first 64 hold a row each). Tiles come and go by TMA: the next
-// chunk's Q and K as soon as the tensor cores have read these, V into the other of two buffers.
+// weigh K and carry the state, half a row each: the second and third terms go to buffers of their own and into the
+// tensor cores before the scores are done, the first into K's place when they are. Tiles come and go by TMA:
+// the next chunk's Q when the scores are done, its K when the state's sums are, V into the other of two buffers.
 // grid: pairs · nseg.
 __global__ void __launch_bounds__(256, 2)
     k_gs_out(const __grid_constant__ Tiles tq, const __grid_constant__ Tiles tk, const __grid_constant__ Tiles tv,
@@ -652,11 +579,11 @@ __global__ void __launch_bounds__(256, 2)
   const int bi = pair / a.heads, hi_ = pair % a.heads;
   const float* gp = a.g + bi * a.gb + hi_ * a.gh;
   const int c0 = seg * a.per_seg, c1 = min(a.nchunk, c0 + a.per_seg), n = c1 - c0;
-  auto load_qk = [&](int i) {
+  auto load_q = [&](int i) {
     mbar_arrive_expect_tx(&sm.qk, 2 * kLTile);
     tma_load_tile(sm.Q, &tq.map, &sm.qk, (c0 + i) * kL, hi_ * tq.head, bi * tq.batch);
-    tma_load_tile(sm.K, &tk.map, &sm.qk, (c0 + i) * kL, hi_ * tk.head, bi * tk.batch);
   };
+  auto load_k = [&](int i) { tma_load_tile(sm.K, &tk.map, &sm.qk, (c0 + i) * kL, hi_ * tk.head, bi * tk.batch); };
   auto load_v = [&](int i) {
     if (i == a.stall) return;
     mbar_arrive_expect_tx(&sm.v[i & 1], kLTile);
@@ -671,7 +598,8 @@ __global__ void __launch_bounds__(256, 2)
     mbar_init(&sm.added, 1);
     sm.abort = 0;
     fence_barrier_init();
-    load_qk(0);
+    load_q(0);
+    load_k(0);
     load_v(0);
   }
   if (warp == 0) tc::alloc(&sm.tmem, kOutCols);
@@ -786,45 +714,67 @@ __global__ void __launch_bounds__(256, 2)
     }
     if (tid == 0) bulk_wait_read<0>();
   } else {
-    F2 S[32];
+    F2 S[16];
     if (warp == 7) {
       fetch_gates(a, gp, (int64_t)c0 * kL, sm.raw[0], lane);
       make_gates<double>(sm.raw[0], sm.gates[0], lane);
       if (n > 1) fetch_gates(a, gp, (int64_t)(c0 + 1) * kL, sm.raw[1], lane);
     }
     before_results();
-    if (id < 64) {
-      load_start<false>(S, a, pair, seg, id);
-      put_state_row(sm.S, S, id);
-    }
+    load_start<false>(S, a, pair, seg, id);
+    put_state_row(sm.S, S, id);
     fence_proxy_async_smem();
     tc::fence_before();
     cta_sync<256>();
     tc::fence_after();
     const uint32_t tm = sm.tmem, tmem = tm + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t dv = desc_of(sm.V[0]), dw = desc_of(sm.W[0], kLTile);
+    const uint32_t dk = desc_of(sm.K), dv = desc_of(sm.V[0]), dw = desc_of(sm.W[0]);
     for (int i = 0; i < n; ++i) {
       const int ph = i & 1;
       const Gates& gt = sm.gates[ph];
       mbar_wait(&sm.qk, ph, a.status, &sm.abort);
-      weigh_row(sm.K, sm.W[0], sm.W[1], id, gt.w[id]);
+      uint4 top[8];
+      {
+        const F2 w = f2(gt.w[id], gt.w[id]);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const uint32_t at = id * 128 + ((c ^ (id & 7)) << 4);
+          uint4 t[3];
+          weigh(*reinterpret_cast<const uint4*>(sm.K + at), w, t);
+          top[c] = t[0];
+          *reinterpret_cast<uint4*>(sm.W[0] + at) = t[1];
+          *reinterpret_cast<uint4*>(sm.W[1] + at) = t[2];
+        }
+      }
       fence_proxy_async_smem();
       tc::fence_before();
       group_sync(2);
+      const uint32_t v = dv + ph * (kLTile >> 4);
       if (id == 0) {
         tc::fence_after();
         mbar_wait(&sm.v[ph], (i >> 1) & 1, a.status, &sm.abort);
-        outer_mma(tm + kColD, dw, dv + ph * (kLTile >> 4));
-        tc::commit(&sm.added);
+        outer_mma(tm + kColD, dw + (kLTile >> 4), v, true);
+        outer_mma(tm + kColD, dw, v, false);
       }
       __syncwarp();
       mbar_wait(&sm.scores, ph, a.status, &sm.abort);  // Q, K and the state's copy have been read
-      if (id == 0 && i + 1 < n) load_qk(i + 1);
+      if (id == 0 && i + 1 < n) load_q(i + 1);
+      __syncwarp();
+#pragma unroll
+      for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(sm.K + id * 128 + ((c ^ (id & 7)) << 4)) = top[c];
+      fence_proxy_async_smem();
+      group_sync(2);
+      if (id == 0) {
+        outer_mma(tm + kColD, dk, v, false);
+        tc::commit(&sm.added);
+      }
       __syncwarp();
       mbar_wait(&sm.added, ph, a.status, &sm.abort);
+      if (id == 0 && i + 1 < n) load_k(i + 1);
+      __syncwarp();
       tc::fence_after();
-      update_state(S, tmem + kColD, sm.W[1], id, exp2_fast(gt.total), 2);
-      if (id < 64) put_state_row(sm.S, S, id);
+      take_sums(S, tmem + kColD, exp2_fast(gt.total));
+      put_state_row(sm.S, S, id);
       if (warp == 7 && i + 1 < n) {
         make_gates<double>(sm.raw[ph ^ 1], sm.gates[ph ^ 1], lane);
         if (i + 2 < n) fetch_gates(a, gp, (int64_t)(c0 + i + 2) * kL, sm.raw[ph], lane);
@@ -834,7 +784,7 @@ __global__ void __launch_bounds__(256, 2)
       cta_sync<256>();
       tc::fence_after();
     }
-    if (a.end != nullptr && seg == a.nseg - 1 && id < 64) store_row(S, a.end + ((size_t)pair * kD + id) * kD);
+    if (a.end != nullptr && seg == a.nseg - 1) store_row(S, a.end + (size_t)pair * kState + half_row(id));
   }
   __syncthreads();
   if (warp == 0) {
@@ -848,13 +798,13 @@ __global__ void __launch_bounds__(256, 2)
 
 struct __align__(1024) BwdSmem {
   uint8_t Q[kLTile], K[kLTile], V[kLTile], G[kLTile];  // G: dO
-  uint8_t S[2][kTile];    // the state before the chunk: rounded, and what the rounding left; [8 pieces][64 rows][16 bytes]
-  uint8_t dS[2][kTile];   // the gradient of the state after the chunk, the same way
-  uint8_t W[2][kLTile];   // u ⊙ Q, two terms; then dV and dK on their way out
-  uint8_t P[2][kLTile];   // P and A, 128 queries x 128 keys, in halves of 64 keys
+  uint8_t S[3][kTile];    // the state before the chunk, three terms, [8 pieces][64 rows][16 bytes] each
+  uint8_t dS[2][kTile];   // the gradient of the state after the chunk, first two terms
+  uint8_t W[2][kLTile];   // u ⊙ Q, first two terms; then dV and dK on their way out
+  uint8_t P[2][kLTile];   // P and A, 128 queries x 128 keys, in halves of 64 keys; P[1]'s first 64 rows, the queries
+                          // before its keys, are not read: they hold the third term of dS
   uint8_t A[2][kLTile];
-  uint8_t out[kLTile];    // dQ on its way out
-  uint8_t swap[kTile];    // the second terms' part of dS, 2^-9 of it, rounded to bf16
+  uint8_t out[kLTile];    // u ⊙ Q, third term; then dQ on its way out
   Gates gates[2];
   __align__(16) float raw[3][kL];
   __align__(16) float rows[2][kL];  // Σ_j A_ij·(q_i·k_j) over j < i, per half of the keys
@@ -915,31 +865,32 @@ __device__ __forceinline__ void finish_row(const F2 (&x)[32], uint32_t tmem, uin
   }
 }
 
-// dS as two bf16 terms into the tiles.
-__device__ __forceinline__ void put_ds(BwdSmem& sm, const F2 (&S)[32], int id) {
-  split_parts(S, sm.swap, id, 3, [&](int c, uint4 h, uint4 l) {
-    const uint32_t at = id * 128 + ((c ^ (id & 7)) << 4);
-    *reinterpret_cast<uint4*>(sm.dS[0] + at) = h;
-    *reinterpret_cast<uint4*>(sm.dS[1] + at) = l;
-  });
+// dS as three bf16 terms into the tiles.
+__device__ __forceinline__ void put_ds(BwdSmem& sm, const F2 (&S)[16], int id) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const uint32_t at = row_of(id) * 128 + (((4 * half_of(id) + c) ^ (id & 7)) << 4);
+    uint32_t t[3][4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) terms_of(S[4 * c + e], t[0][e], t[1][e], t[2][e]);
+    *reinterpret_cast<uint4*>(sm.dS[0] + at) = make_uint4(t[0][0], t[0][1], t[0][2], t[0][3]);
+    *reinterpret_cast<uint4*>(sm.dS[1] + at) = make_uint4(t[1][0], t[1][1], t[1][2], t[1][3]);
+    *reinterpret_cast<uint4*>(sm.P[1] + at) = make_uint4(t[2][0], t[2][1], t[2][2], t[2][3]);
+  }
 }
 
-// Half a row (16-byte pieces c0 .. c0 + 3) of u ⊙ Q, as two bf16 terms, by groups 2 and 3 together.
+// Half a row (16-byte pieces c0 .. c0 + 3) of u ⊙ Q, as three bf16 terms, by groups 2 and 3 together.
 __device__ __forceinline__ void weigh_half(BwdSmem& sm, const GsArgs& a, int id, int c0, float u, int ph, bool later) {
   mbar_wait(&sm.in, ph, a.status, &sm.abort);
-  if (later) mbar_wait(&sm.sent, ph ^ 1, a.status, &sm.abort);  // dV and dK have left the buffers
-  const F2 uu = f2(u, u);
+  if (later) mbar_wait(&sm.sent, ph ^ 1, a.status, &sm.abort);  // the last chunk's gradients have left the buffers
 #pragma unroll
   for (int c = c0; c < c0 + 4; ++c) {
     const uint32_t at = id * 128 + ((c ^ (id & 7)) << 4);
-    const uint4 x = *reinterpret_cast<const uint4*>(sm.Q + at);
-    uint4 h, l;
-    weigh(x.x, uu, h.x, l.x);
-    weigh(x.y, uu, h.y, l.y);
-    weigh(x.z, uu, h.z, l.z);
-    weigh(x.w, uu, h.w, l.w);
-    *reinterpret_cast<uint4*>(sm.W[0] + at) = h;
-    *reinterpret_cast<uint4*>(sm.W[1] + at) = l;
+    uint4 t[3];
+    weigh(*reinterpret_cast<const uint4*>(sm.Q + at), f2(u, u), t);
+    *reinterpret_cast<uint4*>(sm.W[0] + at) = t[0];
+    *reinterpret_cast<uint4*>(sm.W[1] + at) = t[1];
+    *reinterpret_cast<uint4*>(sm.out + at) = t[2];
   }
   fence_proxy_async_smem();
   asm volatile("bar.sync 2, 256;" ::: "memory");
@@ -959,12 +910,11 @@ __device__ __forceinline__ uint64_t pieces_at(const void* tile, int bytes) {
 // `id` of a group holds row `id` of what the group reads from TMEM.
 //   group 0  the scores of keys 0 .. 63: P, A and their sums; dQ
 //   group 1  the same for keys 64 .. 127; dV
-//   group 2  weighs Q (half of each row); carries dS, rows 0 .. 63 the first terms' part and 64 .. 127 the
-//            second's; dg
+//   group 2  weighs Q (half of each row); carries dS, half a row a thread; dg
 //   group 3  weighs Q (the other half); dK
-// All products of a chunk read its tiles from shared memory, which bounds the kernel (some 650 KB a
-// chunk through 128 bytes a cycle). The next chunk's tiles are asked for when the last product has
-// read these, and come while the gradients are rounded and sent out. grid: pairs · nseg.
+// All products of a chunk read its tiles from shared memory, and thread-issued copies of 650 KB pass through it too
+// (3700 of a chunk's cycles by the counted wavefronts of both). The next chunk's tiles are asked for when the last
+// product has read these, and come while the gradients are rounded and sent out. grid: pairs · nseg.
 __global__ void __launch_bounds__(512, 1) k_gs_bwd(const __grid_constant__ BwdTiles tm_, const GsArgs a) {
   extern __shared__ uint8_t smem_raw[];
   BwdSmem& sm = *reinterpret_cast<BwdSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -973,16 +923,16 @@ __global__ void __launch_bounds__(512, 1) k_gs_bwd(const __grid_constant__ BwdTi
   const int bi = pair / a.heads, hi_ = pair % a.heads;
   const float* gp = a.g + bi * a.gb + hi_ * a.gh;
   const int c0 = seg * a.per_seg, c1 = min(a.nchunk, c0 + a.per_seg), n = c1 - c0;
-  const __nv_bfloat16* states = a.ckpt + (size_t)pair * a.nchunk * 2 * kState;
+  const __nv_bfloat16* states = a.ckpt + (size_t)pair * a.nchunk * 3 * kState;
   auto load = [&](int i) {
     if (i == a.stall) return;
     const int t = (c1 - 1 - i) * kL;
-    mbar_arrive_expect_tx(&sm.in, 4 * kLTile + 2 * kTile);
+    mbar_arrive_expect_tx(&sm.in, 4 * kLTile + 3 * kTile);
     tma_load_tile(sm.Q, &tm_.q.map, &sm.in, t, hi_ * tm_.q.head, bi * tm_.q.batch);
     tma_load_tile(sm.K, &tm_.k.map, &sm.in, t, hi_ * tm_.k.head, bi * tm_.k.batch);
     tma_load_tile(sm.G, &tm_.g.map, &sm.in, t, hi_ * tm_.g.head, bi * tm_.g.batch);
     tma_load_tile(sm.V, &tm_.v.map, &sm.in, t, hi_ * tm_.v.head, bi * tm_.v.batch);
-    bulk_load(sm.S, states + (size_t)(c1 - 1 - i) * 2 * kState, 2 * kTile, &sm.in);
+    bulk_load(sm.S, states + (size_t)(c1 - 1 - i) * 3 * kState, 3 * kTile, &sm.in);
   };
   auto prefetch = [&](int i) {
     const int t = (c1 - 1 - i) * kL;
@@ -990,7 +940,7 @@ __global__ void __launch_bounds__(512, 1) k_gs_bwd(const __grid_constant__ BwdTi
     tma_prefetch_tile(&tm_.k.map, t, hi_ * tm_.k.head, bi * tm_.k.batch);
     tma_prefetch_tile(&tm_.g.map, t, hi_ * tm_.g.head, bi * tm_.g.batch);
     tma_prefetch_tile(&tm_.v.map, t, hi_ * tm_.v.head, bi * tm_.v.batch);
-    bulk_prefetch(states + (size_t)(c1 - 1 - i) * 2 * kState, 2 * kTile);
+    bulk_prefetch(states + (size_t)(c1 - 1 - i) * 3 * kState, 3 * kTile);
   };
   if (tid == 0) {
     mbar_init(&sm.in, 1);
@@ -998,7 +948,7 @@ __global__ void __launch_bounds__(512, 1) k_gs_bwd(const __grid_constant__ BwdTi
     mbar_init(&sm.inter, 1);
     mbar_init(&sm.added, 1);
     mbar_init(&sm.grads, 1);
-    mbar_init(&sm.sent, 2);
+    mbar_init(&sm.sent, 3);
     sm.abort = 0;
     fence_barrier_init();
     before_results();  // the states before the chunks
@@ -1007,7 +957,7 @@ __global__ void __launch_bounds__(512, 1) k_gs_bwd(const __grid_constant__ BwdTi
   if (warp == 4) tc::alloc(&sm.tmem, 512);
   // Keys after a query's block of 32 never get a score: zero once.
   for (int i = tid; i < 2 * kLTile / 16; i += 512) {
-    reinterpret_cast<uint4*>(sm.P[0])[i] = make_uint4(0, 0, 0, 0);
+    if (i < kLTile / 16 || i >= (kLTile + kTile) / 16) reinterpret_cast<uint4*>(sm.P[0])[i] = make_uint4(0, 0, 0, 0);
     reinterpret_cast<uint4*>(sm.A[0])[i] = make_uint4(0, 0, 0, 0);
   }
   for (int i = tid; i < 4 * kL; i += 512) (&sm.cols[0][0])[i] = 0.f;
@@ -1015,12 +965,9 @@ __global__ void __launch_bounds__(512, 1) k_gs_bwd(const __grid_constant__ BwdTi
   // Group 2 runs a loop of its own, so that dS's registers are not held through the others' work; barrier
   // 0 joins all groups twice a chunk.
   if (group == 2) {
-    F2 S[32];  // a row of one part of dS
+    F2 S[16];  // half a row of dS
     before_results();
-    if (id < 64)
-      load_start<true>(S, a, pair, seg, id);
-    else
-      load_row(S, nullptr);
+    load_start<true>(S, a, pair, seg, id);
     put_ds(sm, S, id);
     if (warp == 11) {
       fetch_gates(a, gp, (int64_t)(c1 - 1) * kL, sm.raw[0], lane);
@@ -1041,21 +988,23 @@ __global__ void __launch_bounds__(512, 1) k_gs_bwd(const __grid_constant__ BwdTi
       __syncwarp();
       weigh_half(sm, a, id, 0, a.scale * exp2_fast(gt.b[id]), ph, i > 0);
       if (id == 0) {
-        outer_mma(tm + kColDs, desc_of(sm.W[0], kLTile), desc_of(sm.G));
+        outer_mma(tm + kColDs, desc_of(sm.out), desc_of(sm.G), true);
+        outer_mma(tm + kColDs, desc_of(sm.W[1]), desc_of(sm.G), false);
+        outer_mma(tm + kColDs, desc_of(sm.W[0]), desc_of(sm.G), false);
         tc::commit(&sm.added);
       }
       __syncwarp();
       const float keep = exp2_fast(gt.total);
       F2 d = f2(0.f, 0.f);
-      const int r = id & 63;
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        const uint32_t at = (64 * c + r) * 16;
-        const uint4 x = *reinterpret_cast<const uint4*>(sm.S[0] + at), y = *reinterpret_cast<const uint4*>(sm.S[1] + at);
-        d = fma2(S[4 * c], add(from_bf16(x.x), from_bf16(y.x)), d);
-        d = fma2(S[4 * c + 1], add(from_bf16(x.y), from_bf16(y.y)), d);
-        d = fma2(S[4 * c + 2], add(from_bf16(x.z), from_bf16(y.z)), d);
-        d = fma2(S[4 * c + 3], add(from_bf16(x.w), from_bf16(y.w)), d);
+      for (int c = 0; c < 4; ++c) {
+        const uint32_t at = (64 * (4 * half_of(id) + c) + row_of(id)) * 16;
+        const uint4 x = *reinterpret_cast<const uint4*>(sm.S[0] + at), y = *reinterpret_cast<const uint4*>(sm.S[1] + at),
+                    z = *reinterpret_cast<const uint4*>(sm.S[2] + at);
+        d = fma2(S[4 * c], add(from_bf16(x.x), add(from_bf16(y.x), from_bf16(z.x))), d);
+        d = fma2(S[4 * c + 1], add(from_bf16(x.y), add(from_bf16(y.y), from_bf16(z.y))), d);
+        d = fma2(S[4 * c + 2], add(from_bf16(x.z), add(from_bf16(y.z), from_bf16(z.z))), d);
+        d = fma2(S[4 * c + 3], add(from_bf16(x.w), add(from_bf16(y.w), from_bf16(z.w))), d);
       }
       const float2 dd = split(d);
       float dot = dd.x + dd.y;
@@ -1111,10 +1060,7 @@ __global__ void __launch_bounds__(512, 1) k_gs_bwd(const __grid_constant__ BwdTi
       cta_sync<512>();
       tc::fence_after();
     }
-    if (a.end != nullptr && seg == 0) {
-      join_parts(S, sm.P[0], id, 3);  // the products are done
-      if (id < 64) store_row(S, a.end + ((size_t)pair * kD + id) * kD);
-    }
+    if (a.end != nullptr && seg == 0) store_row(S, a.end + (size_t)pair * kState + half_row(id));
   } else {
     fence_proxy_async_smem();
     tc::fence_before();
@@ -1125,7 +1071,7 @@ __global__ void __launch_bounds__(512, 1) k_gs_bwd(const __grid_constant__ BwdTi
       const int ph = i & 1, chunk = c1 - 1 - i;
       const Gates& gt = sm.gates[ph];
       const float mine = gt.b[id];
-      if (i > 0 && group != 0 && id == 32) {
+      if (i > 0 && id == 32) {
         bulk_wait_read<0>();  // the last chunk's gradient has left the buffer
         mbar_arrive(&sm.sent);
       }
@@ -1134,7 +1080,7 @@ __global__ void __launch_bounds__(512, 1) k_gs_bwd(const __grid_constant__ BwdTi
         // which holds it for as long as they run.
         if (tid == 128) {
           const uint32_t dq = desc_of(sm.Q), dk = desc_of(sm.K), dv = desc_of(sm.V), dg = desc_of(sm.G),
-                         dd = desc_of(sm.dS[0]);
+                         dd = desc_of(sm.dS[0]), d3 = desc_of(sm.P[1]);
           mbar_wait(&sm.in, ph, a.status, &sm.abort);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) tc::mma(tm + kColSc, desc_at(dq, kk * 32), desc_at(dk, kk * 32), tc::idesc_bf16(128, 128, 0, 0), kk != 0);
@@ -1142,11 +1088,12 @@ __global__ void __launch_bounds__(512, 1) k_gs_bwd(const __grid_constant__ BwdTi
           for (int kk = 0; kk < 4; ++kk) tc::mma(tm + kColDp, desc_at(dg, kk * 32), desc_at(dv, kk * 32), tc::idesc_bf16(128, 128, 0, 0), kk != 0);
           tc::commit(&sm.scores);
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
+          for (int kk = 0; kk < 12; ++kk)
             tc::mma(tm + kColDqi, desc_at(dg, (kk & 3) * 32), pieces_at(sm.S, kk * 2048), tc::idesc_bf16(128, 64, 0, 0), kk != 0);
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            tc::mma(tm + kColDki, desc_at(dv, (kk & 3) * 32), desc_at(dd, (kk >> 2) * kTile + (kk & 3) * 32), tc::idesc_bf16(128, 64, 0, 0), kk != 0);
+          for (int kk = 0; kk < 12; ++kk)
+            tc::mma(tm + kColDki, desc_at(dv, (kk & 3) * 32), kk < 8 ? desc_at(dd, (kk >> 2) * kTile + (kk & 3) * 32) : desc_at(d3, (kk & 3) * 32),
+                    tc::idesc_bf16(128, 64, 0, 0), kk != 0);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) tc::mma(tm + kColDvi, desc_at(dk, kk * 32), desc_at(dd, kk * 2048), tc::idesc_bf16(128, 64, 0, 1), kk != 0);
           tc::commit(&sm.inter);
@@ -1257,13 +1204,18 @@ __global__ void __launch_bounds__(512, 1) k_gs_bwd(const __grid_constant__ BwdTi
         asm volatile("bar.sync 1, 256;" ::: "memory");
         if (tid == 128) {
           tc::fence_after();
-          const uint32_t dp = desc_of(sm.P[0], kLTile), da = desc_of(sm.A[0], kLTile), dak = desc_of(sm.A[0]), dq = desc_of(sm.Q),
+          // The first 64 queries have no part in the gradients of keys 64 .. 127: A's zeros there stand in for P's.
+          const uint32_t dp = desc_of(sm.P[0], kLTile), dp_early = desc_of(sm.P[0], 3 * kLTile), da = desc_of(sm.A[0], kLTile), dak = desc_of(sm.A[0]), dq = desc_of(sm.Q),
                          dk = desc_of(sm.K), dg = desc_of(sm.G);
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
             tc::mma(tm + kColDq, desc_at(dak, (kk >> 2) * kLTile + (kk & 3) * 32), desc_at(dk, kk * 2048), tc::idesc_bf16(128, 64, 0, 1), kk != 0);
-          outer_mma(tm + kColDv, dp, dg);
-          outer_mma(tm + kColDk, da, dq);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            tc::mma(tm + kColDv, desc_at(kk < 4 ? dp_early : dp, kk * 2048), desc_at(dg, kk * 2048), tc::idesc_bf16(128, 64, 1, 1), kk != 0);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            tc::mma(tm + kColDk, desc_at(da, kk * 2048), desc_at(dq, kk * 2048), tc::idesc_bf16(128, 64, 1, 1), kk != 0);
           tc::commit(&sm.grads);
         }
         __syncwarp();
@@ -1278,7 +1230,6 @@ __global__ void __launch_bounds__(512, 1) k_gs_bwd(const __grid_constant__ BwdTi
                                    group == 0 ? a.scale * exp2_fast(mine) : gt.w[id], group == 0 ? sm.Q : sm.K, id);
       if (group == 0) {
         sm.far[id] = dot;
-        if (id == 32) bulk_wait_read<0>();  // the last chunk's dQ has left its buffer
       }
       if (group == 3) sm.past[id] = dot;
       tc::fence_before();
@@ -1455,7 +1406,7 @@ size_t gated_scan_workspace(const ttt_gated_scan_desc* d, bool backward, int num
   const size_t pairs = (size_t)d->batch * d->heads;
   const Plan p = plan_for(d, num_sms);
   const size_t seg = p.nseg > 1 ? 2 * (round256(pairs * p.nseg * kState * 4) + round256(pairs * p.nseg * 4)) : 0;
-  return (backward ? seg : seg / 2) + (backward ? round256(pairs * p.nchunk * 2 * kState * 2) : 0);
+  return (backward ? seg : seg / 2) + (backward ? round256(pairs * p.nchunk * 3 * kState * 2) : 0);
 }
 
 // The tensor map of [batch, heads, tokens, 64] rows in tiles of 128 tokens.
@@ -1505,7 +1456,7 @@ ttt_status gated_scan(const ttt_gated_scan_desc* d, const void* q, const void* k
   a.seg_decay[0] = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + round256((size_t)pairs * p.nseg * kState * 4));
   SegTiles t = {{tk, tk}, {tv, tv}};
   TTT_TRY(raise_smem(k_gs_segment<false>, kSegSmem));
-  k_gs_segment<false><<<grid, 256, kSegSmem, s>>>(t, a);
+  k_gs_segment<false><<<grid, kSegThreads, kSegSmem, s>>>(t, a);
   TTT_CUDA(cudaGetLastError());
   // The last segment may write S_end before others have read S0: then not on their own.
   a.few = p.nseg <= kFewSegments && S_end != S0;
@@ -1530,7 +1481,7 @@ ttt_status gated_scan_backward(const ttt_gated_scan_desc* d, const void* dout, c
   a.stall = op_stall(p.per_seg > 1);
   uint8_t* w = static_cast<uint8_t*>(ws);
   a.ckpt = reinterpret_cast<__nv_bfloat16*>(w);
-  w += round256((size_t)pairs * p.nchunk * 2 * kState * 2);
+  w += round256((size_t)pairs * p.nchunk * 3 * kState * 2);
   const size_t local_bytes = round256((size_t)pairs * p.nseg * kState * 4), decay_bytes = round256((size_t)pairs * p.nseg * 4);
   for (int i = 0; i < 2; ++i) {
     a.local[i] = reinterpret_cast<float*>(w + i * (local_bytes + decay_bytes));
@@ -1553,7 +1504,7 @@ ttt_status gated_scan_backward(const ttt_gated_scan_desc* d, const void* dout, c
   a.start = S0;
   if (p.nseg > 1) {
     // What the segments add in both directions at once.
-    k_gs_segment<false><<<dim3(grid.x, 2), 256, kSegSmem, s>>>(both, a);
+    k_gs_segment<false><<<dim3(grid.x, 2), kSegThreads, kSegSmem, s>>>(both, a);
     TTT_CUDA(cudaGetLastError());
     a.few = p.nseg <= kFewSegments && dS0 != dS_end;
     if (!a.few) {
@@ -1561,9 +1512,9 @@ ttt_status gated_scan_backward(const ttt_gated_scan_desc* d, const void* dout, c
       a.start = a.local[0];
     }
     // The state before every chunk.
-    TTT_TRY(launch_after(k_gs_segment<true>, grid, 256, kSegSmem, s, both, a));
+    TTT_TRY(launch_after(k_gs_segment<true>, grid, kSegThreads, kSegSmem, s, both, a));
   } else {
-    k_gs_segment<true><<<grid, 256, kSegSmem, s>>>(both, a);
+    k_gs_segment<true><<<grid, kSegThreads, kSegSmem, s>>>(both, a);
     TTT_CUDA(cudaGetLastError());
   }
   a.start = p.nseg > 1 && !a.few ? a.local[1] : dS_end;

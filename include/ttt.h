@@ -539,8 +539,8 @@ typedef struct {
  * fp32) forgets everything before its token: documents laid end to end start with such a gate.
  * Writes o (device bf16) and, where not NULL, S_end (device fp32 like S0: the state after the last
  * token; may be S0 itself). tokens = 0 writes S_end = S0 (or 0) and nothing else. States and sums
- * are fp32; one factor of each product is rounded to bf16, but those that make S_end keep 16 bits
- * or more. Padding must hold finite numbers, since 0 · NaN is NaN: a NaN or an infinity may reach
+ * are fp32; one factor of each product that makes an output is rounded to bf16, those that make S_end
+ * keep their fp32 value. Padding must hold finite numbers, since 0 · NaN is NaN: a NaN or an infinity may reach
  * the outputs (and gradients) of all 128 tokens of its chunk, and through the state those after it,
  * past a gate of −inf too. `status` (device int32 or NULL): as for ttt_target_values_noalloc. Errors: INVALID_ARG,
  * UNSUPPORTED (batch·heads above 2^24, tokens above 2^30, row strides from 2^39 on or, for tokens, 0),
@@ -555,7 +555,7 @@ size_t ttt_gated_scan_workspace(const ttt_gated_scan_desc* desc);
  * [batch, heads, tokens, 64]), dg (device, dense fp32 [batch, heads, tokens]; 0 where the gate's
  * factor is 0 in fp32) and, where not NULL, dS0 (fp32 like S0; may be dS_end itself). The gradients of an input with a
  * stride of 0 are those of its separate rows: the caller adds them up. The states before every
- * chunk of 128 tokens are made again, in the workspace (128 bytes per token, sequence and head). */
+ * chunk of 128 tokens are made again, in the workspace (192 bytes per token, sequence and head). */
 ttt_status ttt_gated_scan_backward(const ttt_gated_scan_desc* desc, const void* d_o, const void* q, const void* k,
                                    const void* v, const float* g, const float* S0, const float* dS_end, void* dq,
                                    void* dk, void* dv, float* dg, float* dS0, void* workspace,
