@@ -688,8 +688,8 @@ int pairs_of(int num_sms) { return std::max(1, num_sms / 2); }
 // much as the first (f above 9472 on 148 SMs): 17 x 2560 x 9728: 20.5 us against 31, 128 tokens: 27 against 31,
 // 192: 35 against 33; 17 x 8192 x 28672: 148 against 278. In one round the pairs are as fast or faster (17 x 2048
 // x 7168: 17.3 against 17.6, 128 tokens: 18.7 against 22.8). Against k_ffn_few it needs more than 8 tokens and
-// long rows: 16 x 4096 x 14336: 41 us against 52, 16 x 512 x 28672: 17.5 against 15.4; 8 x 4096 x 14336: 41
-// against 39.5.
+// long rows: 16 x 4096 x 14336: 41 us against 52, 16 x 512 x 28672: 16.8 against 15.2; with 8 tokens 2560 x 9728:
+// 20.0 against 18.1, 2048 x 16384: 24.6 against 23.0, 4096 x 14336: 40.4 against 41.4, 8192 x 28672: 144 against 147.
 bool takes_rows(int64_t T, int d, int f, int num_sms) {
   return f > FM * pairs_of(num_sms) && T <= 160 && T > (d >= 1024 ? 8 : 16);
 }

@@ -30,15 +30,16 @@
 // segments: the states that the segments add are found first (k_gs_segment), combined in order, and
 // then every segment runs from its own start.
 //
-// What bounds it (B200, 8 x 12 heads x 2048 tokens and 4 x 16 x 8192). Latency: no unit is near its limit (the
-// tensor pipe 17 %, HBM 32 %, instruction issue 28 % of the time). Forward: a chunk's chain of scores, their weights,
-// P·V and outputs takes 6300 cycles in a CTA alone on its SM and 9500 in each of two, whose TMEM leaves no room for
-// a third; the pass over K and V for the segments' starts and the launches' first and last microseconds come
-// on top (45 us, where the bytes need 16). Backward: one CTA an SM, whose chunk (12 400 cycles alone, 14 400
-// with all SMs at work) passes through one set of tiles in shared memory: the next chunk's come when its last
-// product has read them. 215 us of 318, where the bytes need 74; the state passes take the rest. The state before
-// every chunk is kept in pieces of eight columns, all rows of a piece after each other: a warp then writes whole
-// sectors, where rows of 128 bytes took 15 us more.
+// What bounds it (B200): latency, no unit is near its limit (of the time, tensor pipe 17 to 29 %, HBM 26 to 50 %,
+// the counters' fullest SM unit 30 to 47 %). Forward: a chunk's chain of scores, their weights, P·V and outputs
+// beside that of the state; seven chunks take 26.8 us in a CTA alone on the GPU, 29.0 in one on every SM and
+// 41.0 in two, whose TMEM leaves no room for a third. The pass over K and V for the segments' starts and the launches'
+// first and last microseconds come on top (8 x 12 heads x 2048 tokens: 18 + 33 us, which overlap to 45, where
+// the bytes need 16). Backward: one CTA an SM, whose chunk passes through one set of tiles in shared memory (49 us
+// for seven in a CTA alone, 58 in one on every SM); the next chunk's tiles come when its last product has read
+// these. 4 x 16 heads x 8192 tokens: 64 us for what the segments add, 49 for the state before every chunk, 207 to 217
+// for the rest, where the bytes need 74. The state before every chunk is kept in pieces of eight columns, all rows of
+// a piece after each other: a warp then writes whole sectors, where rows of 128 bytes took 15 us more.
 #include <algorithm>
 
 #include "f32x2.cuh"
@@ -912,9 +913,9 @@ __device__ __forceinline__ uint64_t pieces_at(const void* tile, int bytes) {
 //   group 1  the same for keys 64 .. 127; dV
 //   group 2  weighs Q (half of each row); carries dS, half a row a thread; dg
 //   group 3  weighs Q (the other half); dK
-// All products of a chunk read its tiles from shared memory, and thread-issued copies of 650 KB pass through it too
-// (3700 of a chunk's cycles by the counted wavefronts of both). The next chunk's tiles are asked for when the last
-// product has read these, and come while the gradients are rounded and sent out. grid: pairs · nseg.
+// A chunk takes 12 000 cycles, of which the threads' own accesses hold shared memory for 3900 (counted) and the
+// products and copies for a part that no counter shows. The next chunk's tiles are asked for when the last product
+// has read these, and come while the gradients are rounded and sent out. grid: pairs · nseg.
 __global__ void __launch_bounds__(512, 1) k_gs_bwd(const __grid_constant__ BwdTiles tm_, const GsArgs a) {
   extern __shared__ uint8_t smem_raw[];
   BwdSmem& sm = *reinterpret_cast<BwdSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -1326,7 +1327,12 @@ __global__ void __launch_bounds__(128) k_gs_step(const StepArgs a, float* __rest
 // ---- host ----------------------------------------------------------------------------------
 
 // Segments of a sequence: as many as fill the GPU (`slots` CTAs at once) when there are fewer
-// (sequence, head) pairs than that, each of at least four chunks.
+// (sequence, head) pairs than that, each of at least four chunks. A whole round of CTAs more costs nearly what a
+// full one does, and this rule does not look at it: 148, 149 and 296 pairs of 8192 tokens take 219, 254 and 319
+// us, 297 take 464; backward, whose main kernel holds one CTA an SM, 638, 848, 1043 and 1330. The same sequences
+// cut otherwise (before the states had three terms): 96 pairs of 2048 tokens 44.8, 47.6, 41.0 (taken) and 52.8 us
+// with one to four segments; 4 pairs of 65511 76, 60 and 58 with 37, 64 and 74 (taken); backward 64 pairs of 8192
+// 300, 342, 304 (taken), 339 and 335 with 2, 3, 4, 5 and 8.
 int segments(int64_t pairs, int nchunk, int slots) {
   if (pairs >= slots) return 1;
   const int most = std::max(1, nchunk / 4);
