@@ -149,8 +149,9 @@ __device__ __forceinline__ void fetch_gates(const GsArgs& a, const float* gp, in
   wm::cp_commit();
 }
 
-// From the raw gates of the last fetch_gates of this warp, or of the one before (another). Sum: float makes no lo, for decays from or to the
-// chunk's ends alone (64 bits cost k_gs_segment 1 us of 16).
+// From the raw gates of the last fetch_gates of this warp, or of the one before (another). Sum: float makes no
+// lo, for decays from or to the chunk's ends alone (double cost k_gs_segment 3 us of 18; for k_gs_out, sums as pairs
+// of fp32 numbers cost 1 us more than double).
 template <class Sum>
 __device__ __forceinline__ void make_gates(const float* raw, Gates& s, int lane, bool another = false) {
   if (another)
