@@ -381,7 +381,7 @@ struct __align__(1024) SegSmem {
   uint8_t L[2][kLTile];  // the second and third terms
   Gates gates[4];
   __align__(16) float raw[2][kL];
-  uint64_t full[2], done[2], gated[4], read[4];
+  uint64_t full[2], ready[2], done[2], gated[4], read[4];
   uint32_t tmem;
   int abort;
 };
@@ -423,6 +423,7 @@ __global__ void __launch_bounds__(kSegThreads, 2) k_gs_segment(const __grid_cons
   if (tid == 256) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.full[i], 1);
+      mbar_init(&sm.ready[i], 8);  // the weighing warps
       mbar_init(&sm.done[i], 1);
     }
     for (int i = 0; i < 4; ++i) {
@@ -449,7 +450,9 @@ __global__ void __launch_bounds__(kSegThreads, 2) k_gs_segment(const __grid_cons
         if (lane == 0 && i + 1 < n) load(i + 1);  // the tiles of the chunk before have been read
         __syncwarp();
       }
-      asm volatile("bar.sync 1, 288;" ::: "memory");  // the chunk is weighed, and the sums two chunks back have been taken
+      // The chunk is weighed, and the sums two chunks back have been taken. (An mbarrier, whose waits end: at a named
+      // barrier, warps that a wait run out has let go ahead would arrive out of turn, and this one wait for good.)
+      mbar_wait(&sm.ready[ph], (i >> 1) & 1, a.status, &sm.abort);
       if (lane == 0) {
         tc::fence_after();
         const uint32_t d = tm + 64 * ph, y = dy + ph * (kLTile >> 4);
@@ -493,7 +496,8 @@ __global__ void __launch_bounds__(kSegThreads, 2) k_gs_segment(const __grid_cons
       }
       fence_proxy_async_smem();
       tc::fence_before();
-      asm volatile("bar.arrive 1, 288;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.ready[ph]);
     };
     if (warp < 4) {
       for (int i = 0; i < n; ++i) weigh_chunk(i);
@@ -514,6 +518,7 @@ __global__ void __launch_bounds__(kSegThreads, 2) k_gs_segment(const __grid_cons
           mbar_wait(&sm.done[last], ((i - 1) >> 1) & 1, a.status, &sm.abort);
           tc::fence_after();
           const float total = sm.gates[(i - 1) & 3].total;
+          __syncwarp();
           if (lane == 0) mbar_arrive(&sm.read[(i - 1) & 3]);
           take_sums(S, tmem + 64 * last, exp2_fast(total));
           decay += total;
