@@ -10,10 +10,10 @@ device, and strides. Rows of the last dimension are dense and start on 16-byte b
 dimensions may lie in any order, so that views of a projection's output are taken as they are. An input
 may repeat rows along a dimension (stride 0, as expand() makes), an output may not; tokens of a gated
 scan have rows of their own. A tensor that fails raises ValueError and nothing is launched; what the
-library refuses (alignment, strides, sizes out of its range) raises TTTError. Outputs and workspaces that a call makes are allocated on the stream it
-runs on. Every call can be captured into a CUDA graph. A call whose bounded device-side waits ran out
-leaves its outputs incomplete: it says so in ``status`` where that is given, and otherwise through
-:func:`poll_operators`.
+library refuses (alignment, strides, sizes out of its range) raises TTTError. Outputs and workspaces
+that a call makes are allocated on the stream it runs on. Every call can be captured into a CUDA graph.
+A call whose bounded device-side waits ran out leaves its outputs incomplete: it says so in ``status``
+where that is given, and otherwise through :func:`poll_operators`.
 """
 
 from __future__ import annotations
@@ -26,8 +26,8 @@ import torch
 from . import abi
 from .abi import check
 
-__all__ = ["poll_operators", "qk_norm_rope", "qk_norm_rope_backward", "rope_frequencies", "gated_scan", "gated_scan_backward",
-           "gated_scan_step", "gated_ffn", "gated_ffn_backward"]
+__all__ = ["qk_norm_rope", "qk_norm_rope_backward", "rope_frequencies", "gated_scan", "gated_scan_backward",
+           "gated_scan_step", "gated_ffn", "gated_ffn_backward", "poll_operators"]
 
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
@@ -306,11 +306,9 @@ def gated_scan(q, k, v, g, *, scale=1.0, initial=None, out=None, final=None, sta
     """ttt_gated_scan: S_t = e^{g_t}·S_{t-1} + k_tᵀ·v_t, o_t = scale·q_t·S_t per (sequence, head). ``q``,
     ``k``, ``v`` bf16 [batch, heads, tokens, 64] (rows as the module says; at least one sequence and head, tokens
     may be 0), ``g`` fp32 [batch, heads, tokens] (any strides; natural logarithms, -inf forgets everything
-    before its token). All tokens
-    must hold finite numbers, padding too (0 · NaN is NaN). Returns
-    (o, state): o in ``out`` or a new dense tensor; the state after the last token, fp32 [batch,
-    heads, 64, 64], in ``final`` (which may be ``initial``) or a new tensor. ``status`` as for
-    :func:`gated_ffn`."""
+    before its token). All tokens must hold finite numbers, padding too (0 · NaN is NaN). Returns (o, state): o
+    in ``out`` or a new dense tensor; the state after the last token, fp32 [batch, heads, 64, 64], in ``final``
+    (which may be ``initial``) or a new tensor. ``status`` as for :func:`gated_ffn`."""
     dev = _current_device()
     raw, ctx = _place(stream, dev)
     scale = float(scale)  # a plain number: the key must not hold a tensor, whose value may change
